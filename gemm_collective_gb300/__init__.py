@@ -37,6 +37,7 @@ FCC_BF16, FCC_F16, FCC_F32 = 0, 1, 2
 FCC_OP_GEMM_RS, FCC_OP_GEMM_AR, FCC_OP_GEMV_AR, FCC_OP_AG_GEMM, FCC_OP_EMBEDDING_A2A = range(5)
 FCC_MAX_RANKS = 8
 FCC_MAX_EXPERTS = 64
+FCC_MAX_TEACHER = 256
 
 
 class fcc_opts(ctypes.Structure):
@@ -108,6 +109,19 @@ _itime = _sig("fcc_interdecom_time", ctypes.c_double, [ctypes.c_double, ctypes.c
 _choose = _sig("fcc_choose_algo", _I, [_I, _I, _I64, _I64, _I64, _I, _I])
 _attn = _sig("fcc_ring_attention", _I,
              [_I, _P, _P, _P, _P, _I64, _I, _I64, _I, _I, _I, _OPTS, _P])
+_F = ctypes.c_float
+_xent = _sig("fcc_linear_xent", _I,
+             [_I, _P, _P, _P, _I64, _I64, _I64, _P, _P, ctypes.c_int32, _F, _F, _F, _I, _OPTS, _P])
+_xent_grad = _sig("fcc_linear_xent_grad", _I,
+                  [_I, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _P, ctypes.c_int32, _F, _F, _F,
+                   _I, _I, _OPTS, _P])
+_distill = _sig("fcc_linear_distill", _I,
+                [_I, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _F, _F, _I, _OPTS, _P])
+_distill_grad = _sig("fcc_linear_distill_grad", _I,
+                     [_I, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _F, _F, _I, _I,
+                      _OPTS, _P])
+_loss_ws = _sig("fcc_linear_loss_workspace_size", ctypes.c_size_t,
+                [_I, _I64, _I64, _I64, _I, _I, _OPTS])
 _launches = _sig("fcc_launch_count", ctypes.c_uint64, [])
 _version = _sig("fcc_version", ctypes.c_char_p, [])
 _wait_timeout = _sig("fcc_test_wait_timeout", _I, [_I64, _P])
@@ -228,6 +242,45 @@ def fcc_ring_attention(R, Q, K, V, O, S, H, d, causal=False, in_dtype=FCC_BF16,
                        out_dtype=FCC_BF16, opts=None, stream=None):
     _check(_attn(R, _ptrs(Q), _ptrs(K), _ptrs(V), _ptrs(O), S, H, d, 1 if causal else 0,
                  in_dtype, out_dtype, _opts(opts), _stream(stream)), "fcc_ring_attention")
+
+
+def fcc_linear_xent(R, X, W, labels, T, V, D, loss, lse, ignore_index=-100, smoothing=0.0,
+                    z_weight=0.0, softcap=0.0, in_dtype=FCC_BF16, opts=None, stream=None):
+    """Cross entropy of a head split by vocabulary over R ranks; labels: [T] int32 on the device."""
+    _check(_xent(R, _ptrs(X), _ptrs(W), _addr(labels), T, V, D, _ptrs(loss), _ptrs(lse),
+                 ignore_index, smoothing, z_weight, softcap, in_dtype, _opts(opts),
+                 _stream(stream)), "fcc_linear_xent")
+
+
+def fcc_linear_xent_grad(R, X, W, labels, lse, dloss, T, V, D, dX, dW, ignore_index=-100,
+                         smoothing=0.0, z_weight=0.0, softcap=0.0, in_dtype=FCC_BF16,
+                         out_dtype=FCC_BF16, opts=None, stream=None):
+    """Its gradient with respect to X and W (dX or dW None: not wanted); lse from the forward."""
+    _check(_xent_grad(R, _ptrs(X), _ptrs(W), _addr(labels), _ptrs(lse), _addr(dloss), T, V, D,
+                      _ptrs(dX), _ptrs(dW), ignore_index, smoothing, z_weight, softcap, in_dtype,
+                      out_dtype, _opts(opts), _stream(stream)), "fcc_linear_xent_grad")
+
+
+def fcc_linear_distill(R, X, W, teacher_idx, teacher_logits, T, V, D, topk, loss, lse,
+                       temperature=1.0, softcap=0.0, in_dtype=FCC_BF16, opts=None, stream=None):
+    """Distillation from a teacher's top logits ([T, topk] int32 and f32 on the device)."""
+    _check(_distill(R, _ptrs(X), _ptrs(W), _addr(teacher_idx), _addr(teacher_logits), T, V, D,
+                    topk, _ptrs(loss), _ptrs(lse), temperature, softcap, in_dtype, _opts(opts),
+                    _stream(stream)), "fcc_linear_distill")
+
+
+def fcc_linear_distill_grad(R, X, W, teacher_idx, teacher_logits, lse, dloss, T, V, D, topk, dX,
+                            dW, temperature=1.0, softcap=0.0, in_dtype=FCC_BF16,
+                            out_dtype=FCC_BF16, opts=None, stream=None):
+    """Its gradient with respect to X and W (dX or dW None: not wanted); lse from the forward."""
+    _check(_distill_grad(R, _ptrs(X), _ptrs(W), _addr(teacher_idx), _addr(teacher_logits),
+                         _ptrs(lse), _addr(dloss), T, V, D, topk, _ptrs(dX), _ptrs(dW),
+                         temperature, softcap, in_dtype, out_dtype, _opts(opts),
+                         _stream(stream)), "fcc_linear_distill_grad")
+
+
+def fcc_linear_loss_workspace_size(R, T, V, D, topk=0, grad=False, opts=None) -> int:
+    return int(_loss_ws(R, T, V, D, topk, 1 if grad else 0, _opts(opts)))
 
 
 def fcc_choose_algo(op, R, M, N, K, sms=0, max_ctas=0) -> int:

@@ -39,8 +39,8 @@
  *  - Environment defaults, read once when the library first needs one:
  *    FCC_ALGO=fused|unfused|interdecom|ce replaces FCC_ALGO_AUTO (also in
  *    fcc_choose_algo) for the operators with several forms (a form an
- *    operator lacks gives FCC_ERR_UNSUPPORTED; the attention and the MoE
- *    combine have one form and ignore it); FCC_DETERMINISTIC=0|1 is the
+ *    operator lacks gives FCC_ERR_UNSUPPORTED; the attention, the MoE
+ *    combine and the losses have one form and ignore it); FCC_DETERMINISTIC=0|1 is the
  *    summation mode of calls with opts == NULL; FCC_CHUNKS=n (1..64) the
  *    InterDecom chunk count where opts->chunks is 0; FCC_TIMEOUT_MS=n the
  *    device wait limit where opts->timeout_ns is 0.  Unset or unparsable
@@ -62,6 +62,7 @@ typedef struct CUstream_st *fcc_stream_t;
 #define FCC_MAX_RANKS 8
 #define FCC_MAX_EXPERTS 64
 #define FCC_MAX_TABLES 256  /* embedding tables per call */
+#define FCC_MAX_TEACHER 256 /* teacher entries per token (distillation) */
 
 typedef enum { FCC_BF16 = 0, FCC_F16 = 1, FCC_F32 = 2 } fcc_dtype;
 
@@ -336,6 +337,86 @@ fcc_status fcc_ring_attention(int R, const void *const *Q, const void *const *K,
                               const void *const *V, void *const *O, int64_t S, int H, int64_t d,
                               int causal, fcc_dtype in, fcc_dtype out_dtype,
                               const fcc_opts *opts, fcc_stream_t stream);
+
+/*
+ * Linear cross entropy: the loss of a vocabulary-parallel head, forward.  The
+ * head's rows are split over the ranks (rank r holds rows [r*V/R, (r+1)*V/R)),
+ * every rank holds a copy of the tokens' hidden states, and the softmax
+ * statistics are all-reduced:
+ *   x_v = X[r][t] . W[r][v - r*V/R]   (f32)
+ *   l_v = x_v, or softcap * tanh(x_v / softcap) when softcap > 0
+ *   lse[t]  = log sum_v exp(l_v)
+ *   loss[t] = lse - (1 - smoothing) l_y - smoothing / V * sum_v l_v
+ *             + z_weight * lse^2,                     y = labels[t]
+ * written to every rank's loss[r], lse[r].  A label equal to ignore_index
+ * gives loss 0 (lse is still its row's).  Any other label outside [0, V) does
+ * the same and records FCC_ERR_INVALID in the status word.  The logits are
+ * never stored.
+ * X[r]: [T,D] bf16 (the same values in every rank; entries may be one
+ * buffer); W[r]: [V/R,D] bf16; labels: [T] int32 (device); loss[r], lse[r]:
+ * [T] f32.  T, V >= 1 (any, odd ones too), V % R == 0, D % 8 == 0,
+ * 0 <= smoothing < 1, z_weight >= 0.  Logits that are not finite give a loss
+ * that is not.  Repeatable (a fixed order of summation).  Uses workspace
+ * (fcc_linear_loss_workspace_size with topk 0, grad 0).  opts->algo: AUTO or
+ * FUSED; the environment's FCC_ALGO and FCC_CHUNKS do not apply.
+ */
+fcc_status fcc_linear_xent(int R, const void *const *X, const void *const *W,
+                           const int32_t *labels, int64_t T, int64_t V, int64_t D,
+                           float *const *loss, float *const *lse, int32_t ignore_index,
+                           float smoothing, float z_weight, float softcap, fcc_dtype in,
+                           const fcc_opts *opts, fcc_stream_t stream);
+
+/*
+ * Its gradient, from the forward pass's lse and the losses' upstream
+ * gradients dloss ([T] f32, device; a mean over n tokens passes 1/n):
+ *   dl_v = dloss ((1 + 2 z_weight lse) exp(l_v - lse) - smoothing / V
+ *                 - (1 - smoothing) [v = y])
+ *   dx_v = dl_v, times 1 - (l_v / softcap)^2 when softcap > 0
+ *   dX[r]  = sum over all ranks s of dx_s @ W[s]   ([T,D] bf16, to every rank)
+ *   dW[r]  = dx_r^T @ X[r]                         ([V/R,D] bf16)
+ * Ignored rows have no gradient, whatever their dloss holds.  dX or dW may be
+ * NULL (not wanted).  The logits are computed again, a piece of every rank's
+ * vocabulary at a time (opts->chunks pieces; 0 = as few as hold 512 MiB of
+ * dx), and rounded to bf16 as dx; products accumulate in f32.  out_dtype is
+ * FCC_BF16 (an f32 result of bf16 dx would promise digits it does not have).
+ * Uses workspace (fcc_linear_loss_workspace_size with topk 0, grad 1).
+ */
+fcc_status fcc_linear_xent_grad(int R, const void *const *X, const void *const *W,
+                                const int32_t *labels, const float *const *lse,
+                                const float *dloss, int64_t T, int64_t V, int64_t D,
+                                void *const *dX, void *const *dW, int32_t ignore_index,
+                                float smoothing, float z_weight, float softcap, fcc_dtype in,
+                                fcc_dtype out_dtype, const fcc_opts *opts, fcc_stream_t stream);
+
+/*
+ * Distillation from a teacher's top logits on the same head:
+ *   q       = softmax of teacher_logits[t][k] / temperature over the row's entries
+ *   lse[t]  = log sum_v exp(l_v / temperature)       (l as above)
+ *   loss[t] = temperature^2 (sum_k q_k (log q_k - l_{i_k} / temperature) + lse)
+ * with i_k = teacher_idx[t][k]; an index < 0, or a logit of -inf, is no
+ * entry, and a row without entries gives loss 0.  An index >= V is no entry
+ * either and records FCC_ERR_INVALID.  An index given twice counts twice.
+ * The gradient is dl_v = dloss temperature (exp(l_v / temperature - lse)
+ * - sum_k q_k [v = i_k]).  teacher_idx, teacher_logits: [T,topk] int32 / f32
+ * (device), 1 <= topk <= FCC_MAX_TEACHER, in any order; temperature > 0.  All
+ * else as in fcc_linear_xent and fcc_linear_xent_grad.
+ */
+fcc_status fcc_linear_distill(int R, const void *const *X, const void *const *W,
+                              const int32_t *teacher_idx, const float *teacher_logits, int64_t T,
+                              int64_t V, int64_t D, int topk, float *const *loss,
+                              float *const *lse, float temperature, float softcap, fcc_dtype in,
+                              const fcc_opts *opts, fcc_stream_t stream);
+fcc_status fcc_linear_distill_grad(int R, const void *const *X, const void *const *W,
+                                   const int32_t *teacher_idx, const float *teacher_logits,
+                                   const float *const *lse, const float *dloss, int64_t T,
+                                   int64_t V, int64_t D, int topk, void *const *dX,
+                                   void *const *dW, float temperature, float softcap,
+                                   fcc_dtype in, fcc_dtype out_dtype, const fcc_opts *opts,
+                                   fcc_stream_t stream);
+
+/* Scratch bytes of the four calls above (topk 0: cross entropy). */
+size_t fcc_linear_loss_workspace_size(int R, int64_t T, int64_t V, int64_t D, int topk, int grad,
+                                      const fcc_opts *opts);
 
 /* Scratch bytes a call needs (for opts->workspace); 0 if none. */
 size_t fcc_workspace_size(fcc_op op, int R, int64_t M, int64_t N, int64_t K,
