@@ -61,36 +61,86 @@ enum LossKind : int {
 constexpr bool a_mn(int kind) { return kind == LK_DW; }
 constexpr bool b_mn(int kind) { return kind == LK_DX || kind == LK_DW; }
 
+constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
+// Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
+constexpr int threads_of(int kind) { return 64 + 32 * kEpiWarps + (kind == LK_FWD ? 64 : 0); }
+constexpr uint32_t kOutBytes = 32 * 128;  // a warp's staging: 32 rows x 64 bf16, 128-byte swizzle
+// bf16 results leave by TMA stores from shared memory.
+constexpr bool stages_out(int kind) { return kind == LK_DL || kind == LK_DW; }
+
 template <int KIND, int CG>
 struct Cfg {
   static constexpr int kTileM = kBM * CG;
   static constexpr int kBNcta = kBN / CG;                  // B columns this CTA holds
-  static constexpr int kStages = CG == 2 ? 7 : 4;
+  static constexpr int kStages = (CG == 2 ? 7 : 4) - (stages_out(KIND) && CG == 2 ? 1 : 0);
   static constexpr uint32_t kBBytes = kBK * kBNcta * 2;    // 32 or 16 KiB
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
-  static constexpr uint32_t kIdesc = ptx::idesc_bf16_f32(kTileM, kBN, a_mn(KIND), b_mn(KIND));
-  static constexpr int kSmem =
-      1024 + kStages * static_cast<int>(kStageBytes) + (2 * kStages + 5) * 8 + 16;
+  static constexpr uint32_t kOut = stages_out(KIND) ? kEpiWarps * kOutBytes : 0;
+  // Instruction descriptor of a tile `width` columns wide.
+  __device__ static constexpr uint32_t idesc(int width) {
+    return ptx::idesc_bf16_f32(kTileM, width, a_mn(KIND), b_mn(KIND));
+  }
+  static constexpr int kSmem = 1024 + kStages * static_cast<int>(kStageBytes) +
+                               static_cast<int>(kOut) + (2 * kStages + 5) * 8 + 16 +
+                               (KIND == LK_FWD ? 128 * 12 : 0);
   static_assert(kSmem <= 232448, "shared memory per CTA");
+};
+
+// How the dX tiles that would make up a last, partly filled round (all tiles,
+// when they are fewer than the CTAs) are shared: `tiles` tiles of k steps over
+// `ctas` CTAs (pairs).  Each of `groups` CTAs per tile takes `len` steps of
+// it, so that the CTAs of a group walk the same rows of dl and W side by side
+// (equal shares of the tiles' steps laid end to end start everywhere in k and
+// read dl and W from memory once per tile: 321 us against %DX% for 1999 tokens
+// x 50257 x 2048); the helpers, the CTAs left over, share the tiles' remaining
+// tails, laid end to end.  A tile's parts are summed at the end in a fixed
+// order.
+struct Shares {
+  int tiles, ctas, k;
+  int groups, len, tail, helpers;  // tail = k - groups * len
+  int max_parts;
+  __host__ __device__ __forceinline__ long long tails() const {
+    return static_cast<long long>(tiles) * tail;
+  }
+  // The helper that holds step x of the tails: helper h has steps
+  // [h tails / helpers, (h + 1) tails / helpers).
+  __host__ __device__ __forceinline__ int helper_of(long long x) const {
+    return static_cast<int>(((x + 1) * helpers - 1) / tails());
+  }
+  // Parts of shared tile i.
+  __host__ __device__ __forceinline__ int parts(int i) const {
+    if (tail <= 0) return groups;
+    const long long x = static_cast<long long>(i) * tail;
+    return groups + helper_of(x + tail - 1) - helper_of(x) + 1;
+  }
 };
 
 struct LossParams {
   CUtensorMap mapA[FCC_MAX_RANKS];
   CUtensorMap mapB[FCC_MAX_RANKS];
+  CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl piece, DW: dW; box 32 rows x 64
   int R, T, D;
   int Vs;                  // vocabulary rows per rank
   int v0, vn;              // this piece: rows [v0, v0 + vn) of every rank (FWD: 0, Vs)
+  int width;               // tile columns (FWD, DL; a multiple of 16), else kBN
   int tiles_m, tiles_n;    // tiles of one rank (DX: of all)
+  int full_tiles;          // tiles run whole, round-robin (DX: the others are shared, see Work)
   int num_tiles;
   int k_iters;             // 64-deep K steps of a whole tile
   int kb_per_rank;         // DX: K steps per rank
-  int splits;              // DX: parts of the K loop, each with its own f32 slab
+  Shares shares;           // DX: the tiles past full_tiles, by the first piece's K steps
+  int a_rows;              // rows of an A box (K-major A: fewer than 128 when T is)
+  int k_rows;              // DW: tokens of a K step (fewer than 64 when T is)
   int group_m;             // raster group height (tiles)
   // tokens' targets: labels (cross entropy), or per token K sorted vocabulary
   // indices (INT_MAX past the last) and their teacher probabilities
   const int32_t* labels;
   const int32_t* hit_idx;  // [T, K]
   const float* hit_q;      // [T, K]
+  // [T][start_ld]: the first of them at or past a logit tile, by (rank, piece, tile)
+  const uint16_t* hit_start;
+  long long start_ld;
+  int npieces, piece, piece_tiles;
   int K;
   int ignore_index;
   float cap, inv_cap;      // soft cap, 0 = none
@@ -100,17 +150,17 @@ struct LossParams {
   float2* part;            // [R * tiles_n][T]: base-2 maximum and sum
   float* part_sum;         // the same layout: sum of the logits (smoothing), or NULL
   float* pick;             // [T, K] logits at the targets
+  const void* X[FCC_MAX_RANKS];   // the matrices themselves and the labels' logits
+  const void* Wr[FCC_MAX_RANKS];  // (uncapped) computed from them
+  float* own_logit;        // [T]
   // DL
   const float* lse[FCC_MAX_RANKS];
   const float* dloss;
-  // dl: [R][T][ldl] bf16 (DL writes it, the tensor maps of DX and DW read it)
-  uint16_t* dl;
-  long long ldl;
-  // DX: f32 slabs [splits][T][D]; first = 1: overwrite, else add
+  // DX: f32 sums [T][D] of whole tiles and of shared tiles' first parts, and
+  // one [rows][kBN] block for each further part; first = 1: overwrite, else add
   float* acc;
+  float* parts;
   int first;
-  // DW
-  void* out[FCC_MAX_RANKS];  // [Vs, D] bf16
   int* status;
   unsigned long long timeout_ns;
 };
@@ -118,7 +168,8 @@ struct LossParams {
 struct Tile {
   int rank, mt, nt;
   int it_lo, it_hi;  // K steps
-  int split;
+  int part;          // DX: which part of a shared tile (0: goes to acc)
+  int shared;        // DX: index among the shared tiles
 };
 
 __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int group, int& mt,
@@ -136,7 +187,8 @@ template <int KIND>
 __device__ __forceinline__ Tile tile_of(const LossParams& p, int t) {
   Tile tl;
   tl.rank = 0;
-  tl.split = 0;
+  tl.part = 0;
+  tl.shared = 0;
   tl.it_lo = 0;
   tl.it_hi = p.k_iters;
   if constexpr (KIND == LK_FWD || KIND == LK_DL) {
@@ -144,11 +196,7 @@ __device__ __forceinline__ Tile tile_of(const LossParams& p, int t) {
     tl.rank = tl.nt / p.tiles_n;
     tl.nt -= tl.rank * p.tiles_n;
   } else if constexpr (KIND == LK_DX) {
-    const int per = p.tiles_m * p.tiles_n;
-    tl.split = t / per;
-    raster(t - tl.split * per, p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
-    tl.it_lo = static_cast<int>(static_cast<long long>(p.k_iters) * tl.split / p.splits);
-    tl.it_hi = static_cast<int>(static_cast<long long>(p.k_iters) * (tl.split + 1) / p.splits);
+    raster(t, p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
   } else {
     raster(t, p.R * p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
     tl.rank = tl.mt / p.tiles_m;
@@ -157,35 +205,116 @@ __device__ __forceinline__ Tile tile_of(const LossParams& p, int t) {
   return tl;
 }
 
-// A warp's 32 x 32 block (lane i: 32 columns of its row) as bf16 in 16-byte
-// pieces, four lanes to a row: emit(src, k, piece) stores columns 8k .. 8k + 7
-// of lane src's row; every lane calls it.
-template <class Emit>
-__device__ __forceinline__ void store_block_bf16(const uint32_t (&v)[32], int lane, Emit&& emit) {
-  uint4 w[4];
+// What one CTA (pair) works on: whole tiles round-robin, then (dX) its share.
+template <int KIND>
+struct Work {
+  const LossParams& p;
+  int t, npairs, pair;
+  long long cur, end;  // of the tails (a helper); cur = -1: a group's share to do
+  __device__ __forceinline__ Work(const LossParams& p_, int pair_, int npairs_)
+      : p(p_), t(pair_), npairs(npairs_), pair(pair_), cur(0), end(0) {
+    if constexpr (KIND == LK_DX) {
+      const Shares& s = p.shares;
+      const int h = pair - s.groups * s.tiles;
+      if (s.tiles > 0 && h < 0) {
+        cur = -1;
+      } else if (s.tail > 0 && h < s.helpers) {
+        cur = s.tails() * h / s.helpers;
+        end = s.tails() * (h + 1) / s.helpers;
+      }
+    }
+  }
+  __device__ __forceinline__ bool next(Tile& tl) {
+    if (t < p.full_tiles) {
+      tl = tile_of<KIND>(p, t);
+      t += npairs;
+      return true;
+    }
+    if constexpr (KIND == LK_DX) {
+      const Shares& s = p.shares;
+      int i, lo, n, part;
+      if (cur < 0) {
+        const int g = pair / s.tiles;
+        i = pair - g * s.tiles;
+        lo = g * s.len;
+        n = s.len;
+        part = g;
+        cur = 0;
+      } else if (cur < end) {
+        i = static_cast<int>(cur / s.tail);
+        const int x = static_cast<int>(cur - static_cast<long long>(i) * s.tail);
+        n = static_cast<int>(min(static_cast<long long>(s.tail - x), end - cur));
+        lo = s.groups * s.len + x;
+        part = s.groups + pair - s.groups * s.tiles - s.helper_of(static_cast<long long>(i) * s.tail);
+        cur += n;
+      } else {
+        return false;
+      }
+      tl = tile_of<KIND>(p, p.full_tiles + i);
+      tl.shared = i;
+      tl.part = part;
+      // (a shorter last piece has fewer steps than planned, or none)
+      tl.it_lo = min(lo, p.k_iters);
+      tl.it_hi = min(lo + n, p.k_iters);
+      return true;
+    }
+    return false;
+  }
+};
+
+// 32 f32 columns of each lane's row as bf16 into the warp's staging block:
+// half 0 / 1 of its 64 columns (16-byte pieces, 128-byte swizzle).
+__device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
+                                           const uint32_t (&v)[32]) {
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    w[g].x = ptx::pack_bf16x2(__uint_as_float(v[8 * g]), __uint_as_float(v[8 * g + 1]));
-    w[g].y = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
-    w[g].z = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
-    w[g].w = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
+    uint4 w;
+    w.x = ptx::pack_bf16x2(__uint_as_float(v[8 * g]), __uint_as_float(v[8 * g + 1]));
+    w.y = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
+    w.z = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
+    w.w = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
+    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + g) ^ (lane & 7)) << 4)) = w;
   }
-  const int k = lane & 3;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int src = 8 * j + (lane >> 2);
-    uint4 piece = w[0];
-#pragma unroll
-    for (int kk = 0; kk < 4; ++kk) {
-      uint4 x;
-      x.x = __shfl_sync(0xffffffffu, w[kk].x, src);
-      x.y = __shfl_sync(0xffffffffu, w[kk].y, src);
-      x.z = __shfl_sync(0xffffffffu, w[kk].z, src);
-      x.w = __shfl_sync(0xffffffffu, w[kk].w, src);
-      if (kk == k) piece = x;
-    }
-    emit(src, k, piece);
+}
+
+// c tanh(x / c) = c - 2c / (1 + e^{2x/c}), by the approximate exponential and
+// reciprocal: off by about c 2^-22 (an exponential past the range gives +-c).
+__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap) {
+  return fmaf(-2.f * cap, ptx::rcp_approx(1.f + ptx::ex2_approx(x * (2.f * kLog2e * inv_cap))), cap);
+}
+
+// (m, s) of both: base-2 maximum and sum.
+__device__ __forceinline__ void merge(float& m, float& s, float m1, float s1) {
+  const float mn = fmaxf(m, m1);
+  const float off = mn == -INFINITY ? 0.f : mn;
+  // (a sum whose maximum is -inf is 0, or NaN after a NaN logit: kept as it is)
+  s = (m == -INFINITY ? s : s * exp2f(m - off)) + (m1 == -INFINITY ? s1 : s1 * exp2f(m1 - off));
+  m = mn;
+}
+
+// What a logit tile's epilogue thread needs of its token, fetched a tile ahead.
+struct Token {
+  int y;       // the label, or the place of the first target at or past the tile
+  int first;   // DL, teacher: the token's first target (INT_MAX: it has none)
+  float lse, g;
+};
+
+template <int KIND>
+__device__ __forceinline__ Token token_of(const LossParams& p, const Tile& tl, long long row) {
+  Token k{0, INT_MAX, 0.f, 0.f};
+  if (row >= p.T) return k;
+  if (p.labels != nullptr) {
+    k.y = __ldg(p.labels + row);
+  } else {
+    k.y = __ldg(p.hit_start + row * p.start_ld +
+                (tl.rank * p.npieces + p.piece) * p.piece_tiles + tl.nt);
+    if (KIND == LK_DL) k.first = __ldg(p.hit_idx + row * p.K);
   }
+  if (KIND == LK_DL) {
+    k.g = __ldg(p.dloss + row);
+    k.lse = __ldg(p.lse[tl.rank] + row);
+  }
+  return k;
 }
 
 // A token's targets in ascending vocabulary order: `next` is the next one at
@@ -195,34 +324,24 @@ struct Targets {
   int cur, n, next;
 };
 
-__device__ __forceinline__ Targets targets_from(const LossParams& p, bool row_ok, long long row,
+__device__ __forceinline__ Targets targets_from(const LossParams& p, const Token& k, long long row,
                                                 int col0) {
   Targets g{nullptr, 0, 0, INT_MAX};
-  if (!row_ok) return g;
+  if (row >= p.T) return g;
   if (p.labels != nullptr) {
-    const int y = __ldg(p.labels + row);
-    if (y >= col0) g.next = y;  // (an ignored or bad label is dealt with by the caller)
-    g.n = 1;
+    if (k.y >= col0) g.next = k.y;  // (an ignored or bad label is dealt with by the caller)
     return g;
   }
   g.list = p.hit_idx + row * p.K;
   g.n = p.K;
-  int lo = 0, hi = p.K;  // the first entry >= col0
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(g.list + mid) < col0)
-      lo = mid + 1;
-    else
-      hi = mid;
-  }
-  g.cur = lo;
-  if (lo < p.K) g.next = __ldg(g.list + lo);
+  g.cur = k.y;
+  if (g.cur < g.n) g.next = __ldg(g.list + g.cur);
   return g;
 }
 
 __device__ __forceinline__ void targets_advance(Targets& g) {
   ++g.cur;
-  g.next = g.cur < g.n && g.list != nullptr ? __ldg(g.list + g.cur) : INT_MAX;
+  g.next = g.cur < g.n ? __ldg(g.list + g.cur) : INT_MAX;
 }
 
 __device__ __forceinline__ bool label_live(const LossParams& p, int y) {
@@ -230,7 +349,7 @@ __device__ __forceinline__ bool label_live(const LossParams& p, int y) {
 }
 
 template <int KIND, int CG>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(threads_of(KIND), 1)
 loss_gemm_kernel(const __grid_constant__ LossParams p) {
   using C = Cfg<KIND, CG>;
   constexpr int kStages = C::kStages;
@@ -241,13 +360,15 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kStages * kABytes;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kStages * C::kBBytes);
+  uint8_t* sO = sB + kStages * C::kBBytes;  // DL, DW: the epilogue warps' staging blocks
+  uint64_t* full = reinterpret_cast<uint64_t*>(sO + C::kOut);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sStat = reinterpret_cast<float*>(tmem_slot + 4);  // FWD: [128][3]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -262,7 +383,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&tfull[b], 1);
-      ptx::mbar_init(&tempty[b], 4 * CG);  // every epilogue warp of the pair
+      ptx::mbar_init(&tempty[b], kEpiWarps * CG);  // every epilogue warp of the pair
     }
     ptx::mbar_init(mma_done, 1);
     *abort_flag = 0;
@@ -296,26 +417,34 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
   ptx::griddep_launch_dependents();
   const uint32_t tmem_base = *tmem_slot;
   const ptx::Waiter W{abort_flag, p.status, p.timeout_ns};
+  Work<KIND> work(p, pair, npairs);
+  Tile tl;
+  // B columns per CTA: of a logit tile its width's half or whole, else fixed
+  const int bn_cta = (KIND == LK_FWD || KIND == LK_DL) ? p.width / CG : C::kBNcta;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
       uint32_t issued = 0, last_parity = 0;
+      // (rows of A past a short box stay as they are: they only make rows of
+      // the result that nothing reads)
+      const uint32_t stage_bytes =
+          a_mn(KIND) ? static_cast<uint32_t>(kBM + C::kBNcta) * p.k_rows * 2
+                     : static_cast<uint32_t>(p.a_rows) * kBK * 2 + static_cast<uint32_t>(bn_cta) * kBK * 2;
       bool ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
-        const Tile tl = tile_of<KIND>(p, t);
-        const int m0 = tl.mt * TM + static_cast<int>(cta) * kBM;       // this CTA's A rows
-        const int n0 = tl.nt * kBN + static_cast<int>(cta) * C::kBNcta;  // and B columns
+      while (ok && work.next(tl)) {
+        const int m0 = tl.mt * TM + static_cast<int>(cta) * kBM;  // this CTA's A rows
+        const int n0 = tl.nt * (bn_cta * CG) + static_cast<int>(cta) * bn_cta;  // and B columns
+        int r = tl.rank, kb = tl.it_lo;
+        if constexpr (KIND == LK_DX) {
+          r = tl.it_lo / p.kb_per_rank;
+          kb = tl.it_lo - r * p.kb_per_rank;
+        }
         for (int it = tl.it_lo; it < tl.it_hi; ++it) {
-          if (!W.wait(&empty[stage], phase ^ 1u)) {
+          if (!W.wait_suspended(&empty[stage], phase ^ 1u)) {
             ok = false;
             break;
-          }
-          int r = tl.rank, kb = it;
-          if constexpr (KIND == LK_DX) {
-            r = it / p.kb_per_rank;
-            kb = it - r * p.kb_per_rank;
           }
           const CUtensorMap* ma = &p.mapA[r];
           const CUtensorMap* mb = &p.mapB[r];
@@ -324,9 +453,9 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           uint32_t bar = 0;
           if constexpr (kPair) {
             bar = ptx::mapa(ptx::smem_addr(&full[stage]), 0);
-            if (cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+            if (cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
           } else {
-            ptx::mbar_arrive_expect_tx(&full[stage], C::kStageBytes);
+            ptx::mbar_arrive_expect_tx(&full[stage], stage_bytes);
           }
           auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
             if constexpr (kPair)
@@ -354,6 +483,11 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             stage = 0;
             phase ^= 1u;
           }
+          ++kb;
+          if (KIND == LK_DX && kb == p.kb_per_rank) {
+            kb = 0;
+            ++r;
+          }
         }
       }
       if (*abort_flag && cta == 0) {
@@ -369,19 +503,22 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       uint32_t stage = 0, phase = 0;
       uint32_t acc = 0, acc_phase = 0;
       bool any = false, ok = true;
-      for (int t = pair; t < p.num_tiles && ok; t += npairs) {
-        const Tile tl = tile_of<KIND>(p, t);
-        if (!W.wait(&tempty[acc], acc_phase ^ 1u)) break;
+      const uint32_t idesc = C::idesc(bn_cta * CG);
+      while (ok && work.next(tl)) {
+        if (!W.wait_suspended(&tempty[acc], acc_phase ^ 1u)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kBN;
         for (int it = tl.it_lo; it < tl.it_hi; ++it) {
-          if (!W.wait(&full[stage], phase)) {
+          if (!W.wait_suspended(&full[stage], phase)) {
             ok = false;
             break;
           }
           ptx::tc_fence_after();
           const uint32_t a_addr = ptx::smem_addr(sA + stage * kABytes);
           const uint32_t b_addr = ptx::smem_addr(sB + stage * C::kBBytes);
+          // (DW: no MMA for 16 rows past the last token, which a short box
+          // does not fill)
+          const int steps = KIND == LK_DW ? min(kBK, p.T - it * kBK) : kBK;
 #pragma unroll
           for (int kk = 0; kk < kBK / 16; ++kk) {
             // K-major: 16 elements (32 B) on inside the swizzled row;
@@ -393,10 +530,11 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
                                     ? ptx::smem_desc_sw128(b_addr + kk * 2048, kBoxBytes, 1024)
                                     : ptx::smem_desc_sw128(b_addr + kk * 32, 16, 1024);
             const uint32_t accum = (it > tl.it_lo || kk > 0) ? 1u : 0u;
+            if (KIND == LK_DW && 16 * kk >= steps) continue;
             if constexpr (kPair)
-              ptx::mma_f16_pair(d_tmem, ad, bd, C::kIdesc, accum);
+              ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
             else
-              ptx::mma_f16(d_tmem, ad, bd, C::kIdesc, accum);
+              ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
           }
           if constexpr (kPair)
             ptx::mma_commit_pair_arrive_ctas(&empty[stage], 0x3);
@@ -424,86 +562,101 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         W.drain(mma_done, 0, kDrainNs);
       }
     }
-  } else {
+  } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------- epilogue
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
+    const int q = warp & 3;            // TMEM lane quarter this warp may access
+    const int half = (warp - 2) >> 2;  // it takes every other 64 columns, from 64 half on
+    const int trow = q * 32 + lane;    // its row of the CTA's 128
+    uint8_t* buf = sO + (warp - 2) * kOutBytes;
     const uint32_t tempty_leader0 = kPair ? ptx::mapa(ptx::smem_addr(&tempty[0]), 0) : 0u;
     uint32_t acc = 0, acc_phase = 0;
-    // The whole warp polls and stops as one (the TMEM loads are collective).
-    auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, W.wait(bar, parity) ? 1 : 0) != 0;
+    // The whole warp polls and stops as one (the TMEM loads are collective);
+    // FWD: both warps of a lane quarter, which meet at a named barrier below.
+    auto wait_tile = [&]() -> bool {
+      bool ok = __all_sync(0xffffffffu, W.wait_suspended(&tfull[acc], acc_phase) ? 1 : 0) != 0;
+      if constexpr (KIND == LK_FWD) ok = !ptx::named_barrier_or(1 + q, 64, !ok);
+      if (ok) ptx::tc_fence_after();
+      return ok;
     };
-    for (int t = pair; t < p.num_tiles; t += npairs) {
-      const Tile tl = tile_of<KIND>(p, t);
-      const long long row = static_cast<long long>(tl.mt) * TM + cta * kBM + q * 32 + lane;
-      const int col0 = tl.nt * kBN;  // within the piece (FWD, DL) or D (DX, DW)
+    // Hands the accumulator back (every warp, after its last read of it).
+    auto release_acc = [&]() {
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair)
+          ptx::mbar_arrive_cluster(tempty_leader0 + acc * 8);
+        else
+          ptx::mbar_arrive(&tempty[acc]);
+      }
+    };
+    // The staged 64 columns to (x, y) of a map, by one lane.
+    auto store_out = [&](const CUtensorMap* map, int x, int y) {
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::tma_store_2d(map, buf, x, y);
+        ptx::bulk_commit();
+      }
+    };
+    auto buf_free = [&]() {
+      if (lane == 0) ptx::bulk_wait_read();
+      __syncwarp();
+    };
+    bool more = work.next(tl);
+    Tile ahead = tl;
+    Token token_ahead{};
+    auto row_of = [&](const Tile& w) {  // the warp's first row
+      return w.mt * TM + static_cast<int>(cta) * kBM + q * 32;
+    };
+    if constexpr (KIND == LK_FWD || KIND == LK_DL) {
+      if (more) token_ahead = token_of<KIND>(p, ahead, row_of(ahead) + lane);
+    }
+    while (more) {
+      tl = ahead;
+      const Token tok = token_ahead;
+      more = work.next(ahead);
+      const int row0 = row_of(tl);
+      const long long row = row0 + lane;
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kBN;
-      auto release_acc = [&]() {
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (kPair)
-            ptx::mbar_arrive_cluster(tempty_leader0 + acc * 8);
-          else
-            ptx::mbar_arrive(&tempty[acc]);
-        }
-      };
       if constexpr (KIND == LK_FWD || KIND == LK_DL) {
         const bool row_ok = row < p.T;
+        const int col0 = tl.nt * p.width;                // within the piece
         const int vcol0 = tl.rank * p.Vs + p.v0 + col0;  // the tile's first vocabulary index
-        const int ncols = min(kBN, p.vn - col0);
-        Targets tg = targets_from(p, row_ok, row, vcol0);
-        // DL: the token's coefficients (all zero and not live: an ignored row)
+        const int ncols = min(p.width, p.vn - col0);
+        // (the other half's targets are passed over below)
+        Targets tg = targets_from(p, tok, row, vcol0);
+        if (more) token_ahead = token_of<KIND>(p, ahead, row_of(ahead) + lane);
+        // DL: the token's coefficients (not live: an ignored row, all zeros)
         float ca = 0.f, cb = 0.f, cw = 0.f, off2 = 0.f;
         bool live = false;
         if constexpr (KIND == LK_DL) {
           if (row_ok) {
-            const float g = __ldg(p.dloss + row);
-            const float lse = __ldg(p.lse[tl.rank] + row);
-            off2 = lse * kLog2e;
+            off2 = tok.lse * kLog2e;
             if (p.labels != nullptr) {
-              const int y = __ldg(p.labels + row);
-              live = label_live(p, y);
-              if (tl.rank == 0 && vcol0 == 0 && !live && y != p.ignore_index)
+              live = label_live(p, tok.y);
+              if (vcol0 == 0 && !live && tok.y != p.ignore_index)
                 atomicCAS(p.status, 0, FCC_ERR_INVALID);
-              ca = g * (1.f + 2.f * p.z * lse);
-              cb = g * (p.smoothing / static_cast<float>(p.R * p.Vs));
-              cw = g * (1.f - p.smoothing);
+              ca = tok.g * (1.f + 2.f * p.z * tok.lse);
+              cb = tok.g * (p.smoothing / static_cast<float>(p.R * p.Vs));
+              cw = tok.g * (1.f - p.smoothing);
             } else {
-              live = __ldg(p.hit_idx + row * p.K) != INT_MAX;
-              ca = g * p.tau;
-              cw = g * p.tau;
+              live = tok.first != INT_MAX;
+              ca = tok.g * p.tau;
+              cw = tok.g * p.tau;
             }
           }
         }
-        if (!wait_warp(&tfull[acc], acc_phase)) break;
-        ptx::tc_fence_after();
+        if (!wait_tile()) break;
         float m2 = -INFINITY, sum = 0.f, lsum = 0.f;  // FWD: base-2 maximum, sum; plain sum
-#pragma unroll 1
-        for (int c = 0; c < kBN; c += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          ptx::tmem_ld_32x32b_x32(taddr + c, v);
-          ptx::tmem_ld_wait();
-          if (c == kBN - 32) release_acc();
-          const int nc = ncols - c;  // valid columns of the chunk
-          if (nc <= 0) continue;
+        // One chunk of 32 columns from c on, of which nc > 0 exist.
+        auto chunk = [&](uint32_t (&v)[32], int c, int nc) {
           if (p.cap > 0.f) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              v[k] = __float_as_uint(p.cap * tanhf(__uint_as_float(v[k]) * p.inv_cap));
+              v[k] = __float_as_uint(soft_cap(__uint_as_float(v[k]), p.cap, p.inv_cap));
           }
+          const int vc = vcol0 + c, vend = vc + min(32, nc);
           if constexpr (KIND == LK_FWD) {
-            while (tg.next < vcol0 + c + 32) {
-              const int at = tg.next - (vcol0 + c);
-              float x = 0.f;
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k == at) x = __uint_as_float(v[k]);
-              if (at < nc) p.pick[row * p.K + tg.cur] = x;
-              if (at >= nc) break;  // (the next rank's columns)
-              targets_advance(tg);
-            }
             if (nc < 32) {
 #pragma unroll
               for (int k = 0; k < 32; ++k)
@@ -531,6 +684,17 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
                 if (k < nc) l4[k & 3] += __uint_as_float(v[k]);
               lsum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
             }
+            // Targets in the chunk; those before it are the other half's.
+            while (tg.next < vc) targets_advance(tg);
+            while (tg.next < vend) {
+              const int at = tg.next - vc;
+              float x = 0.f;
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k == at) x = __uint_as_float(v[k]);
+              p.pick[row * p.K + tg.cur] = x;
+              targets_advance(tg);
+            }
           } else {
             float d[32];
 #pragma unroll
@@ -538,13 +702,13 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               const float pv = ptx::ex2_approx(fmaf(__uint_as_float(v[k]), p.c2, -off2));
               d[k] = fmaf(ca, pv, -cb);
             }
-            while (tg.next < vcol0 + c + 32) {
-              const int at = tg.next - (vcol0 + c);
+            while (tg.next < vc) targets_advance(tg);
+            while (tg.next < vend) {
+              const int at = tg.next - vc;
               const float w = p.labels != nullptr ? cw : cw * __ldg(p.hit_q + row * p.K + tg.cur);
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (k == at) d[k] -= w;
-              if (at >= nc) break;
               targets_advance(tg);
             }
 #pragma unroll
@@ -556,80 +720,142 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               }
               v[k] = live ? __float_as_uint(x) : 0u;
             }
-            __syncwarp();
-            const int ok = row_ok ? 1 : 0;
-            uint16_t* dst0 = p.dl + static_cast<long long>(tl.rank) * p.T * p.ldl + col0 + c;
-            store_block_bf16(v, lane, [&](int src, int k, const uint4& x) {
-              const long long srow = row - lane + src;
-              if (__shfl_sync(0xffffffffu, ok, src) && col0 + c + 8 * k + 8 <= p.ldl)
-                ptx::st_global_v4(dst0 + srow * p.ldl + 8 * k, x.x, x.y, x.z, x.w);
-            });
+          }
+          __syncwarp();
+        };
+        // 64 columns at a time; the second 32 come from TMEM behind the first.
+#pragma unroll 1
+        for (int c = 64 * half; c < ncols; c += 128) {
+          uint32_t v[2][32];
+          ptx::tmem_ld_32x32b_x32(taddr + c, v[0]);
+          ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
+          ptx::tmem_ld_wait();
+          const int nc = ncols - c;
+          chunk(v[0], c, nc);
+          if (nc > 32) chunk(v[1], c + 32, nc - 32);
+          if constexpr (KIND == LK_DL) {
+            buf_free();
+            stage_bf16(buf, lane, 0, v[0]);
+            stage_bf16(buf, lane, 1, v[1]);
+            // (columns past the piece's end are not stored)
+            if (row0 < p.T) store_out(&p.mapO[tl.rank], col0 + c, row0);
           }
         }
+        release_acc();
         if constexpr (KIND == LK_FWD) {
-          if (row_ok) {
+          // The second warp of the lane quarter hands its part to the first.
+          float* stat = sStat + trow * 3;
+          if (half == 1) {
+            stat[0] = m2;
+            stat[1] = sum;
+            stat[2] = lsum;
+          }
+          ptx::named_barrier_sync(1 + q, 64);
+          if (half == 0 && row_ok) {
+            merge(m2, sum, stat[0], stat[1]);
             const long long o = static_cast<long long>(tl.rank * p.tiles_n + tl.nt) * p.T + row;
             p.part[o] = make_float2(m2, sum);
-            if (p.part_sum != nullptr) p.part_sum[o] = lsum;
+            if (p.part_sum != nullptr) p.part_sum[o] = lsum + stat[2];
           }
         }
       } else if constexpr (KIND == LK_DX) {
         const bool row_ok = row < p.T;
-        if (!wait_warp(&tfull[acc], acc_phase)) break;
-        ptx::tc_fence_after();
-        float* dst = p.acc + (static_cast<long long>(tl.split) * p.T + row) * p.D + col0;
+        const int col0 = tl.nt * kBN;
+        const int width = min(kBN, p.D - col0);
+        const bool none = tl.it_lo >= tl.it_hi;  // (no steps of a short last piece: adds nothing)
+        if (!wait_tile()) break;
+        float* dst = tl.part == 0
+                         ? p.acc + row * p.D + col0
+                         : p.parts + (static_cast<long long>(tl.shared) * (p.shares.max_parts - 1) +
+                                      tl.part - 1) * (TM * kBN) +
+                               (cta * kBM + trow) * kBN;
 #pragma unroll 1
-        for (int c = 0; c < kBN; c += 32) {
-          uint32_t v[32];
-          __syncwarp();
-          ptx::tmem_ld_32x32b_x32(taddr + c, v);
+        for (int c = 64 * half; c < width; c += 128) {
+          uint32_t v[64];
+          ptx::tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+          ptx::tmem_ld_32x32b_x32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
           ptx::tmem_ld_wait();
-          if (c == kBN - 32) release_acc();
-          if (!row_ok) continue;
-          if (tl.it_lo >= tl.it_hi) {  // (a short last piece leaves this part no K steps)
-            if (!p.first) continue;
+          if (row_ok && (p.first || !none)) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] = 0u;
-          }
-#pragma unroll
-          for (int g = 0; g < 8; ++g) {
-            if (col0 + c + 4 * g + 4 > p.D) continue;
-            float4 x = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
-                                   __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
-            float4* o = reinterpret_cast<float4*>(dst + c + 4 * g);
-            if (!p.first) {
-              const float4 y = *o;
-              x.x += y.x;
-              x.y += y.y;
-              x.z += y.z;
-              x.w += y.w;
+            for (int g = 0; g < 16; ++g) {
+              if (c + 4 * g + 4 > width) continue;
+              float4 x = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                     __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+              if (none) x = make_float4(0.f, 0.f, 0.f, 0.f);
+              float4* o = reinterpret_cast<float4*>(dst + c + 4 * g);
+              if (!p.first) {
+                const float4 y = *o;
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+              }
+              *o = x;
             }
-            *o = x;
           }
-        }
-      } else {
-        const bool row_ok = row < p.vn;
-        if (!wait_warp(&tfull[acc], acc_phase)) break;
-        ptx::tc_fence_after();
-        uint16_t* dst = static_cast<uint16_t*>(p.out[tl.rank]) +
-                        (static_cast<long long>(p.v0)) * p.D + col0;
-        const int ok = row_ok ? 1 : 0;
-#pragma unroll 1
-        for (int c = 0; c < kBN; c += 32) {
-          uint32_t v[32];
           __syncwarp();
-          ptx::tmem_ld_32x32b_x32(taddr + c, v);
-          ptx::tmem_ld_wait();
-          if (c == kBN - 32) release_acc();
-          store_block_bf16(v, lane, [&](int src, int k, const uint4& x) {
-            const long long srow = row - lane + src;
-            if (__shfl_sync(0xffffffffu, ok, src) && col0 + c + 8 * k + 8 <= p.D)
-              ptx::st_global_v4(dst + srow * p.D + c + 8 * k, x.x, x.y, x.z, x.w);
-          });
         }
+        release_acc();
+      } else {
+        const int col0 = tl.nt * kBN;
+        const int width = min(kBN, p.D - col0);
+        if (!wait_tile()) break;
+#pragma unroll 1
+        for (int c = 64 * half; c < width; c += 128) {
+          uint32_t v[2][32];
+          ptx::tmem_ld_32x32b_x32(taddr + c, v[0]);
+          ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
+          ptx::tmem_ld_wait();
+          buf_free();
+          stage_bf16(buf, lane, 0, v[0]);
+          stage_bf16(buf, lane, 1, v[1]);
+          // (columns past D, and rows past the piece, which are past the
+          // shard, are not stored)
+          if (row0 < p.vn) store_out(&p.mapO[tl.rank], col0 + c, p.v0 + row0);
+        }
+        release_acc();
       }
       acc ^= 1u;
       if (acc == 0) acc_phase ^= 1u;
+    }
+    if constexpr (stages_out(KIND)) {
+      if (lane == 0) ptx::bulk_wait_all();
+    }
+  } else {
+    // ------------------------------------- the labels' own logits (FWD, labels)
+    // Two warps beside the GEMM take one token at a time and compute x_y =
+    // X_t . W_y in f32 with short chains of additions.  The tensor core's sum
+    // of D/16 partial sums loses up to a few 1e-6 of it, which shows in the
+    // loss (lse - l_y) more than in lse; these 2 D f32 products per token are
+    // hidden behind the 2 V D of the GEMM.
+    if constexpr (KIND == LK_FWD) {
+      if (p.labels != nullptr) {
+        const int vecs = p.D / 8;
+        for (long long t = blockIdx.x * 2 + (warp - 2 - kEpiWarps); t < p.T; t += 2 * gridDim.x) {
+          const int y = __ldg(p.labels + t);
+          if (!label_live(p, y)) continue;
+          const int r = y / p.Vs;
+          const uint4* x = reinterpret_cast<const uint4*>(p.X[r]) + t * vecs;
+          const uint4* w = reinterpret_cast<const uint4*>(p.Wr[r]) +
+                           static_cast<long long>(y - r * p.Vs) * vecs;
+          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+          for (int i = lane; i < vecs; i += 32) {
+            const uint4 a = __ldg(x + i), b = __ldg(w + i);
+            const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              s[2 * k] = fmaf(__uint_as_float(au[k] << 16), __uint_as_float(bu[k] << 16), s[2 * k]);
+              s[2 * k + 1] = fmaf(__uint_as_float(au[k] & 0xffff0000u),
+                                  __uint_as_float(bu[k] & 0xffff0000u), s[2 * k + 1]);
+            }
+          }
+          float d = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+          if (lane == 0) p.own_logit[t] = d;
+        }
+      }
     }
   }
 
@@ -652,78 +878,119 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
 }
 
 // ------------------------------------------------------------ teacher entries
-// One CTA of `n2` threads (a power of two >= K, at least 32) per token: the
-// valid entries' probabilities q = softmax(teacher / tau) and their order by
-// vocabulary index (a bitonic sort in shared memory; equal indices stay
-// separate entries), written as hit_idx (INT_MAX past the last) and hit_q.
+// One warp per token: the valid entries' probabilities q = softmax(teacher /
+// tau) and their order by vocabulary index, written as hit_idx (INT_MAX past
+// the last) and hit_q; then, per logit tile, the place of the first entry at
+// or past it.  E entries per lane (lane i: places iE .. iE + E - 1) are sorted
+// by (index, place in the list) with a bitonic network, whose short strides
+// stay within a lane and whose long ones are shuffles.
 struct TeacherArgs {
   const int32_t* idx;   // [T, K], negative = no entry
   const float* logits;  // [T, K]
   int32_t* hit_idx;
   float* hit_q;
-  int T, K, V;
+  uint16_t* hit_start;  // [T][start_ld]
+  long long start_ld;
+  int T, K, V, Vs;
+  int npieces, piece_tiles, piece_rows, width;  // logit tiles of a rank
   float inv_tau;
   int* status;
 };
 
-__global__ void __launch_bounds__(256) teacher_kernel(const TeacherArgs a) {
+constexpr int kTeacherWarps = 4;
+
+template <int E>
+__global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const TeacherArgs a) {
   ptx::griddep_wait();  // launched with programmatic stream serialization
   ptx::griddep_launch_dependents();
-  __shared__ int key[FCC_MAX_TEACHER];
-  __shared__ float val[FCC_MAX_TEACHER];
-  __shared__ float red[8];
-  const int n2 = blockDim.x, k = threadIdx.x, lane = k & 31, warp = k >> 5;
-  const long long row = blockIdx.x;
-  int id = INT_MAX;
-  float x = -INFINITY;
-  if (k < a.K) {
-    const int i = __ldg(a.idx + row * a.K + k);
-    if (i >= 0 && i < a.V) {
-      x = __ldg(a.logits + row * a.K + k);
-      if (x != -INFINITY) id = i;  // (a logit of -inf is no entry)
-    } else if (i >= a.V) {
-      atomicCAS(a.status, 0, FCC_ERR_INVALID);
+  constexpr int N = 32 * E;
+  __shared__ float prob[kTeacherWarps][N];
+  __shared__ int sorted[kTeacherWarps][N];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long row = static_cast<long long>(blockIdx.x) * kTeacherWarps + w;
+  if (row >= a.T) return;
+  int id[E];
+  float x[E];
+  float m = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int k = 32 * e + lane;
+    id[e] = INT_MAX;
+    x[e] = -INFINITY;
+    if (k < a.K) {
+      const int i = __ldg(a.idx + row * a.K + k);
+      if (i >= 0 && i < a.V) {
+        x[e] = __ldg(a.logits + row * a.K + k);
+        if (x[e] != -INFINITY) id[e] = i;  // (a logit of -inf is no entry)
+      } else if (i >= a.V) {
+        atomicCAS(a.status, 0, FCC_ERR_INVALID);
+      }
     }
+    m = fmaxf(m, x[e]);  // (drops a NaN; the sum keeps it)
   }
-  // softmax over the valid entries (fmaxf drops a NaN; the sum keeps it)
-  float m = x;
+#pragma unroll
   for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = red[0];
-  for (int w = 1; w < n2 / 32; ++w) m = fmaxf(m, red[w]);
-  __syncthreads();
-  // (the difference is taken before the scaling, which could overflow)
-  const float e = id != INT_MAX ? expf((x - m) * a.inv_tau) : 0.f;
-  float s = e;
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    // (the difference is taken before the scaling, which could overflow)
+    x[e] = id[e] != INT_MAX ? expf((x[e] - m) * a.inv_tau) : 0.f;
+    s += x[e];
+  }
+#pragma unroll
   for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  if (lane == 0) red[warp] = s;
-  __syncthreads();
-  s = red[0];
-  for (int w = 1; w < n2 / 32; ++w) s += red[w];
-  key[k] = id;
-  val[k] = id != INT_MAX ? e / s : 0.f;
-  __syncthreads();
-  for (int size = 2; size <= n2; size <<= 1) {
+  unsigned long long key[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    prob[w][32 * e + lane] = id[e] != INT_MAX ? x[e] / s : 0.f;
+    key[e] = (static_cast<unsigned long long>(id[e]) << 8) | static_cast<unsigned>(32 * e + lane);
+  }
+  // (any start order will do: the place in the list is part of the key)
+#pragma unroll
+  for (int size = 2; size <= N; size <<= 1) {
+#pragma unroll
     for (int stride = size >> 1; stride > 0; stride >>= 1) {
-      const int j = k ^ stride;
-      if (j > k) {
-        const bool up = (k & size) == 0;
-        if ((key[k] > key[j]) == up) {
-          const int ti = key[k];
-          key[k] = key[j];
-          key[j] = ti;
-          const float tv = val[k];
-          val[k] = val[j];
-          val[j] = tv;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int i = lane * E + e;
+        const bool up = (i & size) == 0;
+        if (stride >= E) {
+          const unsigned long long o = __shfl_xor_sync(0xffffffffu, key[e], stride / E);
+          const bool low = (i & stride) == 0;
+          key[e] = (low == up) == (o < key[e]) ? o : key[e];
+        } else if ((e & stride) == 0) {
+          unsigned long long &u = key[e], &v = key[e | (stride & (E - 1))];
+          if ((v < u) == up) {
+            const unsigned long long t = u;
+            u = v;
+            v = t;
+          }
         }
       }
-      __syncthreads();
     }
   }
-  if (k < a.K) {
-    a.hit_idx[row * a.K + k] = key[k];
-    a.hit_q[row * a.K + k] = val[k];
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int place = lane * E + e, at = static_cast<int>(key[e] >> 8);
+    sorted[w][place] = at;
+    if (place < a.K) {
+      a.hit_idx[row * a.K + place] = at;
+      a.hit_q[row * a.K + place] = prob[w][key[e] & 255u];
+    }
+  }
+  __syncwarp();
+  for (int t = lane; t < a.start_ld; t += 32) {
+    const int rp = t / a.piece_tiles;
+    const int r = rp / a.npieces;
+    const int col = min((rp - r * a.npieces) * a.piece_rows + (t - rp * a.piece_tiles) * a.width, a.Vs);
+    const int first = r * a.Vs + col;
+    int lo = 0;  // entries before `first`: all of the first lo, and maybe more
+#pragma unroll
+    for (int half = N / 2; half > 0; half >>= 1)
+      if (sorted[w][lo + half - 1] < first) lo += half;
+    if (sorted[w][lo] < first) ++lo;
+    a.hit_start[row * a.start_ld + t] = static_cast<uint16_t>(lo);
   }
 }
 
@@ -736,23 +1003,16 @@ struct CombineArgs {
   const float2* part;
   const float* part_sum;
   const float* pick;
+  const float* own_logit;
   const int32_t* labels;
   const int32_t* hit_idx;
   const float* hit_q;
   float* loss[FCC_MAX_RANKS];
   float* lse[FCC_MAX_RANKS];
   int R, T, V, K, nparts, tok, ignore_index;
-  float tau, smoothing, z;
+  float tau, smoothing, z, cap;
   int* status;
 };
-
-__device__ __forceinline__ void merge(float& m, float& s, float m1, float s1) {
-  const float mn = fmaxf(m, m1);
-  const float off = mn == -INFINITY ? 0.f : mn;
-  // (a sum whose maximum is -inf is 0, or NaN after a NaN logit: kept as it is)
-  s = (m == -INFINITY ? s : s * exp2f(m - off)) + (m1 == -INFINITY ? s1 : s1 * exp2f(m1 - off));
-  m = mn;
-}
 
 __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) {
   ptx::griddep_wait();  // launched with programmatic stream serialization
@@ -792,7 +1052,8 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
     __syncthreads();
   }
   if (part != 0 || t >= a.T) return;
-  const float lse = (sm[threadIdx.x] + log2f(ss[threadIdx.x])) * kLn2;
+  const float log2s = log2f(ss[threadIdx.x]);
+  float lse = (sm[threadIdx.x] + log2s) * kLn2;
   float loss = 0.f;
   if (a.labels != nullptr) {
     const int y = __ldg(a.labels + t);
@@ -800,8 +1061,22 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
       if (y < 0 || y >= a.V) {
         atomicCAS(a.status, 0, FCC_ERR_INVALID);
       } else {
-        loss = lse - (1.f - a.smoothing) * __ldg(a.pick + t) + a.z * lse * lse;
-        if (a.part_sum != nullptr) loss -= a.smoothing / static_cast<float>(a.V) * sl[threadIdx.x];
+        // The label's logit l inside the sum is the tensor core's; the more
+        // exact one is l + e, and with p = exp(l - lse) the sum's logarithm
+        // then grows by log(1 + p (exp(e) - 1)).  lse - l is taken in base 2
+        // from the sum's own maximum, so that a label that is the maximum
+        // loses nothing.
+        const float l = __ldg(a.pick + t);
+        const float x = __ldg(a.own_logit + t);
+        const float e = (a.cap > 0.f ? a.cap * tanhf(x / a.cap) : x) - l;
+        const float l2 = __fmul_rn(l, kLog2e);  // (rounded as the maximum was)
+        const float grow = log1pf(exp2f(l2 - sm[threadIdx.x] - log2s) * expm1f(e));
+        const float gap = (sm[threadIdx.x] - l2 + log2s) * kLn2 + (grow - e);
+        lse += grow;
+        loss = gap + a.z * lse * lse;
+        // lse - (1 - eps) l_y - eps / V sum l = gap + eps (l_y - mean l)
+        if (a.part_sum != nullptr)
+          loss += a.smoothing * (l + e - sl[threadIdx.x] / static_cast<float>(a.V));
       }
     }
   } else if (__ldg(a.hit_idx + t * a.K) != INT_MAX) {
@@ -814,33 +1089,50 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
 }
 
 // ------------------------------------------------------------------ dX finish
-// dX[r] = bf16(sum of the f32 slabs, in order) for every rank.
+// dX[r] = bf16(acc + the further parts of shared tiles, in order) for every
+// rank.  A CTA takes kFinRows rows of a tile: 64 threads of 4 columns a row.
+constexpr int kFinRows = 8;
 struct FinishArgs {
   const float* acc;
+  const float* parts;
   void* out[FCC_MAX_RANKS];
-  long long n;  // T * D, a multiple of 8
-  int splits, R;
+  int T, D, R;
+  int tile_m, tiles_m, tiles_n, group_m, full_tiles;
+  Shares shares;
 };
 
-__global__ void __launch_bounds__(256) dx_finish_kernel(const FinishArgs a) {
+__global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ FinishArgs a) {
   ptx::griddep_wait();  // launched with programmatic stream serialization
   ptx::griddep_launch_dependents();
-  const long long nv = a.n / 8;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < nv;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < a.splits; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(a.acc + s * a.n) + 2 * i;
-      const float4 u = __ldcs(p), w = __ldcs(p + 1);
-      x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-      x[4] += w.x; x[5] += w.y; x[6] += w.z; x[7] += w.w;
+  const int per = a.tile_m / kFinRows;
+  const int t = blockIdx.x / per;
+  const int r0 = (blockIdx.x - t * per) * kFinRows;
+  int mt, nt;
+  raster(t, a.tiles_m, a.tiles_n, a.group_m, mt, nt);
+  const int c = (threadIdx.x & 63) * 4;
+  const int col = nt * kBN + c;
+  int n = 1;
+  long long part0 = 0;
+  if (t >= a.full_tiles) {
+    n = a.shares.parts(t - a.full_tiles);
+    part0 = static_cast<long long>(t - a.full_tiles) * (a.shares.max_parts - 1);
+  }
+  if (col + 4 > a.D) return;
+  for (int rr = r0 + (threadIdx.x >> 6); rr < r0 + kFinRows; rr += 4) {
+    const long long row = static_cast<long long>(mt) * a.tile_m + rr;
+    if (row >= a.T) return;
+    float4 x = __ldcs(reinterpret_cast<const float4*>(a.acc + row * a.D + col));
+    for (int i = 1; i < n; ++i) {
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(
+          a.parts + ((part0 + i - 1) * a.tile_m + rr) * kBN + c));
+      x.x += y.x;
+      x.y += y.y;
+      x.z += y.z;
+      x.w += y.w;
     }
-    uint4 o;
-    o.x = ptx::pack_bf16x2(x[0], x[1]);
-    o.y = ptx::pack_bf16x2(x[2], x[3]);
-    o.z = ptx::pack_bf16x2(x[4], x[5]);
-    o.w = ptx::pack_bf16x2(x[6], x[7]);
-    for (int r = 0; r < a.R; ++r) reinterpret_cast<uint4*>(a.out[r])[i] = o;
+    const uint2 o = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
+    for (int r = 0; r < a.R; ++r)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out[r]) + row * a.D + col) = o;
   }
 }
 
@@ -858,39 +1150,8 @@ cudaError_t launch_kind(const LossParams& p, int grid, cudaStream_t st) {
   constexpr int kSmem = Cfg<KIND, CG>::kSmem;
   const cudaError_t e = smem_attr_once(attr_set, kern, kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid, 1, 1), dim3(kGemmThreads, 1, 1), kSmem, st,
+  return launch_pdl(kern, dim3(grid, 1, 1), dim3(threads_of(KIND), 1, 1), kSmem, st,
                     CG == 2 ? 2u : 1u, p);
-}
-
-// One of the four products: tile counts for the shape, then the launch over
-// at most `sms` CTAs.
-template <int KIND>
-cudaError_t launch_loss_gemm(LossParams& p, int cg, int sms, cudaStream_t st) {
-  const int64_t tm = static_cast<int64_t>(kBM) * cg;
-  int64_t tiles = 0;
-  if (KIND == LK_FWD || KIND == LK_DL) {
-    p.tiles_m = static_cast<int>(cdiv(p.T, tm));
-    p.tiles_n = static_cast<int>(cdiv(p.vn, kBN));
-    p.k_iters = static_cast<int>(cdiv(p.D, kBK));
-    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
-  } else if (KIND == LK_DX) {
-    p.tiles_m = static_cast<int>(cdiv(p.T, tm));
-    p.tiles_n = static_cast<int>(cdiv(p.D, kBN));
-    p.kb_per_rank = static_cast<int>(cdiv(p.vn, kBK));
-    p.k_iters = p.R * p.kb_per_rank;
-    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits;
-  } else {
-    p.tiles_m = static_cast<int>(cdiv(p.vn, tm));
-    p.tiles_n = static_cast<int>(cdiv(p.D, kBN));
-    p.k_iters = static_cast<int>(cdiv(p.T, kBK));
-    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
-  }
-  if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
-  p.num_tiles = static_cast<int>(tiles);
-  p.group_m = 8;
-  const int slots = std::max(1, std::min(sms / cg, gemm_max_clusters(cg)));
-  const int grid = cg * std::min(slots, p.num_tiles);
-  return cg == 2 ? launch_kind<KIND, 2>(p, grid, st) : launch_kind<KIND, 1>(p, grid, st);
 }
 
 // A CTA pair per tile when the rows exceed 128 and the single-CTA tiles
@@ -899,6 +1160,75 @@ int choose_cg(const fcc_opts* o, int64_t rows, int64_t single_tiles, int sms) {
   if (sms < 2) return 1;
   if (o != nullptr && (o->cta_pair == 1 || o->cta_pair == 2)) return o->cta_pair;
   return rows > kBM && single_tiles > sms ? 2 : 1;
+}
+
+// Width of the logit tiles: the widest of the fewest (rounds of tiles x
+// width), counting 16 columns per tile for what does not depend on the width.
+// One token on 32000 words: 143 tiles of 224 columns in one round, not 125 of
+// 256.  `step`: 16, or 64 where whole 64-column blocks are stored.
+int choose_width(int R, int64_t tiles_m, int64_t vn, int slots, int step) {
+  int best = kBN;
+  int64_t least = INT64_MAX;
+  for (int w = kBN; w >= kBN / 2; w -= step) {
+    const int64_t cost = cdiv(tiles_m * R * cdiv(vn, w), slots) * (w + 16);
+    if (cost < least) {
+      least = cost;
+      best = w;
+    }
+  }
+  return best;
+}
+
+// The shares of `rest` tiles of k steps over at most `slots` CTAs (pairs), of
+// four steps at least.
+Shares plan_shares(int rest, int k, int slots) {
+  Shares s;
+  std::memset(&s, 0, sizeof(s));
+  s.max_parts = 1;
+  if (rest == 0) return s;
+  const int64_t total = static_cast<int64_t>(rest) * k;
+  s.tiles = rest;
+  s.k = k;
+  s.ctas = static_cast<int>(std::max<int64_t>(rest, std::min<int64_t>(slots, total / 4)));
+  s.groups = s.ctas / rest;
+  s.helpers = s.ctas - s.groups * rest;
+  s.len = static_cast<int>(s.helpers > 0 ? cdiv(total, s.ctas) : cdiv(k, s.groups));
+  s.tail = std::max(0, k - s.groups * s.len);
+  s.helpers = static_cast<int>(std::min<int64_t>(s.helpers, s.tails()));  // (none of them idle)
+  for (int i = 0; i < rest; ++i) s.max_parts = std::max(s.max_parts, s.parts(i));
+  return s;
+}
+
+int slots_of(int cg, int sms) { return std::max(1, std::min(sms / cg, gemm_max_clusters(cg))); }
+
+// One of the four products: tile counts for the shape, then the launch over
+// at most `sms` CTAs.
+template <int KIND>
+cudaError_t launch_loss_gemm(LossParams& p, int cg, int sms, cudaStream_t st) {
+  const int64_t tm = static_cast<int64_t>(kBM) * cg;
+  const int slots = slots_of(cg, sms);
+  int64_t tiles = 0;
+  if (KIND == LK_FWD || KIND == LK_DL) {
+    p.tiles_m = static_cast<int>(cdiv(p.T, tm));
+    p.tiles_n = static_cast<int>(cdiv(p.vn, p.width));
+    p.k_iters = static_cast<int>(cdiv(p.D, kBK));
+    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
+  } else if (KIND == LK_DX) {
+    p.kb_per_rank = static_cast<int>(cdiv(p.vn, kBK));
+    p.k_iters = p.R * p.kb_per_rank;
+    tiles = p.num_tiles;  // (planned by the caller, with the shares)
+  } else {
+    p.tiles_m = static_cast<int>(cdiv(p.vn, tm));
+    p.tiles_n = static_cast<int>(cdiv(p.D, kBN));
+    p.k_iters = static_cast<int>(cdiv(p.T, kBK));
+    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
+  }
+  if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
+  p.num_tiles = static_cast<int>(tiles);
+  if (KIND != LK_DX) p.full_tiles = p.num_tiles;
+  const int shared = p.shares.groups * p.shares.tiles + p.shares.helpers;
+  const int grid = cg * std::max(std::min(slots, p.full_tiles), shared);
+  return cg == 2 ? launch_kind<KIND, 2>(p, grid, st) : launch_kind<KIND, 1>(p, grid, st);
 }
 
 // What one call is about, checked.
@@ -956,13 +1286,14 @@ int usable_sms(const fcc_opts* o) {
 }
 
 // Scratch layout.  Forward: partials, target logits; distillation also the
-// sorted teacher entries.  Backward: the piece's dl, the dX slabs.
+// sorted teacher entries.  Backward: the piece's dl, the f32 sums of dX.
 struct Plan {
-  size_t hit_idx = 0, hit_q = 0, pick = 0, part = 0, part_sum = 0;
-  size_t dl = 0, acc = 0, total = 0;
+  size_t hit_idx = 0, hit_q = 0, hit_start = 0, pick = 0, own_logit = 0, part = 0, part_sum = 0;
+  size_t dl = 0, acc = 0, parts = 0, total = 0;
+  int cg = 1, width = kBN;  // logit tiles
   int nparts = 0;
-  int64_t piece = 0;  // vocabulary rows of a piece, per rank
-  int splits = 1;     // K parts of dX
+  int64_t piece = 0;        // vocabulary rows of a piece, per rank (forward: all)
+  int npieces = 1, piece_tiles = 0;
 };
 
 constexpr size_t kPieceBytes = size_t(512) << 20;  // dl held at a time
@@ -978,15 +1309,9 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     p.hit_q = off;
     off += up256(static_cast<size_t>(T) * K * 4);
   }
-  if (!grad) {
-    p.nparts = static_cast<int>(R * cdiv(Vs, kBN));
-    p.pick = off;
-    off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
-    p.part = off;
-    off += up256(static_cast<size_t>(p.nparts) * T * 8);
-    p.part_sum = off;
-    if (smoothing) off += up256(static_cast<size_t>(p.nparts) * T * 4);
-  } else {
+  int64_t rows = Vs;  // vocabulary rows of a launch, per rank
+  p.piece = Vs;
+  if (grad) {
     // Equal pieces, whole tiles of 256 rows, as few as hold kPieceBytes of dl
     // (or the caller's count).
     const int64_t most = std::max<int64_t>(
@@ -994,16 +1319,39 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     int64_t n = o != nullptr && o->chunks > 0 ? o->chunks : cdiv(Vs, most);
     n = std::max<int64_t>(1, std::min(n, cdiv(Vs, kBN)));
     p.piece = cdiv(cdiv(Vs, n), kBN) * kBN;
+    rows = std::min(p.piece, Vs);
+    p.npieces = static_cast<int>(cdiv(Vs, p.piece));
+  }
+  p.cg = choose_cg(o, T, cdiv(T, kBM) * R * cdiv(rows, kBN), sms);
+  p.width = choose_width(R, cdiv(T, kBM * p.cg), rows, std::max(1, sms / p.cg), grad ? 64 : 16);
+  p.piece_tiles = static_cast<int>(cdiv(rows, p.width));
+  if (K > 0) {
+    p.hit_start = off;
+    off += up256(static_cast<size_t>(T) * R * p.npieces * p.piece_tiles * 2);
+  }
+  if (!grad) {
+    p.nparts = static_cast<int>(R * cdiv(Vs, p.width));
+    p.pick = off;
+    off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
+    p.own_logit = off;
+    if (K == 0) off += up256(static_cast<size_t>(T) * 4);
+    p.part = off;
+    off += up256(static_cast<size_t>(p.nparts) * T * 8);
+    p.part_sum = off;
+    if (smoothing) off += up256(static_cast<size_t>(p.nparts) * T * 4);
+  } else {
     p.dl = off;
     off += up256(static_cast<size_t>(R) * T * p.piece * 2);
     if (want_dx) {
-      // Few dX tiles: split the vocabulary's K loop so that all SMs have work.
-      const int64_t tiles = cdiv(T, kBM) * cdiv(D, kBN);
-      const int64_t k_iters = R * cdiv(std::min(p.piece, Vs), kBK);
-      p.splits = static_cast<int>(
-          std::max<int64_t>(1, std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), k_iters / 4)));
       p.acc = off;
-      off += up256(static_cast<size_t>(p.splits) * T * D * 4);
+      off += up256(static_cast<size_t>(T) * D * 4);
+      // Blocks for the shared tiles' further parts: fewer than the shares and
+      // the shared tiles together, each at most the CTAs (pairs).
+      const int64_t tiles = cdiv(T, kBM) * cdiv(D, kBN);
+      const int64_t steps = tiles * R * cdiv(rows, kBK);
+      p.parts = off;
+      off += up256(std::min(static_cast<size_t>(2 * sms) * (kBM * kBN * 4),
+                            static_cast<size_t>(steps / 4 + tiles + 1) * (2 * kBM * kBN * 4)));
     }
   }
   p.total = off;
@@ -1019,13 +1367,20 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
   p.Vs = static_cast<int>(c.V / c.R);
   p.v0 = 0;
   p.vn = p.Vs;
-  p.splits = pl.splits;
+  p.width = pl.width;
+  p.npieces = pl.npieces;
+  p.piece_tiles = pl.piece_tiles;
+  p.start_ld = static_cast<long long>(c.R) * pl.npieces * pl.piece_tiles;
+  p.group_m = 16;
+  p.a_rows = static_cast<int>(std::min<int64_t>(c.T, kBM));
+  p.k_rows = static_cast<int>(std::min<int64_t>(cdiv(c.T, 16) * 16, kBK));
   p.K = std::max(c.K, 1);
   if (c.K == 0) {
     p.labels = c.labels;
   } else {
     p.hit_idx = reinterpret_cast<int32_t*>(base + pl.hit_idx);
     p.hit_q = reinterpret_cast<float*>(base + pl.hit_q);
+    p.hit_start = reinterpret_cast<uint16_t*>(base + pl.hit_start);
   }
   p.ignore_index = c.ignore_index;
   p.cap = c.softcap;
@@ -1050,18 +1405,27 @@ cudaError_t launch_teacher(const Call& c, const Plan& pl, char* base, int* statu
   a.V = static_cast<int>(c.V);
   a.inv_tau = 1.f / c.tau;
   a.status = status;
-  unsigned n2 = 32;
-  while (n2 < static_cast<unsigned>(c.K)) n2 <<= 1;
-  return launch_pdl(teacher_kernel, dim3(static_cast<unsigned>(c.T)), dim3(n2), 0, c.st, 1u, a);
+  a.hit_start = reinterpret_cast<uint16_t*>(base + pl.hit_start);
+  a.start_ld = static_cast<long long>(c.R) * pl.npieces * pl.piece_tiles;
+  a.Vs = static_cast<int>(c.V / c.R);
+  a.npieces = pl.npieces;
+  a.piece_tiles = pl.piece_tiles;
+  a.piece_rows = static_cast<int>(pl.piece);
+  a.width = pl.width;
+  const auto kern = c.K <= 32 ? teacher_kernel<1> : c.K <= 64 ? teacher_kernel<2>
+                    : c.K <= 128 ? teacher_kernel<4> : teacher_kernel<8>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(cdiv(c.T, kTeacherWarps))),
+                    dim3(32 * kTeacherWarps), 0, c.st, 1u, a);
 }
 
 // Tensor maps of the logit product: X rows and W rows, both K-major.
-fcc_status logit_maps(LossParams& p, const Call& c, int cg) {
+fcc_status logit_maps(LossParams& p, const Call& c, const Plan& pl) {
   for (int r = 0; r < c.R; ++r) {
-    fcc_status s = internal_encode_map(&p.mapA[r], c.X[r], c.T, c.D, c.D, kBM);
+    fcc_status s = internal_encode_map(&p.mapA[r], c.X[r], c.T, c.D, c.D,
+                                       static_cast<uint32_t>(p.a_rows));
     if (s == FCC_OK)
       s = internal_encode_map(&p.mapB[r], c.W[r], c.V / c.R, c.D, c.D,
-                              static_cast<uint32_t>(kBN / cg));
+                              static_cast<uint32_t>(pl.width / pl.cg));
     if (s != FCC_OK) return s;
   }
   return FCC_OK;
@@ -1074,7 +1438,8 @@ fcc_status forward(const Call& c, float* const* loss, float* const* lse) {
   for (int r = 0; r < c.R; ++r)
     if (!al(loss[r], 4) || !al(lse[r], 4)) return FCC_ERR_INVALID;
   if (s != FCC_OK) return s;
-  const Plan pl = plan_of(c.R, c.T, c.V, c.D, c.K, false, c.smoothing > 0.f, false, 1, c.opts);
+  const Plan pl = plan_of(c.R, c.T, c.V, c.D, c.K, false, c.smoothing > 0.f, false,
+                          usable_sms(c.opts), c.opts);
   void* ws = nullptr;
   int* status = nullptr;
   int sms = 0;
@@ -1086,19 +1451,24 @@ fcc_status forward(const Call& c, float* const* loss, float* const* lse) {
   p.part = reinterpret_cast<float2*>(base + pl.part);
   p.part_sum = c.smoothing > 0.f ? reinterpret_cast<float*>(base + pl.part_sum) : nullptr;
   p.pick = reinterpret_cast<float*>(base + pl.pick);
-  const int cg = choose_cg(c.opts, c.T, cdiv(c.T, kBM) * pl.nparts, sms);
-  if ((s = logit_maps(p, c, cg)) != FCC_OK) return s;
+  p.own_logit = reinterpret_cast<float*>(base + pl.own_logit);
+  for (int r = 0; r < c.R; ++r) {
+    p.X[r] = c.X[r];
+    p.Wr[r] = c.W[r];
+  }
+  if ((s = logit_maps(p, c, pl)) != FCC_OK) return s;
   uint64_t launches = 2;
   if (c.K > 0) {
     if (launch_teacher(c, pl, base, status) != cudaSuccess) return FCC_ERR_CUDA;
     ++launches;
   }
-  if (launch_loss_gemm<LK_FWD>(p, cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
+  if (launch_loss_gemm<LK_FWD>(p, pl.cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
   CombineArgs a;
   std::memset(&a, 0, sizeof(a));
   a.part = p.part;
   a.part_sum = p.part_sum;
   a.pick = p.pick;
+  a.own_logit = p.own_logit;
   a.labels = p.labels;
   a.hit_idx = p.hit_idx;
   a.hit_q = p.hit_q;
@@ -1115,6 +1485,7 @@ fcc_status forward(const Call& c, float* const* loss, float* const* lse) {
   a.tau = c.tau;
   a.smoothing = c.smoothing;
   a.z = c.z;
+  a.cap = c.softcap;
   a.status = status;
   // Tokens per CTA: 32 when that still fills the SMs, fewer for few tokens.
   a.tok = 32;
@@ -1150,47 +1521,62 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
   char* base = static_cast<char*>(ws);
   LossParams base_p;
   common_params(base_p, c, pl, base, status, timeout_ns);
-  base_p.dl = reinterpret_cast<uint16_t*>(base + pl.dl);
-  base_p.ldl = pl.piece;
-  base_p.acc = want_dx ? reinterpret_cast<float*>(base + pl.acc) : nullptr;
   base_p.dloss = dloss;
-  for (int r = 0; r < c.R; ++r) {
-    base_p.lse[r] = lse[r];
-    base_p.out[r] = want_dw ? dW[r] : nullptr;
-  }
-  const int64_t Vs = c.V / c.R;
-  const int cg_dl = choose_cg(c.opts, c.T, cdiv(c.T, kBM) * c.R * cdiv(std::min(pl.piece, Vs), kBN), sms);
-  const int cg_dx = choose_cg(c.opts, c.T, cdiv(c.T, kBM) * cdiv(c.D, kBN) * pl.splits, sms);
-  const int cg_dw = choose_cg(c.opts, std::min(pl.piece, Vs),
-                              cdiv(std::min(pl.piece, Vs), kBM) * cdiv(c.D, kBN) * c.R, sms);
+  for (int r = 0; r < c.R; ++r) base_p.lse[r] = lse[r];
+  const int64_t Vs = c.V / c.R, rows = std::min(pl.piece, Vs);
   uint64_t launches = 0;
   if (c.K > 0) {
     if (launch_teacher(c, pl, base, status) != cudaSuccess) return FCC_ERR_CUDA;
     ++launches;
   }
-  LossParams p_dl = base_p;
-  if ((s = logit_maps(p_dl, c, cg_dl)) != FCC_OK) return s;
-  LossParams p_dx = base_p, p_dw = base_p;
+  LossParams p_dl = base_p, p_dx = base_p, p_dw = base_p;
+  if ((s = logit_maps(p_dl, c, pl)) != FCC_OK) return s;
+  // dX tiles: a CTA pair each when the tokens fill more than half of one.
+  const int cg_dx = c.opts != nullptr && c.opts->cta_pair != 0 && sms >= 2 ? c.opts->cta_pair
+                    : (c.T > kBM && sms >= 2 ? 2 : 1);
+  const int cg_dw = choose_cg(c.opts, rows, cdiv(rows, kBM) * cdiv(c.D, kBN) * c.R, sms);
+  if (want_dx) {
+    p_dx.tiles_m = static_cast<int>(cdiv(c.T, kBM * cg_dx));
+    p_dx.tiles_n = static_cast<int>(cdiv(c.D, kBN));
+    const int64_t tiles = static_cast<int64_t>(p_dx.tiles_m) * p_dx.tiles_n;
+    if (tiles > (1ll << 24)) return FCC_ERR_INVALID;
+    const int slots = slots_of(cg_dx, sms);
+    p_dx.num_tiles = static_cast<int>(tiles);
+    p_dx.full_tiles = p_dx.num_tiles / slots * slots;
+    p_dx.shares = plan_shares(p_dx.num_tiles - p_dx.full_tiles,
+                              static_cast<int>(c.R * cdiv(rows, kBK)), slots);
+    const size_t blocks = static_cast<size_t>(p_dx.shares.tiles) * (p_dx.shares.max_parts - 1);
+    if (blocks * cg_dx * (kBM * kBN * 4) > pl.total - pl.parts) return FCC_ERR_INVALID;
+    p_dx.acc = reinterpret_cast<float*>(base + pl.acc);
+    p_dx.parts = reinterpret_cast<float*>(base + pl.parts);
+  }
   for (int r = 0; r < c.R; ++r) {
     // W and X again, MN-major boxes of 64 rows
     if ((s = internal_encode_map(&p_dx.mapB[r], c.W[r], Vs, c.D, c.D, kBK)) != FCC_OK) return s;
-    if ((s = internal_encode_map(&p_dw.mapB[r], c.X[r], c.T, c.D, c.D, kBK)) != FCC_OK) return s;
+    if ((s = internal_encode_map(&p_dw.mapB[r], c.X[r], c.T, c.D, c.D, base_p.k_rows)) != FCC_OK)
+      return s;
+    if (want_dw &&
+        (s = internal_encode_map(&p_dw.mapO[r], dW[r], Vs, c.D, c.D, 32)) != FCC_OK)
+      return s;
   }
   for (int64_t v0 = 0; v0 < Vs; v0 += pl.piece) {
     const int vn = static_cast<int>(std::min(pl.piece, Vs - v0));
     for (LossParams* p : {&p_dl, &p_dx, &p_dw}) {
       p->v0 = static_cast<int>(v0);
       p->vn = vn;
+      p->piece = static_cast<int>(v0 / pl.piece);
     }
     // dl holds vn valid columns: the maps end there (reads past them give zeros)
     if (v0 == 0 || v0 + vn == Vs) {
       for (int r = 0; r < c.R; ++r) {
-        const uint16_t* d = base_p.dl + static_cast<size_t>(r) * c.T * pl.piece;
-        if ((s = internal_encode_map(&p_dx.mapA[r], d, c.T, vn, pl.piece, kBM)) != FCC_OK) return s;
-        if ((s = internal_encode_map(&p_dw.mapA[r], d, c.T, vn, pl.piece, kBK)) != FCC_OK) return s;
+        const char* d = base + pl.dl + static_cast<size_t>(r) * c.T * pl.piece * 2;
+        if ((s = internal_encode_map(&p_dl.mapO[r], d, c.T, vn, pl.piece, 32)) != FCC_OK ||
+            (s = internal_encode_map(&p_dx.mapA[r], d, c.T, vn, pl.piece, base_p.a_rows)) != FCC_OK ||
+            (s = internal_encode_map(&p_dw.mapA[r], d, c.T, vn, pl.piece, base_p.k_rows)) != FCC_OK)
+          return s;
       }
     }
-    if (launch_loss_gemm<LK_DL>(p_dl, cg_dl, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
+    if (launch_loss_gemm<LK_DL>(p_dl, pl.cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
     ++launches;
     if (want_dx) {
       p_dx.first = v0 == 0 ? 1 : 0;
@@ -1205,12 +1591,19 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
   if (want_dx) {
     FinishArgs f;
     std::memset(&f, 0, sizeof(f));
-    f.acc = base_p.acc;
+    f.acc = p_dx.acc;
+    f.parts = p_dx.parts;
     for (int r = 0; r < c.R; ++r) f.out[r] = dX[r];
-    f.n = c.T * c.D;
-    f.splits = pl.splits;
+    f.T = p_dx.T;
+    f.D = p_dx.D;
     f.R = c.R;
-    const int64_t blocks = std::min<int64_t>(cdiv(f.n / 8, 256), static_cast<int64_t>(sms) * 8);
+    f.tile_m = kBM * cg_dx;
+    f.tiles_m = p_dx.tiles_m;
+    f.tiles_n = p_dx.tiles_n;
+    f.group_m = p_dx.group_m;
+    f.full_tiles = p_dx.full_tiles;
+    f.shares = p_dx.shares;
+    const int blocks = p_dx.num_tiles * (f.tile_m / kFinRows);
     if (launch_pdl(dx_finish_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.st, 1u,
                    f) != cudaSuccess)
       return FCC_ERR_CUDA;

@@ -98,6 +98,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 
+// The same, letting the hardware suspend the thread for up to `ns` before it
+// answers: a warp that waits long issues next to nothing meanwhile.
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded waiting.  `abort_flag` lives in shared memory and is raised by the
 // first thread of the CTA that times out, so the other roles stop waiting too.
 struct Waiter {
@@ -124,6 +138,22 @@ struct Waiter {
           fail();
           return false;
         }
+      }
+    }
+  }
+
+  // wait(), suspended for up to kSuspendNs at a time.  On a part that runs at
+  // its power limit, what the waiting warps do not issue the tensor cores get.
+  static constexpr uint32_t kSuspendNs = 20000;
+  __device__ __forceinline__ bool wait_suspended(uint64_t* bar, uint32_t parity) const {
+    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
+    const uint64_t t0 = globaltimer();
+    while (true) {
+      if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
+      if (*abort_flag) return false;
+      if (globaltimer() - t0 > timeout_ns) {
+        fail();
+        return false;
       }
     }
   }
@@ -391,6 +421,35 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn, b
          | (static_cast<uint32_t>(b_mn) << 16)       // B major
          | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// 2-D tiled store shared -> global as one bulk group's operation: elements past
+// the tensor's end are not written.  The source is written by generic stores,
+// then fence_proxy_async_smem(), before the issuing thread reads it here.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until this thread's bulk stores have read their sources / are complete.
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// 1 / x by the hardware's approximate reciprocal (PTX rcp.approx.ftz.f32,
+// relative error about 2^-23; 1 / inf = 0).
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // ------------------------------------------------------------- TMA gather4
