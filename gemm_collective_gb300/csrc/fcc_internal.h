@@ -253,9 +253,10 @@ fcc_status internal_prepare(const fcc_opts* o, size_t ws_bytes, void** ws, int**
 fcc_status internal_make_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols,
                              uint32_t box_rows);
 // The same over rows `ld` elements apart (ld % 8 == 0), encoded anew on every
-// call: cols may be any number, and reads past it give zeros.
+// call: cols may be any number, and reads past it give zeros.  A box of 64
+// columns has the 128-byte swizzle, one of 32 the 64-byte swizzle.
 fcc_status internal_encode_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols,
-                               int64_t ld, uint32_t box_rows);
+                               int64_t ld, uint32_t box_rows, uint32_t box_cols = 64);
 // A side stream and n <= 8 events of the current device (after internal_prepare).
 fcc_status internal_side_stream(cudaStream_t* side, cudaEvent_t* ev, int n);
 // The device's side streams 0..nside-1 (nside <= 4) and events 0..nev-1

@@ -33,6 +33,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "fcc.h"
 #include "fcc_internal.h"
@@ -50,23 +51,24 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 enum LossKind : int {
-  LK_FWD = 0,  // logits -> softmax statistics and target logits
-  LK_DL = 1,   // logits -> dl of one vocabulary piece
-  LK_DX = 2,   // dX (+)= dl W over the ranks' pieces
-  LK_DW = 3,   // dW rows of the piece = dl^T X
+  LK_FWD = 0,   // logits -> softmax statistics and target logits
+  LK_DL = 1,    // logits -> dl of one vocabulary piece
+  LK_GRAD = 2,  // dX (+)= dl W over the ranks' pieces, and dW rows of the piece = dl^T X
 };
 // Operand layouts: X and W rows are contiguous along D, dl rows along the
-// vocabulary.  Logits contract D (both K-major); dX contracts the vocabulary
-// (dl K-major, W MN-major); dW contracts the tokens (both MN-major).
-constexpr bool a_mn(int kind) { return kind == LK_DW; }
-constexpr bool b_mn(int kind) { return kind == LK_DX || kind == LK_DW; }
+// vocabulary.  Logits contract D (both operands K-major); dX contracts the
+// vocabulary (dl K-major, W MN-major); dW contracts the tokens (dl and X both
+// MN-major).
+constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
 // Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
 constexpr int threads_of(int kind) { return 64 + 32 * kEpiWarps + (kind == LK_FWD ? 64 : 0); }
-constexpr uint32_t kOutBytes = 32 * 128;  // a warp's staging: 32 rows x 64 bf16, 128-byte swizzle
+// A warp's staging: 32 rows x 64 bf16 (dW: one block, 128-byte swizzle; dl:
+// two of 32 columns, 64-byte swizzle, so that a tile may end after either).
+constexpr uint32_t kOutBytes = 32 * 128;
 // bf16 results leave by TMA stores from shared memory.
-constexpr bool stages_out(int kind) { return kind == LK_DL || kind == LK_DW; }
+constexpr bool stages_out(int kind) { return kind != LK_FWD; }
 
 template <int KIND, int CG>
 struct Cfg {
@@ -77,8 +79,8 @@ struct Cfg {
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kOut = stages_out(KIND) ? kEpiWarps * kOutBytes : 0;
   // Instruction descriptor of a tile `width` columns wide.
-  __device__ static constexpr uint32_t idesc(int width) {
-    return ptx::idesc_bf16_f32(kTileM, width, a_mn(KIND), b_mn(KIND));
+  __device__ static constexpr uint32_t idesc(int width, bool a_mn) {
+    return ptx::idesc_bf16_f32(kTileM, width, a_mn, b_mn(KIND));
   }
   static constexpr int kSmem = 1024 + kStages * static_cast<int>(kStageBytes) +
                                static_cast<int>(kOut) + (2 * kStages + 5) * 8 + 16 +
@@ -118,16 +120,18 @@ struct Shares {
 struct LossParams {
   CUtensorMap mapA[FCC_MAX_RANKS];
   CUtensorMap mapB[FCC_MAX_RANKS];
-  CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl piece, DW: dW; box 32 rows x 64
+  CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl piece, box 32 rows x 32; GRAD: dW, 32 x 64
+  CUtensorMap mapA2[FCC_MAX_RANKS];  // GRAD: mapA, mapB of dX are dl and W, of dW these:
+  CUtensorMap mapB2[FCC_MAX_RANKS];  // dl and X in boxes of k_rows tokens
   int R, T, D;
   int Vs;                  // vocabulary rows per rank
   int v0, vn;              // this piece: rows [v0, v0 + vn) of every rank (FWD: 0, Vs)
-  int width;               // tile columns (FWD, DL; a multiple of 16), else kBN
-  int tiles_m, tiles_n;    // tiles of one rank (DX: of all)
-  int full_tiles;          // tiles run whole, round-robin (DX: the others are shared, see Work)
-  int num_tiles;
-  int k_iters;             // 64-deep K steps of a whole tile
-  int kb_per_rank;         // DX: K steps per rank
+  int width;               // tile columns (FWD, DL: a multiple of 32), else kBN
+  int tiles_m, tiles_n;    // tiles of one rank (GRAD: of dX, over all)
+  int full_tiles;          // tiles run whole, round-robin (dX: the others are shared, see Shares)
+  int k_iters;             // 64-deep K steps of a whole tile (GRAD: of dX)
+  int kb_per_rank;         // dX: K steps per rank
+  int dw_tiles_m, dw_tiles;  // dW: row tiles of one rank, tiles over all
   Shares shares;           // DX: the tiles past full_tiles, by the first piece's K steps
   int a_rows;              // rows of an A box (K-major A: fewer than 128 when T is)
   int k_rows;              // DW: tokens of a K step (fewer than 64 when T is)
@@ -156,7 +160,7 @@ struct LossParams {
   // DL
   const float* lse[FCC_MAX_RANKS];
   const float* dloss;
-  // DX: f32 sums [T][D] of whole tiles and of shared tiles' first parts, and
+  // dX: f32 sums [T][D] of whole tiles and of shared tiles' first parts, and
   // one [rows][kBN] block for each further part; first = 1: overwrite, else add
   float* acc;
   float* parts;
@@ -168,8 +172,9 @@ struct LossParams {
 struct Tile {
   int rank, mt, nt;
   int it_lo, it_hi;  // K steps
-  int part;          // DX: which part of a shared tile (0: goes to acc)
-  int shared;        // DX: index among the shared tiles
+  int part;          // dX: which part of a shared tile (0: goes to acc)
+  int shared;        // dX: index among the shared tiles
+  bool dw;           // GRAD: a tile of dW, else of dX
 };
 
 __device__ __forceinline__ void raster(int t, int tiles_m, int tiles_n, int group, int& mt,
@@ -189,31 +194,42 @@ __device__ __forceinline__ Tile tile_of(const LossParams& p, int t) {
   tl.rank = 0;
   tl.part = 0;
   tl.shared = 0;
+  tl.dw = false;
   tl.it_lo = 0;
   tl.it_hi = p.k_iters;
   if constexpr (KIND == LK_FWD || KIND == LK_DL) {
     raster(t, p.tiles_m, p.R * p.tiles_n, p.group_m, tl.mt, tl.nt);
     tl.rank = tl.nt / p.tiles_n;
     tl.nt -= tl.rank * p.tiles_n;
-  } else if constexpr (KIND == LK_DX) {
-    raster(t, p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
   } else {
-    raster(t, p.R * p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
-    tl.rank = tl.mt / p.tiles_m;
-    tl.mt -= tl.rank * p.tiles_m;
+    raster(t, p.tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
   }
   return tl;
 }
 
-// What one CTA (pair) works on: whole tiles round-robin, then (dX) its share.
+__device__ __forceinline__ Tile dw_tile_of(const LossParams& p, int t) {
+  Tile tl;
+  tl.part = 0;
+  tl.shared = 0;
+  tl.dw = true;
+  tl.it_lo = 0;
+  tl.it_hi = (p.T + kBK - 1) / kBK;
+  raster(t, p.R * p.dw_tiles_m, p.tiles_n, p.group_m, tl.mt, tl.nt);
+  tl.rank = tl.mt / p.dw_tiles_m;
+  tl.mt -= tl.rank * p.dw_tiles_m;
+  return tl;
+}
+
+// What one CTA (pair) works on: whole tiles round-robin; GRAD: whole dX tiles,
+// its share of the others, and dW tiles round-robin.
 template <int KIND>
 struct Work {
   const LossParams& p;
-  int t, npairs, pair;
+  int t, tw, npairs, pair;
   long long cur, end;  // of the tails (a helper); cur = -1: a group's share to do
   __device__ __forceinline__ Work(const LossParams& p_, int pair_, int npairs_)
-      : p(p_), t(pair_), npairs(npairs_), pair(pair_), cur(0), end(0) {
-    if constexpr (KIND == LK_DX) {
+      : p(p_), t(pair_), tw(pair_), npairs(npairs_), pair(pair_), cur(0), end(0) {
+    if constexpr (KIND == LK_GRAD) {
       const Shares& s = p.shares;
       const int h = pair - s.groups * s.tiles;
       if (s.tiles > 0 && h < 0) {
@@ -224,13 +240,19 @@ struct Work {
       }
     }
   }
-  __device__ __forceinline__ bool next(Tile& tl) {
+  __device__ __forceinline__ bool next_dw(Tile& tl) {
+    if (tw >= p.dw_tiles) return false;
+    tl = dw_tile_of(p, tw);
+    tw += npairs;
+    return true;
+  }
+  __device__ __forceinline__ bool next_dx(Tile& tl) {
     if (t < p.full_tiles) {
       tl = tile_of<KIND>(p, t);
       t += npairs;
       return true;
     }
-    if constexpr (KIND == LK_DX) {
+    if constexpr (KIND == LK_GRAD) {
       const Shares& s = p.shares;
       int i, lo, n, part;
       if (cur < 0) {
@@ -260,10 +282,15 @@ struct Work {
     }
     return false;
   }
+  __device__ __forceinline__ bool next(Tile& tl) {
+    return next_dx(tl) || (KIND == LK_GRAD && next_dw(tl));
+  }
 };
 
-// 32 f32 columns of each lane's row as bf16 into the warp's staging block:
-// half 0 / 1 of its 64 columns (16-byte pieces, 128-byte swizzle).
+// 32 f32 columns of each lane's row as bf16 into the warp's staging: half 0 / 1
+// of 64 columns (WIDE, 128-byte swizzle) or a block of 32 (64-byte swizzle), in
+// 16-byte pieces without bank conflicts.
+template <bool WIDE>
 __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
                                            const uint32_t (&v)[32]) {
 #pragma unroll
@@ -273,7 +300,9 @@ __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
     w.y = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
     w.z = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
     w.w = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
-    *reinterpret_cast<uint4*>(buf + lane * 128 + (((half * 4 + g) ^ (lane & 7)) << 4)) = w;
+    const int at = WIDE ? lane * 128 + (((half * 4 + g) ^ (lane & 7)) << 4)
+                        : half * 2048 + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4);
+    *reinterpret_cast<uint4*>(buf + at) = w;
   }
 }
 
@@ -429,15 +458,17 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       uint32_t issued = 0, last_parity = 0;
       // (rows of A past a short box stay as they are: they only make rows of
       // the result that nothing reads)
-      const uint32_t stage_bytes =
-          a_mn(KIND) ? static_cast<uint32_t>(kBM + C::kBNcta) * p.k_rows * 2
-                     : static_cast<uint32_t>(p.a_rows) * kBK * 2 + static_cast<uint32_t>(bn_cta) * kBK * 2;
+      const uint32_t bytes_x =
+          static_cast<uint32_t>(p.a_rows) * kBK * 2 + static_cast<uint32_t>(bn_cta) * kBK * 2;
+      const uint32_t bytes_w = static_cast<uint32_t>(kBM + C::kBNcta) * p.k_rows * 2;
       bool ok = true;
       while (ok && work.next(tl)) {
         const int m0 = tl.mt * TM + static_cast<int>(cta) * kBM;  // this CTA's A rows
         const int n0 = tl.nt * (bn_cta * CG) + static_cast<int>(cta) * bn_cta;  // and B columns
+        const bool dw = KIND == LK_GRAD && tl.dw;
+        const uint32_t stage_bytes = dw ? bytes_w : bytes_x;
         int r = tl.rank, kb = tl.it_lo;
-        if constexpr (KIND == LK_DX) {
+        if (KIND == LK_GRAD && !dw) {
           r = tl.it_lo / p.kb_per_rank;
           kb = tl.it_lo - r * p.kb_per_rank;
         }
@@ -446,8 +477,8 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             ok = false;
             break;
           }
-          const CUtensorMap* ma = &p.mapA[r];
-          const CUtensorMap* mb = &p.mapB[r];
+          const CUtensorMap* ma = dw ? &p.mapA2[r] : &p.mapA[r];
+          const CUtensorMap* mb = dw ? &p.mapB2[r] : &p.mapB[r];
           uint8_t* a_dst = sA + stage * kABytes;
           uint8_t* b_dst = sB + stage * C::kBBytes;
           uint32_t bar = 0;
@@ -463,15 +494,15 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             else
               ptx::tma_load_2d(dst, map, &full[stage], x, y);
           };
-          if constexpr (a_mn(KIND)) {
+          if (dw) {
             for (int i = 0; i < kBM / 64; ++i)
               load(a_dst + i * kBoxBytes, ma, m0 + 64 * i, kb * kBK);
           } else {
             load(a_dst, ma, kb * kBK, m0);
           }
           if constexpr (b_mn(KIND)) {
-            // W rows of the piece (DX) or tokens (DW) down, D across
-            const int y = (KIND == LK_DX ? p.v0 : 0) + kb * kBK;
+            // W rows of the piece (dX) or tokens (dW) down, D across
+            const int y = (dw ? 0 : p.v0) + kb * kBK;
             for (int i = 0; i < C::kBNcta / 64; ++i)
               load(b_dst + i * kBoxBytes, mb, n0 + 64 * i, y);
           } else {
@@ -484,7 +515,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             phase ^= 1u;
           }
           ++kb;
-          if (KIND == LK_DX && kb == p.kb_per_rank) {
+          if (KIND == LK_GRAD && !dw && kb == p.kb_per_rank) {
             kb = 0;
             ++r;
           }
@@ -503,49 +534,54 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       uint32_t stage = 0, phase = 0;
       uint32_t acc = 0, acc_phase = 0;
       bool any = false, ok = true;
-      const uint32_t idesc = C::idesc(bn_cta * CG);
       while (ok && work.next(tl)) {
         if (!W.wait_suspended(&tempty[acc], acc_phase ^ 1u)) break;
         ptx::tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kBN;
-        for (int it = tl.it_lo; it < tl.it_hi; ++it) {
-          if (!W.wait_suspended(&full[stage], phase)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const uint32_t a_addr = ptx::smem_addr(sA + stage * kABytes);
-          const uint32_t b_addr = ptx::smem_addr(sB + stage * C::kBBytes);
-          // (DW: no MMA for 16 rows past the last token, which a short box
-          // does not fill)
-          const int steps = KIND == LK_DW ? min(kBK, p.T - it * kBK) : kBK;
+        // The tile's K steps, for one layout of A (dW: dl MN-major, else K-major).
+        auto k_loop = [&](auto mn) {
+          constexpr bool kDw = decltype(mn)::value;
+          const uint32_t idesc = C::idesc(bn_cta * CG, kDw);
+          for (int it = tl.it_lo; it < tl.it_hi; ++it) {
+            if (!W.wait_suspended(&full[stage], phase)) return false;
+            ptx::tc_fence_after();
+            const uint32_t a_addr = ptx::smem_addr(sA + stage * kABytes);
+            const uint32_t b_addr = ptx::smem_addr(sB + stage * C::kBBytes);
+            // (dW: no MMA for 16 rows past the last token, which a short box
+            // does not fill)
+            const int steps = kDw ? min(kBK, p.T - it * kBK) : kBK;
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            // K-major: 16 elements (32 B) on inside the swizzled row;
-            // MN-major: 16 k rows (2 KiB) on, 64-wide boxes 8 KiB apart.
-            const uint64_t ad = a_mn(KIND)
-                                    ? ptx::smem_desc_sw128(a_addr + kk * 2048, kBoxBytes, 1024)
-                                    : ptx::smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-            const uint64_t bd = b_mn(KIND)
-                                    ? ptx::smem_desc_sw128(b_addr + kk * 2048, kBoxBytes, 1024)
-                                    : ptx::smem_desc_sw128(b_addr + kk * 32, 16, 1024);
-            const uint32_t accum = (it > tl.it_lo || kk > 0) ? 1u : 0u;
-            if (KIND == LK_DW && 16 * kk >= steps) continue;
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              // K-major: 16 elements (32 B) on inside the swizzled row;
+              // MN-major: 16 k rows (2 KiB) on, 64-wide boxes 8 KiB apart.
+              const uint64_t ad = kDw ? ptx::smem_desc_sw128(a_addr + kk * 2048, kBoxBytes, 1024)
+                                      : ptx::smem_desc_sw128(a_addr + kk * 32, 16, 1024);
+              const uint64_t bd = b_mn(KIND)
+                                      ? ptx::smem_desc_sw128(b_addr + kk * 2048, kBoxBytes, 1024)
+                                      : ptx::smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+              const uint32_t accum = (it > tl.it_lo || kk > 0) ? 1u : 0u;
+              if (kDw && 16 * kk >= steps) continue;
+              if constexpr (kPair)
+                ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
+              else
+                ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
+            }
             if constexpr (kPair)
-              ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
+              ptx::mma_commit_pair_arrive_ctas(&empty[stage], 0x3);
             else
-              ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
+              ptx::mma_commit(&empty[stage]);
+            any = true;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          if constexpr (kPair)
-            ptx::mma_commit_pair_arrive_ctas(&empty[stage], 0x3);
-          else
-            ptx::mma_commit(&empty[stage]);
-          any = true;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+          return true;
+        };
+        if (KIND == LK_GRAD && tl.dw)
+          ok = k_loop(std::true_type{});
+        else
+          ok = k_loop(std::false_type{});
         if (!ok) break;
         if constexpr (kPair)
           ptx::mma_commit_pair_arrive_ctas(&tfull[acc], 0x3);
@@ -589,12 +625,13 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           ptx::mbar_arrive(&tempty[acc]);
       }
     };
-    // The staged 64 columns to (x, y) of a map, by one lane.
-    auto store_out = [&](const CUtensorMap* map, int x, int y) {
+    // The staged columns to (x, y) of a map, by one lane: 64 of dW, or `blocks`
+    // blocks of 32 of dl.
+    auto store_out = [&](const CUtensorMap* map, int x, int y, int blocks) {
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ptx::tma_store_2d(map, buf, x, y);
+        for (int b = 0; b < blocks; ++b) ptx::tma_store_2d(map, buf + 2048 * b, x + 32 * b, y);
         ptx::bulk_commit();
       }
     };
@@ -735,10 +772,10 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           if (nc > 32) chunk(v[1], c + 32, nc - 32);
           if constexpr (KIND == LK_DL) {
             buf_free();
-            stage_bf16(buf, lane, 0, v[0]);
-            stage_bf16(buf, lane, 1, v[1]);
+            stage_bf16<false>(buf, lane, 0, v[0]);
+            if (nc > 32) stage_bf16<false>(buf, lane, 1, v[1]);
             // (columns past the piece's end are not stored)
-            if (row0 < p.T) store_out(&p.mapO[tl.rank], col0 + c, row0);
+            if (row0 < p.T) store_out(&p.mapO[tl.rank], col0 + c, row0, nc > 32 ? 2 : 1);
           }
         }
         release_acc();
@@ -758,7 +795,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             if (p.part_sum != nullptr) p.part_sum[o] = lsum + stat[2];
           }
         }
-      } else if constexpr (KIND == LK_DX) {
+      } else if (!tl.dw) {
         const bool row_ok = row < p.T;
         const int col0 = tl.nt * kBN;
         const int width = min(kBN, p.D - col0);
@@ -782,15 +819,13 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               float4 x = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
                                      __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
               if (none) x = make_float4(0.f, 0.f, 0.f, 0.f);
-              float4* o = reinterpret_cast<float4*>(dst + c + 4 * g);
-              if (!p.first) {
-                const float4 y = *o;
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
-              }
-              *o = x;
+              // (one CTA adds to an element once per piece, so the sum's order
+              // is the pieces'; the additions need no answer)
+              float* o = dst + c + 4 * g;
+              if (p.first)
+                *reinterpret_cast<float4*>(o) = x;
+              else
+                ptx::red_add_v4_f32(o, x.x, x.y, x.z, x.w);
             }
           }
           __syncwarp();
@@ -807,11 +842,11 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
           ptx::tmem_ld_wait();
           buf_free();
-          stage_bf16(buf, lane, 0, v[0]);
-          stage_bf16(buf, lane, 1, v[1]);
+          stage_bf16<true>(buf, lane, 0, v[0]);
+          stage_bf16<true>(buf, lane, 1, v[1]);
           // (columns past D, and rows past the piece, which are past the
           // shard, are not stored)
-          if (row0 < p.vn) store_out(&p.mapO[tl.rank], col0 + c, p.v0 + row0);
+          if (row0 < p.vn) store_out(&p.mapO[tl.rank], col0 + c, p.v0 + row0, 1);
         }
         release_acc();
       }
@@ -1162,14 +1197,14 @@ int choose_cg(const fcc_opts* o, int64_t rows, int64_t single_tiles, int sms) {
   return rows > kBM && single_tiles > sms ? 2 : 1;
 }
 
-// Width of the logit tiles: the widest of the fewest (rounds of tiles x
-// width), counting 16 columns per tile for what does not depend on the width.
-// One token on 32000 words: 143 tiles of 224 columns in one round, not 125 of
-// 256.  `step`: 16, or 64 where whole 64-column blocks are stored.
-int choose_width(int R, int64_t tiles_m, int64_t vn, int slots, int step) {
+// Width of the logit tiles, a multiple of 32: the widest of the least (rounds
+// of tiles x width), counting 16 columns per tile for what does not depend on
+// the width.  One token on 32000 words: 143 tiles of 224 columns in one round,
+// not 125 of 256; a few thousand words spread over all SMs in tiles of 32.
+int choose_width(int R, int64_t tiles_m, int64_t vn, int slots) {
   int best = kBN;
   int64_t least = INT64_MAX;
-  for (int w = kBN; w >= kBN / 2; w -= step) {
+  for (int w = kBN; w >= 32; w -= 32) {
     const int64_t cost = cdiv(tiles_m * R * cdiv(vn, w), slots) * (w + 16);
     if (cost < least) {
       least = cost;
@@ -1201,33 +1236,24 @@ Shares plan_shares(int rest, int k, int slots) {
 
 int slots_of(int cg, int sms) { return std::max(1, std::min(sms / cg, gemm_max_clusters(cg))); }
 
-// One of the four products: tile counts for the shape, then the launch over
-// at most `sms` CTAs.
+// One of the products over at most `sms` CTAs.  The logit tiles are counted
+// here; the gradients' tiles are planned by the caller.
 template <int KIND>
 cudaError_t launch_loss_gemm(LossParams& p, int cg, int sms, cudaStream_t st) {
   const int64_t tm = static_cast<int64_t>(kBM) * cg;
   const int slots = slots_of(cg, sms);
-  int64_t tiles = 0;
-  if (KIND == LK_FWD || KIND == LK_DL) {
+  int64_t busy = 0;
+  if (KIND != LK_GRAD) {
     p.tiles_m = static_cast<int>(cdiv(p.T, tm));
     p.tiles_n = static_cast<int>(cdiv(p.vn, p.width));
     p.k_iters = static_cast<int>(cdiv(p.D, kBK));
-    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
-  } else if (KIND == LK_DX) {
-    p.kb_per_rank = static_cast<int>(cdiv(p.vn, kBK));
-    p.k_iters = p.R * p.kb_per_rank;
-    tiles = p.num_tiles;  // (planned by the caller, with the shares)
+    busy = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
+    if (busy > (1ll << 30)) return cudaErrorInvalidValue;
+    p.full_tiles = static_cast<int>(busy);
   } else {
-    p.tiles_m = static_cast<int>(cdiv(p.vn, tm));
-    p.tiles_n = static_cast<int>(cdiv(p.D, kBN));
-    p.k_iters = static_cast<int>(cdiv(p.T, kBK));
-    tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.R;
+    busy = std::max({p.full_tiles, p.shares.groups * p.shares.tiles + p.shares.helpers, p.dw_tiles});
   }
-  if (tiles > (1ll << 30)) return cudaErrorInvalidValue;
-  p.num_tiles = static_cast<int>(tiles);
-  if (KIND != LK_DX) p.full_tiles = p.num_tiles;
-  const int shared = p.shares.groups * p.shares.tiles + p.shares.helpers;
-  const int grid = cg * std::max(std::min(slots, p.full_tiles), shared);
+  const int grid = cg * static_cast<int>(std::min<int64_t>(slots, busy));
   return cg == 2 ? launch_kind<KIND, 2>(p, grid, st) : launch_kind<KIND, 1>(p, grid, st);
 }
 
@@ -1323,7 +1349,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     p.npieces = static_cast<int>(cdiv(Vs, p.piece));
   }
   p.cg = choose_cg(o, T, cdiv(T, kBM) * R * cdiv(rows, kBN), sms);
-  p.width = choose_width(R, cdiv(T, kBM * p.cg), rows, std::max(1, sms / p.cg), grad ? 64 : 16);
+  p.width = choose_width(R, cdiv(T, kBM * p.cg), rows, std::max(1, sms / p.cg));
   p.piece_tiles = static_cast<int>(cdiv(rows, p.width));
   if (K > 0) {
     p.hit_start = off;
@@ -1529,81 +1555,80 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     if (launch_teacher(c, pl, base, status) != cudaSuccess) return FCC_ERR_CUDA;
     ++launches;
   }
-  LossParams p_dl = base_p, p_dx = base_p, p_dw = base_p;
+  LossParams p_dl = base_p, p = base_p;
   if ((s = logit_maps(p_dl, c, pl)) != FCC_OK) return s;
-  // dX tiles: a CTA pair each when the tokens fill more than half of one.
-  const int cg_dx = c.opts != nullptr && c.opts->cta_pair != 0 && sms >= 2 ? c.opts->cta_pair
-                    : (c.T > kBM && sms >= 2 ? 2 : 1);
-  const int cg_dw = choose_cg(c.opts, rows, cdiv(rows, kBM) * cdiv(c.D, kBN) * c.R, sms);
+  // Gradient tiles: a CTA pair each when there are more than 128 tokens.
+  const int cg = sms < 2 ? 1
+                 : c.opts != nullptr && c.opts->cta_pair != 0 ? c.opts->cta_pair
+                 : c.T > kBM ? 2 : 1;
+  const int slots = slots_of(cg, sms);
+  const int64_t tm = static_cast<int64_t>(kBM) * cg;
+  p.width = kBN;
+  p.tiles_m = static_cast<int>(cdiv(c.T, tm));
+  p.tiles_n = static_cast<int>(cdiv(c.D, kBN));
+  int dx_tiles = 0;
   if (want_dx) {
-    p_dx.tiles_m = static_cast<int>(cdiv(c.T, kBM * cg_dx));
-    p_dx.tiles_n = static_cast<int>(cdiv(c.D, kBN));
-    const int64_t tiles = static_cast<int64_t>(p_dx.tiles_m) * p_dx.tiles_n;
+    const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     if (tiles > (1ll << 24)) return FCC_ERR_INVALID;
-    const int slots = slots_of(cg_dx, sms);
-    p_dx.num_tiles = static_cast<int>(tiles);
-    p_dx.full_tiles = p_dx.num_tiles / slots * slots;
-    p_dx.shares = plan_shares(p_dx.num_tiles - p_dx.full_tiles,
-                              static_cast<int>(c.R * cdiv(rows, kBK)), slots);
-    const size_t blocks = static_cast<size_t>(p_dx.shares.tiles) * (p_dx.shares.max_parts - 1);
-    if (blocks * cg_dx * (kBM * kBN * 4) > pl.total - pl.parts) return FCC_ERR_INVALID;
-    p_dx.acc = reinterpret_cast<float*>(base + pl.acc);
-    p_dx.parts = reinterpret_cast<float*>(base + pl.parts);
+    dx_tiles = static_cast<int>(tiles);
+    p.full_tiles = dx_tiles / slots * slots;
+    p.shares = plan_shares(dx_tiles - p.full_tiles, static_cast<int>(c.R * cdiv(rows, kBK)), slots);
+    const size_t blocks = static_cast<size_t>(p.shares.tiles) * (p.shares.max_parts - 1);
+    if (blocks * cg * (kBM * kBN * 4) > pl.total - pl.parts) return FCC_ERR_INVALID;
+    p.acc = reinterpret_cast<float*>(base + pl.acc);
+    p.parts = reinterpret_cast<float*>(base + pl.parts);
   }
+  if (want_dw && cdiv(rows, tm) * c.R * p.tiles_n > (1ll << 30)) return FCC_ERR_INVALID;
   for (int r = 0; r < c.R; ++r) {
-    // W and X again, MN-major boxes of 64 rows
-    if ((s = internal_encode_map(&p_dx.mapB[r], c.W[r], Vs, c.D, c.D, kBK)) != FCC_OK) return s;
-    if ((s = internal_encode_map(&p_dw.mapB[r], c.X[r], c.T, c.D, c.D, base_p.k_rows)) != FCC_OK)
+    // W and X again, MN-major boxes
+    if ((s = internal_encode_map(&p.mapB[r], c.W[r], Vs, c.D, c.D, kBK)) != FCC_OK ||
+        (s = internal_encode_map(&p.mapB2[r], c.X[r], c.T, c.D, c.D, p.k_rows)) != FCC_OK)
       return s;
-    if (want_dw &&
-        (s = internal_encode_map(&p_dw.mapO[r], dW[r], Vs, c.D, c.D, 32)) != FCC_OK)
+    if (want_dw && (s = internal_encode_map(&p.mapO[r], dW[r], Vs, c.D, c.D, 32)) != FCC_OK)
       return s;
   }
   for (int64_t v0 = 0; v0 < Vs; v0 += pl.piece) {
     const int vn = static_cast<int>(std::min(pl.piece, Vs - v0));
-    for (LossParams* p : {&p_dl, &p_dx, &p_dw}) {
-      p->v0 = static_cast<int>(v0);
-      p->vn = vn;
-      p->piece = static_cast<int>(v0 / pl.piece);
-    }
+    p_dl.v0 = p.v0 = static_cast<int>(v0);
+    p_dl.vn = p.vn = vn;
+    p_dl.piece = static_cast<int>(v0 / pl.piece);
     // dl holds vn valid columns: the maps end there (reads past them give zeros)
     if (v0 == 0 || v0 + vn == Vs) {
       for (int r = 0; r < c.R; ++r) {
         const char* d = base + pl.dl + static_cast<size_t>(r) * c.T * pl.piece * 2;
-        if ((s = internal_encode_map(&p_dl.mapO[r], d, c.T, vn, pl.piece, 32)) != FCC_OK ||
-            (s = internal_encode_map(&p_dx.mapA[r], d, c.T, vn, pl.piece, base_p.a_rows)) != FCC_OK ||
-            (s = internal_encode_map(&p_dw.mapA[r], d, c.T, vn, pl.piece, base_p.k_rows)) != FCC_OK)
+        if ((s = internal_encode_map(&p_dl.mapO[r], d, c.T, vn, pl.piece, 32, 32)) != FCC_OK ||
+            (s = internal_encode_map(&p.mapA[r], d, c.T, vn, pl.piece, p.a_rows)) != FCC_OK ||
+            (s = internal_encode_map(&p.mapA2[r], d, c.T, vn, pl.piece, p.k_rows)) != FCC_OK)
           return s;
       }
     }
     if (launch_loss_gemm<LK_DL>(p_dl, pl.cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
-    ++launches;
-    if (want_dx) {
-      p_dx.first = v0 == 0 ? 1 : 0;
-      if (launch_loss_gemm<LK_DX>(p_dx, cg_dx, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
-      ++launches;
-    }
+    p.first = v0 == 0 ? 1 : 0;
+    p.kb_per_rank = static_cast<int>(cdiv(vn, kBK));
+    p.k_iters = c.R * p.kb_per_rank;
     if (want_dw) {
-      if (launch_loss_gemm<LK_DW>(p_dw, cg_dw, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
-      ++launches;
+      p.dw_tiles_m = static_cast<int>(cdiv(vn, tm));
+      p.dw_tiles = p.dw_tiles_m * c.R * p.tiles_n;
     }
+    if (launch_loss_gemm<LK_GRAD>(p, cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
+    launches += 2;
   }
   if (want_dx) {
     FinishArgs f;
     std::memset(&f, 0, sizeof(f));
-    f.acc = p_dx.acc;
-    f.parts = p_dx.parts;
+    f.acc = p.acc;
+    f.parts = p.parts;
     for (int r = 0; r < c.R; ++r) f.out[r] = dX[r];
-    f.T = p_dx.T;
-    f.D = p_dx.D;
+    f.T = p.T;
+    f.D = p.D;
     f.R = c.R;
-    f.tile_m = kBM * cg_dx;
-    f.tiles_m = p_dx.tiles_m;
-    f.tiles_n = p_dx.tiles_n;
-    f.group_m = p_dx.group_m;
-    f.full_tiles = p_dx.full_tiles;
-    f.shares = p_dx.shares;
-    const int blocks = p_dx.num_tiles * (f.tile_m / kFinRows);
+    f.tile_m = static_cast<int>(tm);
+    f.tiles_m = p.tiles_m;
+    f.tiles_n = p.tiles_n;
+    f.group_m = p.group_m;
+    f.full_tiles = p.full_tiles;
+    f.shares = p.shares;
+    const int blocks = dx_tiles * (f.tile_m / kFinRows);
     if (launch_pdl(dx_finish_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.st, 1u,
                    f) != cudaSuccess)
       return FCC_ERR_CUDA;
