@@ -55,10 +55,13 @@ enum LossKind : int {
   LK_DL = 1,    // logits -> dl of one vocabulary piece
   LK_GRAD = 2,  // dX (+)= dl W over the ranks' pieces, and dW rows of the piece = dl^T X
 };
-// Operand layouts: X and W rows are contiguous along D, dl rows along the
-// vocabulary.  Logits contract D (both operands K-major); dX contracts the
-// vocabulary (dl K-major, W MN-major); dW contracts the tokens (dl and X both
-// MN-major).
+// Operand layouts: X and W rows are contiguous along D.  dl, the library's own,
+// is kept in panels of 64 vocabulary entries, [panel][token][64], tokens padded
+// to 32 with zeros: every box of dl that a product loads is one contiguous run
+// (row-major over the whole piece, a box's 128-byte rows lie a piece apart, and
+// the tensor cores were busy %DLROW% of dX and dW, against %DLPANEL% this way).
+// Logits contract D (both operands K-major); dX contracts the vocabulary (dl
+// K-major, W MN-major); dW contracts the tokens (dl and X both MN-major).
 constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
@@ -120,12 +123,13 @@ struct Shares {
 struct LossParams {
   CUtensorMap mapA[FCC_MAX_RANKS];
   CUtensorMap mapB[FCC_MAX_RANKS];
-  CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl piece, box 32 rows x 32; GRAD: dW, 32 x 64
+  CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl, box 32 tokens x 32; GRAD: dW, 32 rows x 64
   CUtensorMap mapA2[FCC_MAX_RANKS];  // GRAD: mapA, mapB of dX are dl and W, of dW these:
   CUtensorMap mapB2[FCC_MAX_RANKS];  // dl and X in boxes of k_rows tokens
   int R, T, D;
   int Vs;                  // vocabulary rows per rank
   int v0, vn;              // this piece: rows [v0, v0 + vn) of every rank (FWD: 0, Vs)
+  int tpad;                // rows of a dl panel: the tokens, to a multiple of 32
   int width;               // tile columns (FWD, DL: a multiple of 32), else kBN
   int tiles_m, tiles_n;    // tiles of one rank (GRAD: of dX, over all)
   int full_tiles;          // tiles run whole, round-robin (dX: the others are shared, see Shares)
@@ -455,77 +459,96 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t stage = 0, phase = 0;
-      uint32_t issued = 0, last_parity = 0;
+      int64_t loads = 0;  // stages filled so far
       // (rows of A past a short box stay as they are: they only make rows of
       // the result that nothing reads)
       const uint32_t bytes_x =
           static_cast<uint32_t>(p.a_rows) * kBK * 2 + static_cast<uint32_t>(bn_cta) * kBK * 2;
       const uint32_t bytes_w = static_cast<uint32_t>(kBM + C::kBNcta) * p.k_rows * 2;
+      // (a pair's bytes are counted on the leader's barriers)
+      const uint32_t full0 = kPair ? ptx::mapa(ptx::smem_addr(full), 0) : 0u;
       bool ok = true;
       while (ok && work.next(tl)) {
         const int m0 = tl.mt * TM + static_cast<int>(cta) * kBM;  // this CTA's A rows
         const int n0 = tl.nt * (bn_cta * CG) + static_cast<int>(cta) * bn_cta;  // and B columns
-        const bool dw = KIND == LK_GRAD && tl.dw;
-        const uint32_t stage_bytes = dw ? bytes_w : bytes_x;
-        int r = tl.rank, kb = tl.it_lo;
-        if (KIND == LK_GRAD && !dw) {
-          r = tl.it_lo / p.kb_per_rank;
-          kb = tl.it_lo - r * p.kb_per_rank;
-        }
-        for (int it = tl.it_lo; it < tl.it_hi; ++it) {
-          if (!W.wait_suspended(&empty[stage], phase ^ 1u)) {
-            ok = false;
-            break;
+        // The tile's loads, for one of the two products of GRAD (dW, or dX and
+        // the logits): as little as possible per K step, for one thread issues
+        // them all.
+        auto k_loop = [&](auto w) {
+          constexpr bool kDw = decltype(w)::value;
+          const uint32_t stage_bytes = kDw ? bytes_w : bytes_x;
+          int r = tl.rank, kb = tl.it_lo;
+          if (KIND == LK_GRAD && !kDw) {
+            r = tl.it_lo / p.kb_per_rank;
+            kb = tl.it_lo - r * p.kb_per_rank;
           }
-          const CUtensorMap* ma = dw ? &p.mapA2[r] : &p.mapA[r];
-          const CUtensorMap* mb = dw ? &p.mapB2[r] : &p.mapB[r];
-          uint8_t* a_dst = sA + stage * kABytes;
-          uint8_t* b_dst = sB + stage * C::kBBytes;
-          uint32_t bar = 0;
-          if constexpr (kPair) {
-            bar = ptx::mapa(ptx::smem_addr(&full[stage]), 0);
-            if (cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
-          } else {
-            ptx::mbar_arrive_expect_tx(&full[stage], stage_bytes);
+          const CUtensorMap* ma = kDw ? &p.mapA2[r] : &p.mapA[r];
+          const CUtensorMap* mb = kDw ? &p.mapB2[r] : &p.mapB[r];
+          // A: (x, y) and their steps; dW a second box, one panel on
+          int ax = 0, ay = m0, by = 0;
+          if constexpr (kDw) {
+            ay = (m0 >> 6) * p.tpad;
+          } else if constexpr (KIND == LK_GRAD) {
+            ay = kb * p.tpad + m0;  // (panel kb)
+            by = p.v0 + kb * kBK;
           }
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
-            if constexpr (kPair)
-              ptx::tma_load_2d_pair(dst, map, bar, x, y);
-            else
-              ptx::tma_load_2d(dst, map, &full[stage], x, y);
-          };
-          if (dw) {
-            for (int i = 0; i < kBM / 64; ++i)
-              load(a_dst + i * kBoxBytes, ma, m0 + 64 * i, kb * kBK);
-          } else {
-            load(a_dst, ma, kb * kBK, m0);
+          for (int it = tl.it_lo; it < tl.it_hi; ++it) {
+            if (!W.wait_suspended(&empty[stage], phase ^ 1u)) return false;
+            uint8_t* a_dst = sA + stage * kABytes;
+            uint8_t* b_dst = sB + stage * C::kBBytes;
+            const uint32_t bar = full0 + stage * 8;
+            if (!kPair || cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+              if constexpr (kPair)
+                ptx::tma_load_2d_pair(dst, map, bar, x, y);
+              else
+                ptx::tma_load_2d(dst, map, &full[stage], x, y);
+            };
+            load(a_dst, ma, ax, ay);
+            if constexpr (kDw) load(a_dst + kBoxBytes, ma, ax, ay + p.tpad);
+            if constexpr (b_mn(KIND)) {
+              // W rows of the piece (dX) or tokens (dW) down, D across
+#pragma unroll
+              for (int i = 0; i < C::kBNcta / 64; ++i)
+                load(b_dst + i * kBoxBytes, mb, n0 + 64 * i, by);
+            } else {
+              load(b_dst, mb, ax, p.v0 + n0);
+            }
+            ++loads;
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if constexpr (kDw) {
+              ay += kBK;
+              by += kBK;
+            } else if constexpr (KIND == LK_GRAD) {
+              ay += p.tpad;
+              by += kBK;
+              if (++kb == p.kb_per_rank) {
+                kb = 0;
+                ++r;
+                ++ma;
+                ++mb;
+                ay = m0;
+                by = p.v0;
+              }
+            } else {
+              ax += kBK;
+            }
           }
-          if constexpr (b_mn(KIND)) {
-            // W rows of the piece (dX) or tokens (dW) down, D across
-            const int y = (dw ? 0 : p.v0) + kb * kBK;
-            for (int i = 0; i < C::kBNcta / 64; ++i)
-              load(b_dst + i * kBoxBytes, mb, n0 + 64 * i, y);
-          } else {
-            load(b_dst, mb, kb * kBK, p.v0 + n0);
-          }
-          issued |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          ++kb;
-          if (KIND == LK_GRAD && !dw && kb == p.kb_per_rank) {
-            kb = 0;
-            ++r;
-          }
-        }
+          return true;
+        };
+        if (KIND == LK_GRAD && tl.dw)
+          ok = k_loop(std::true_type{});
+        else
+          ok = k_loop(std::false_type{});
       }
       if (*abort_flag && cta == 0) {
         // Loads in flight write into shared memory: let them land (in a pair
         // all are counted on the leader's barriers).
-        for (int s = 0; s < kStages; ++s)
-          if (issued & (1u << s)) W.drain(&full[s], (last_parity >> s) & 1u, kDrainNs);
+        for (int64_t i = loads > kStages ? loads - kStages : 0; i < loads; ++i)
+          W.drain(&full[i % kStages], static_cast<uint32_t>((i / kStages) & 1), kDrainNs);
       }
     }
   } else if (warp == 1) {
@@ -542,29 +565,35 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         auto k_loop = [&](auto mn) {
           constexpr bool kDw = decltype(mn)::value;
           const uint32_t idesc = C::idesc(bn_cta * CG, kDw);
+          const uint64_t a_desc0 = ptx::smem_desc_sw128(ptx::smem_addr(sA), kDw ? kBoxBytes : 16, 1024);
+          const uint64_t b_desc0 =
+              ptx::smem_desc_sw128(ptx::smem_addr(sB), b_mn(KIND) ? kBoxBytes : 16, 1024);
           for (int it = tl.it_lo; it < tl.it_hi; ++it) {
             if (!W.wait_suspended(&full[stage], phase)) return false;
             ptx::tc_fence_after();
-            const uint32_t a_addr = ptx::smem_addr(sA + stage * kABytes);
-            const uint32_t b_addr = ptx::smem_addr(sB + stage * C::kBBytes);
-            // (dW: no MMA for 16 rows past the last token, which a short box
-            // does not fill)
-            const int steps = kDw ? min(kBK, p.T - it * kBK) : kBK;
-#pragma unroll
-            for (int kk = 0; kk < kBK / 16; ++kk) {
-              // K-major: 16 elements (32 B) on inside the swizzled row;
-              // MN-major: 16 k rows (2 KiB) on, 64-wide boxes 8 KiB apart.
-              const uint64_t ad = kDw ? ptx::smem_desc_sw128(a_addr + kk * 2048, kBoxBytes, 1024)
-                                      : ptx::smem_desc_sw128(a_addr + kk * 32, 16, 1024);
-              const uint64_t bd = b_mn(KIND)
-                                      ? ptx::smem_desc_sw128(b_addr + kk * 2048, kBoxBytes, 1024)
-                                      : ptx::smem_desc_sw128(b_addr + kk * 32, 16, 1024);
+            // The stage's descriptors; a K step of 16 on is 32 B within the
+            // swizzled row (K-major) or 2 KiB (MN-major, 64-wide boxes 8 KiB
+            // apart), added to the address field.
+            const uint64_t ad = a_desc0 + stage * (kABytes >> 4);
+            const uint64_t bd = b_desc0 + stage * (C::kBBytes >> 4);
+            auto mma = [&](int kk) {
               const uint32_t accum = (it > tl.it_lo || kk > 0) ? 1u : 0u;
-              if (kDw && 16 * kk >= steps) continue;
+              const uint64_t a_kk = ad + kk * ((kDw ? 2048 : 32) >> 4);
+              const uint64_t b_kk = bd + kk * ((b_mn(KIND) ? 2048 : 32) >> 4);
               if constexpr (kPair)
-                ptx::mma_f16_pair(d_tmem, ad, bd, idesc, accum);
+                ptx::mma_f16_pair(d_tmem, a_kk, b_kk, idesc, accum);
               else
-                ptx::mma_f16(d_tmem, ad, bd, idesc, accum);
+                ptx::mma_f16(d_tmem, a_kk, b_kk, idesc, accum);
+            };
+            // (dW: no MMA for 16 rows past the last token, which a short box
+            // does not fill; the usual step has no such test, which the one
+            // thread that issues would feel)
+            const int tokens = kDw ? p.T - it * kBK : kBK;
+            if (tokens > kBK - 16) {
+#pragma unroll
+              for (int kk = 0; kk < kBK / 16; ++kk) mma(kk);
+            } else {
+              for (int kk = 0; 16 * kk < tokens; ++kk) mma(kk);
             }
             if constexpr (kPair)
               ptx::mma_commit_pair_arrive_ctas(&empty[stage], 0x3);
@@ -625,13 +654,22 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           ptx::mbar_arrive(&tempty[acc]);
       }
     };
-    // The staged columns to (x, y) of a map, by one lane: 64 of dW, or `blocks`
-    // blocks of 32 of dl.
-    auto store_out = [&](const CUtensorMap* map, int x, int y, int blocks) {
+    // The staged columns leave by TMA, issued by one lane: dW, 64 columns to
+    // (x, y); dl, `blocks` blocks of 32 columns from piece column x on.
+    auto store_dw = [&](const CUtensorMap* map, int x, int y) {
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        for (int b = 0; b < blocks; ++b) ptx::tma_store_2d(map, buf + 2048 * b, x + 32 * b, y);
+        ptx::tma_store_2d(map, buf, x, y);
+        ptx::bulk_commit();
+      }
+    };
+    auto store_dl = [&](const CUtensorMap* map, int x, int row, int blocks) {
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        for (int b = 0; b < blocks; ++b, x += 32)
+          ptx::tma_store_2d(map, buf + 2048 * b, x & 63, (x >> 6) * p.tpad + row);
         ptx::bulk_commit();
       }
     };
@@ -757,25 +795,32 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               }
               v[k] = live ? __float_as_uint(x) : 0u;
             }
+            if (nc < 32) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (k >= nc) v[k] = 0u;
+            }
           }
           __syncwarp();
         };
-        // 64 columns at a time; the second 32 come from TMEM behind the first.
+        // 64 columns at a time.  DL: a piece's last tile also writes the zeros
+        // up to the end of its last panel.
+        int end = ncols;
+        if (KIND == LK_DL && tl.nt == p.tiles_n - 1) end = ((p.vn + 63) & ~63) - col0;
 #pragma unroll 1
-        for (int c = 64 * half; c < ncols; c += 128) {
+        for (int c = 64 * half; c < end; c += 128) {
           uint32_t v[2][32];
           ptx::tmem_ld_32x32b_x32(taddr + c, v[0]);
           ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
           ptx::tmem_ld_wait();
           const int nc = ncols - c;
-          chunk(v[0], c, nc);
-          if (nc > 32) chunk(v[1], c + 32, nc - 32);
+          if (KIND == LK_DL || nc > 0) chunk(v[0], c, nc);
+          if (KIND == LK_DL || nc > 32) chunk(v[1], c + 32, nc - 32);
           if constexpr (KIND == LK_DL) {
             buf_free();
             stage_bf16<false>(buf, lane, 0, v[0]);
-            if (nc > 32) stage_bf16<false>(buf, lane, 1, v[1]);
-            // (columns past the piece's end are not stored)
-            if (row0 < p.T) store_out(&p.mapO[tl.rank], col0 + c, row0, nc > 32 ? 2 : 1);
+            stage_bf16<false>(buf, lane, 1, v[1]);
+            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, end - c > 32 ? 2 : 1);
           }
         }
         release_acc();
@@ -846,7 +891,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           stage_bf16<true>(buf, lane, 1, v[1]);
           // (columns past D, and rows past the piece, which are past the
           // shard, are not stored)
-          if (row0 < p.vn) store_out(&p.mapO[tl.rank], col0 + c, p.v0 + row0, 1);
+          if (row0 < p.vn) store_dw(&p.mapO[tl.rank], col0 + c, p.v0 + row0);
         }
         release_acc();
       }
@@ -1328,7 +1373,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
              int sms, const fcc_opts* o) {
   Plan p;
   size_t off = 0;
-  const int64_t Vs = V / R;
+  const int64_t Vs = V / R, tpad = cdiv(T, 32) * 32;
   if (K > 0) {
     p.hit_idx = off;
     off += up256(static_cast<size_t>(T) * K * 4);
@@ -1341,7 +1386,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     // Equal pieces, whole tiles of 256 rows, as few as hold kPieceBytes of dl
     // (or the caller's count).
     const int64_t most = std::max<int64_t>(
-        kBN, static_cast<int64_t>(kPieceBytes / (static_cast<size_t>(T) * R * 2)) / kBN * kBN);
+        kBN, static_cast<int64_t>(kPieceBytes / (static_cast<size_t>(tpad) * R * 2)) / kBN * kBN);
     int64_t n = o != nullptr && o->chunks > 0 ? o->chunks : cdiv(Vs, most);
     n = std::max<int64_t>(1, std::min(n, cdiv(Vs, kBN)));
     p.piece = cdiv(cdiv(Vs, n), kBN) * kBN;
@@ -1367,7 +1412,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     if (smoothing) off += up256(static_cast<size_t>(p.nparts) * T * 4);
   } else {
     p.dl = off;
-    off += up256(static_cast<size_t>(R) * T * p.piece * 2);
+    off += up256(static_cast<size_t>(R) * tpad * p.piece * 2);
     if (want_dx) {
       p.acc = off;
       off += up256(static_cast<size_t>(T) * D * 4);
@@ -1398,6 +1443,7 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
   p.piece_tiles = pl.piece_tiles;
   p.start_ld = static_cast<long long>(c.R) * pl.npieces * pl.piece_tiles;
   p.group_m = 16;
+  p.tpad = static_cast<int>(cdiv(c.T, 32) * 32);
   p.a_rows = static_cast<int>(std::min<int64_t>(c.T, kBM));
   p.k_rows = static_cast<int>(std::min<int64_t>(cdiv(c.T, 16) * 16, kBK));
   p.K = std::max(c.K, 1);
@@ -1579,6 +1625,8 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     p.parts = reinterpret_cast<float*>(base + pl.parts);
   }
   if (want_dw && cdiv(rows, tm) * c.R * p.tiles_n > (1ll << 30)) return FCC_ERR_INVALID;
+  const int64_t panels = pl.piece / 64;
+  if (panels * p.tpad > INT32_MAX) return FCC_ERR_INVALID;
   for (int r = 0; r < c.R; ++r) {
     // W and X again, MN-major boxes
     if ((s = internal_encode_map(&p.mapB[r], c.W[r], Vs, c.D, c.D, kBK)) != FCC_OK ||
@@ -1586,22 +1634,19 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
       return s;
     if (want_dw && (s = internal_encode_map(&p.mapO[r], dW[r], Vs, c.D, c.D, 32)) != FCC_OK)
       return s;
+    // dl's panels, one below another
+    const char* d = base + pl.dl + static_cast<size_t>(r) * panels * p.tpad * 128;
+    const int64_t dl_rows = panels * p.tpad;
+    if ((s = internal_encode_map(&p_dl.mapO[r], d, dl_rows, 64, 64, 32, 32)) != FCC_OK ||
+        (s = internal_encode_map(&p.mapA[r], d, dl_rows, 64, 64, p.a_rows)) != FCC_OK ||
+        (s = internal_encode_map(&p.mapA2[r], d, dl_rows, 64, 64, p.k_rows)) != FCC_OK)
+      return s;
   }
   for (int64_t v0 = 0; v0 < Vs; v0 += pl.piece) {
     const int vn = static_cast<int>(std::min(pl.piece, Vs - v0));
     p_dl.v0 = p.v0 = static_cast<int>(v0);
     p_dl.vn = p.vn = vn;
     p_dl.piece = static_cast<int>(v0 / pl.piece);
-    // dl holds vn valid columns: the maps end there (reads past them give zeros)
-    if (v0 == 0 || v0 + vn == Vs) {
-      for (int r = 0; r < c.R; ++r) {
-        const char* d = base + pl.dl + static_cast<size_t>(r) * c.T * pl.piece * 2;
-        if ((s = internal_encode_map(&p_dl.mapO[r], d, c.T, vn, pl.piece, 32, 32)) != FCC_OK ||
-            (s = internal_encode_map(&p.mapA[r], d, c.T, vn, pl.piece, p.a_rows)) != FCC_OK ||
-            (s = internal_encode_map(&p.mapA2[r], d, c.T, vn, pl.piece, p.k_rows)) != FCC_OK)
-          return s;
-      }
-    }
     if (launch_loss_gemm<LK_DL>(p_dl, pl.cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
     p.first = v0 == 0 ? 1 : 0;
     p.kb_per_rank = static_cast<int>(cdiv(vn, kBK));
