@@ -138,13 +138,20 @@ def _addr(x) -> int:
     return int(x)
 
 
+_PTRS = [ctypes.c_void_p * n for n in range(FCC_MAX_EXPERTS + 1)]  # array types by length
+
+
 def _ptrs(seq):
     if seq is None:
         return None
     if isinstance(seq, ctypes.Array):  # built once by ptr_array()
         return seq
-    vals = [_addr(x) for x in seq]
-    return (ctypes.c_void_p * len(vals))(*vals)
+    try:
+        vals = [x.data_ptr() for x in seq]
+    except AttributeError:
+        vals = [_addr(x) for x in seq]
+    n = len(vals)
+    return (_PTRS[n] if n < len(_PTRS) else ctypes.c_void_p * n)(*vals)
 
 
 def ptr_array(seq):
@@ -160,9 +167,10 @@ def ptr_array(seq):
 def _stream(s) -> int:
     if s is None:
         return 0
-    if hasattr(s, "cuda_stream"):
-        return int(s.cuda_stream)
-    return int(s)
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        return int(s)
 
 
 def _opts(o):

@@ -64,6 +64,16 @@ enum LossKind : int {
 // K-major, W MN-major); dW contracts the tokens (dl and X both MN-major).
 constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 
+// The tensor core cuts its accumulator off instead of rounding it, once for
+// every 16 of D, so a logit comes out smaller by about 1.6e-8 of itself per
+// step: 4.2e-6 at D = 4096, 8.3e-6 at 8192, measured on sums whose terms agree
+// in sign, and as much on average on sums of random terms (in expectation a
+// partial sum is the same part of the final one).  The forward pass multiplies
+// it back.  Adding up shorter chains in registers costs 4 % (chains of 1024)
+// to 34 % (of 256) of the forward pass.
+constexpr float kCutPerStep = 1.6e-8f;
+constexpr float kHeavy = 0.125f;  // a teacher entry whose logit is also computed by itself
+
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
 // Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
 constexpr int threads_of(int kind) { return 64 + 32 * kEpiWarps + (kind == LK_FWD ? 64 : 0); }
@@ -199,14 +209,15 @@ struct LossParams {
   int ignore_index;
   float cap, inv_cap;      // soft cap, 0 = none
   float c2;                // log2(e) / tau
+  float grow;              // FWD: what the tensor core's sums lose on average, see kCutPerStep
   float tau, smoothing, z;
   // FWD
   float2* part;            // [R * tiles_n][T]: base-2 maximum and sum
   float* part_sum;         // the same layout: sum of the logits (smoothing), or NULL
   float* pick;             // [T, K] logits at the targets
   const void* X[FCC_MAX_RANKS];   // the matrices themselves and the labels' logits
-  const void* Wr[FCC_MAX_RANKS];  // (uncapped) computed from them
-  float* own_logit;        // [T]
+  const void* Wr[FCC_MAX_RANKS];  // (or the heavy entries') logits, uncapped, computed from them
+  float* own_logit;        // [T, K]
   // DL
   const float* lse[FCC_MAX_RANKS];
   const float* dloss;
@@ -529,11 +540,10 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             if (!W.wait_suspended(&empty[stage], phase ^ 1u)) return false;
             uint8_t* a_dst = sA + stage * kABytes;
             uint8_t* b_dst = sB + stage * C::kBBytes;
-            const uint32_t bar = full0 + stage * 8;
             if (!kPair || cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
               if constexpr (kPair)
-                ptx::tma_load_2d_pair(dst, map, bar, x, y);
+                ptx::tma_load_2d_pair(dst, map, full0 + stage * 8, x, y);
               else
                 ptx::tma_load_2d(dst, map, &full[stage], x, y);
             };
@@ -758,6 +768,18 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         float m2 = -INFINITY, sum = 0.f, lsum = 0.f;  // FWD: base-2 maximum, sum; plain sum
         // One chunk of 32 columns from c on, of which nc > 0 exist.
         auto chunk = [&](uint32_t (&v)[32], int c, int nc) {
+          if constexpr (KIND == LK_FWD) {
+            const uint64_t grow2 = ptx::f32x2_pack(p.grow, p.grow);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float x0, x1;
+              ptx::f32x2_unpack(
+                  ptx::f32x2_mul(ptx::f32x2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                                 grow2), x0, x1);
+              v[k] = __float_as_uint(x0);
+              v[k + 1] = __float_as_uint(x1);
+            }
+          }
           if (p.cap > 0.f) {
 #pragma unroll
             for (int k = 0; k < 32; ++k)
@@ -948,38 +970,53 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       if (lane == 0) ptx::bulk_wait_all();
     }
   } else {
-    // ------------------------------------- the labels' own logits (FWD, labels)
-    // Two warps beside the GEMM take one token at a time and compute x_y =
-    // X_t . W_y in f32 with short chains of additions.  The tensor core's sum
-    // of D/16 partial sums loses up to a few 1e-6 of it, which shows in the
-    // loss (lse - l_y) more than in lse; these 2 D f32 products per token are
-    // hidden behind the 2 V D of the GEMM.
+    // ------------------------------------------ the targets' own logits (FWD)
+    // Two warps beside the GEMM take one token at a time and compute X_t . W_i
+    // in f32, with short chains of additions, for its label or its teacher
+    // entries of probability 1/8 or more: the logits that the loss takes from
+    // lse one by one, whose errors do not average out.  2 D products for each
+    // are hidden behind the 2 V D of the GEMM.
     if constexpr (KIND == LK_FWD) {
-      if (p.labels != nullptr) {
-        const int vecs = p.D / 8;
-        for (long long t = blockIdx.x * 2 + (warp - 2 - kEpiWarps); t < p.T; t += 2 * gridDim.x) {
+      const int vecs = p.D / 8;
+      auto own_logit = [&](long long t, int y) {
+        const int r = y / p.Vs;
+        const uint4* x = reinterpret_cast<const uint4*>(p.X[r]) + t * vecs;
+        const uint4* w = reinterpret_cast<const uint4*>(p.Wr[r]) +
+                         static_cast<long long>(y - r * p.Vs) * vecs;
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int i = lane; i < vecs; i += 32) {
+          const uint4 a = __ldg(x + i), b = __ldg(w + i);
+          const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            s[2 * k] = fmaf(__uint_as_float(au[k] << 16), __uint_as_float(bu[k] << 16), s[2 * k]);
+            s[2 * k + 1] = fmaf(__uint_as_float(au[k] & 0xffff0000u),
+                                __uint_as_float(bu[k] & 0xffff0000u), s[2 * k + 1]);
+          }
+        }
+        float d = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+        return d;
+      };
+      for (long long t = blockIdx.x * 2 + (warp - 2 - kEpiWarps); t < p.T; t += 2 * gridDim.x) {
+        if (p.labels != nullptr) {
           const int y = __ldg(p.labels + t);
           if (!label_live(p, y)) continue;
-          const int r = y / p.Vs;
-          const uint4* x = reinterpret_cast<const uint4*>(p.X[r]) + t * vecs;
-          const uint4* w = reinterpret_cast<const uint4*>(p.Wr[r]) +
-                           static_cast<long long>(y - r * p.Vs) * vecs;
-          float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-          for (int i = lane; i < vecs; i += 32) {
-            const uint4 a = __ldg(x + i), b = __ldg(w + i);
-            const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              s[2 * k] = fmaf(__uint_as_float(au[k] << 16), __uint_as_float(bu[k] << 16), s[2 * k]);
-              s[2 * k + 1] = fmaf(__uint_as_float(au[k] & 0xffff0000u),
-                                  __uint_as_float(bu[k] & 0xffff0000u), s[2 * k + 1]);
+          const float d = own_logit(t, y);
+          if (lane == 0) p.own_logit[t] = d;
+        } else {
+          for (int k0 = 0; k0 < p.K; k0 += 32) {
+            const bool in = k0 + lane < p.K;
+            const int id = in ? __ldg(p.hit_idx + t * p.K + k0 + lane) : INT_MAX;
+            const bool heavy = id != INT_MAX && __ldg(p.hit_q + t * p.K + k0 + lane) >= kHeavy;
+            for (unsigned left = __ballot_sync(0xffffffffu, heavy); left != 0; left &= left - 1) {
+              const int j = __ffs(left) - 1;
+              const float d = own_logit(t, __shfl_sync(0xffffffffu, id, j));
+              if (lane == 0) p.own_logit[t * p.K + k0 + j] = d;
             }
           }
-          float d = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-          if (lane == 0) p.own_logit[t] = d;
         }
       }
     }
@@ -1136,77 +1173,102 @@ struct CombineArgs {
   float* loss[FCC_MAX_RANKS];
   float* lse[FCC_MAX_RANKS];
   int R, T, V, K, nparts, tok, ignore_index;
-  float tau, smoothing, z, cap;
+  float tau, c2, smoothing, z, cap;
   int* status;
 };
 
 __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) {
   ptx::griddep_wait();  // launched with programmatic stream serialization
   ptx::griddep_launch_dependents();
-  __shared__ float sm[256], ss[256], sl[256], sh[256];
+  __shared__ float sm[256], ss[256], sl[256], sg[256];
   const int token = threadIdx.x & (a.tok - 1), part = threadIdx.x / a.tok;
   const int parts = 256 / a.tok;
   const long long t = static_cast<long long>(blockIdx.x) * a.tok + token;
-  float m = -INFINITY, s = 0.f, l = 0.f, h = 0.f;
+  float m = -INFINITY, s = 0.f, l = 0.f;
   if (t < a.T) {
     for (int i = part; i < a.nparts; i += parts) {
       const float2 x = __ldg(a.part + static_cast<long long>(i) * a.T + t);
       merge(m, s, x.x, x.y);
       if (a.part_sum != nullptr) l += __ldg(a.part_sum + static_cast<long long>(i) * a.T + t);
     }
-    if (a.labels == nullptr) {
-      // sum_k q_k (log q_k - l_k / tau); an entry of probability 0 adds nothing
-      for (int k = part; k < a.K; k += parts) {
-        if (__ldg(a.hit_idx + t * a.K + k) == INT_MAX) continue;
-        const float q = __ldg(a.hit_q + t * a.K + k);
-        if (q != 0.f) h += q * (logf(q) - __ldg(a.pick + t * a.K + k) / a.tau);
-      }
-    }
   }
   sm[threadIdx.x] = m;
   ss[threadIdx.x] = s;
   sl[threadIdx.x] = l;
-  sh[threadIdx.x] = h;
   __syncthreads();
   for (int n = parts / 2; n > 0; n >>= 1) {
     if (part < n) {
       const int o = threadIdx.x + n * a.tok;
       merge(sm[threadIdx.x], ss[threadIdx.x], sm[o], ss[o]);
       sl[threadIdx.x] += sl[o];
-      sh[threadIdx.x] += sh[o];
+    }
+    __syncthreads();
+  }
+  m = sm[token];
+  const float log2s = log2f(ss[token]);
+  const float lsum = sl[token];
+  __syncthreads();
+  // The targets.  lse - l_k is taken in base 2 from the sum's own maximum
+  // (rounded as the target's logit is here), so that a target that is the
+  // maximum loses nothing.  Where the logit is also known by itself, l + e, it
+  // takes the place of the tensor core's l; in the sum too, whose logarithm
+  // then grows by log(1 + sum_k p_k (exp(e_k / tau) - 1)).
+  float gap = 0.f, more = 0.f, own = 0.f;  // own: the label's logit
+  bool live = false;
+  auto target = [&](long long at, bool exact, bool in_sum) {
+    const float x = __ldg(a.pick + at);
+    const float x2 = __fmul_rn(x, a.c2);
+    float e = 0.f;
+    if (exact) {
+      const float y = __ldg(a.own_logit + at);
+      e = (a.cap > 0.f ? a.cap * tanhf(y / a.cap) : y) - x;
+      if (in_sum) more += exp2f(x2 - m - log2s) * expm1f(e / a.tau);
+    }
+    own = x + e;
+    return (m - x2 + log2s) * kLn2 - e / a.tau;
+  };
+  if (t < a.T) {
+    if (a.labels != nullptr) {
+      const int y = __ldg(a.labels + t);
+      live = y != a.ignore_index && y >= 0 && y < a.V;
+      if (part == 0) {
+        if (live)
+          gap = target(t, true, true);
+        else if (y != a.ignore_index)
+          atomicCAS(a.status, 0, FCC_ERR_INVALID);
+      }
+    } else {
+      live = __ldg(a.hit_idx + t * a.K) != INT_MAX;
+      for (int k = part; k < a.K; k += parts) {
+        const long long at = t * a.K + k;
+        const int id = __ldg(a.hit_idx + at);
+        const float q = id != INT_MAX ? __ldg(a.hit_q + at) : 0.f;
+        if (q == 0.f) continue;  // (an entry of probability 0 adds nothing)
+        // (an index given twice is in the sum once)
+        const bool again = k > 0 && __ldg(a.hit_idx + at - 1) == id && __ldg(a.hit_q + at - 1) >= kHeavy;
+        gap += q * (logf(q) + target(at, q >= kHeavy, !again));
+      }
+    }
+  }
+  ss[threadIdx.x] = gap;
+  sg[threadIdx.x] = more;
+  __syncthreads();
+  for (int n = parts / 2; n > 0; n >>= 1) {
+    if (part < n) {
+      ss[threadIdx.x] += ss[threadIdx.x + n * a.tok];
+      sg[threadIdx.x] += sg[threadIdx.x + n * a.tok];
     }
     __syncthreads();
   }
   if (part != 0 || t >= a.T) return;
-  const float log2s = log2f(ss[threadIdx.x]);
-  float lse = (sm[threadIdx.x] + log2s) * kLn2;
+  const float grow = log1pf(sg[threadIdx.x]);
+  const float lse = (m + log2s) * kLn2 + grow;
   float loss = 0.f;
-  if (a.labels != nullptr) {
-    const int y = __ldg(a.labels + t);
-    if (y != a.ignore_index) {
-      if (y < 0 || y >= a.V) {
-        atomicCAS(a.status, 0, FCC_ERR_INVALID);
-      } else {
-        // The label's logit l inside the sum is the tensor core's; the more
-        // exact one is l + e, and with p = exp(l - lse) the sum's logarithm
-        // then grows by log(1 + p (exp(e) - 1)).  lse - l is taken in base 2
-        // from the sum's own maximum, so that a label that is the maximum
-        // loses nothing.
-        const float l = __ldg(a.pick + t);
-        const float x = __ldg(a.own_logit + t);
-        const float e = (a.cap > 0.f ? a.cap * tanhf(x / a.cap) : x) - l;
-        const float l2 = __fmul_rn(l, kLog2e);  // (rounded as the maximum was)
-        const float grow = log1pf(exp2f(l2 - sm[threadIdx.x] - log2s) * expm1f(e));
-        const float gap = (sm[threadIdx.x] - l2 + log2s) * kLn2 + (grow - e);
-        lse += grow;
-        loss = gap + a.z * lse * lse;
-        // lse - (1 - eps) l_y - eps / V sum l = gap + eps (l_y - mean l)
-        if (a.part_sum != nullptr)
-          loss += a.smoothing * (l + e - sl[threadIdx.x] / static_cast<float>(a.V));
-      }
-    }
-  } else if (__ldg(a.hit_idx + t * a.K) != INT_MAX) {
-    loss = a.tau * a.tau * (sh[threadIdx.x] + lse);
+  if (live) {
+    loss = a.tau * a.tau * (ss[threadIdx.x] + grow);  // (labels: tau = 1)
+    if (a.labels != nullptr) loss += a.z * lse * lse;
+    // lse - (1 - eps) l_y - eps / V sum l = (lse - l_y) + eps (l_y - mean l)
+    if (a.part_sum != nullptr) loss += a.smoothing * (own - lsum / static_cast<float>(a.V));
   }
   for (int r = 0; r < a.R; ++r) {
     a.loss[r][t] = loss;
@@ -1249,6 +1311,7 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ 
     const long long row = static_cast<long long>(mt) * a.tile_m + rr;
     if (row >= a.T) return;
     float4 x = __ldcs(reinterpret_cast<const float4*>(a.acc + row * a.D + col));
+#pragma unroll 4
     for (int i = 1; i < n; ++i) {
       const float4 y = __ldcs(reinterpret_cast<const float4*>(
           a.parts + ((part0 + i - 1) * a.tile_m + rr) * kBN + c));
@@ -1455,7 +1518,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     p.pick = off;
     off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
     p.own_logit = off;
-    if (K == 0) off += up256(static_cast<size_t>(T) * 4);
+    off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
     p.part = off;
     off += up256(static_cast<size_t>(p.nparts) * T * 8);
     p.part_sum = off;
@@ -1508,6 +1571,7 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
   p.inv_cap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
   p.tau = c.tau;
   p.c2 = static_cast<float>(1.4426950408889634 / c.tau);
+  p.grow = 1.f + kCutPerStep * static_cast<float>(cdiv(c.D, 16));
   p.smoothing = c.smoothing;
   p.z = c.z;
   p.status = status;
@@ -1604,6 +1668,7 @@ fcc_status forward(const Call& c, float* const* loss, float* const* lse) {
   a.nparts = pl.nparts;
   a.ignore_index = c.ignore_index;
   a.tau = c.tau;
+  a.c2 = p.c2;
   a.smoothing = c.smoothing;
   a.z = c.z;
   a.cap = c.softcap;
