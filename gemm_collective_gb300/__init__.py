@@ -125,6 +125,7 @@ _loss_ws = _sig("fcc_linear_loss_workspace_size", ctypes.c_size_t,
 _launches = _sig("fcc_launch_count", ctypes.c_uint64, [])
 _version = _sig("fcc_version", ctypes.c_char_p, [])
 _wait_timeout = _sig("fcc_test_wait_timeout", _I, [_I64, _P])
+_suspended_wait_timeout = _sig("fcc_test_suspended_wait_timeout", _I, [_I64, _P])
 _grouped_wait_timeout = _sig("fcc_test_grouped_wait_timeout", _I, [_I64, _P])
 _ksplit_wait_timeout = _sig("fcc_test_ksplit_wait_timeout", _I, [_I64, _P])
 
@@ -331,6 +332,10 @@ def fcc_version() -> str:
 
 def fcc_test_wait_timeout(timeout_ns: int, stream=None):
     _check(_wait_timeout(timeout_ns, _stream(stream)), "fcc_test_wait_timeout")
+
+
+def fcc_test_suspended_wait_timeout(timeout_ns: int, stream=None):
+    _check(_suspended_wait_timeout(timeout_ns, _stream(stream)), "fcc_test_suspended_wait_timeout")
 
 
 def fcc_test_grouped_wait_timeout(timeout_ns: int, stream=None):

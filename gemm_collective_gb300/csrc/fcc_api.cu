@@ -1021,7 +1021,16 @@ fcc_status fcc_test_wait_timeout(int64_t timeout_ns, fcc_stream_t stream) {
   DeviceState* d = nullptr;
   fcc_status s = device_state(&d);
   if (s != FCC_OK) return s;
-  return cuda_fail(launch_wait_probe(d->status, static_cast<unsigned long long>(timeout_ns),
+  return cuda_fail(launch_wait_probe(d->status, static_cast<unsigned long long>(timeout_ns), 0,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fcc_status fcc_test_suspended_wait_timeout(int64_t timeout_ns, fcc_stream_t stream) {
+  if (timeout_ns <= 0) return FCC_ERR_INVALID;
+  DeviceState* d = nullptr;
+  fcc_status s = device_state(&d);
+  if (s != FCC_OK) return s;
+  return cuda_fail(launch_wait_probe(d->status, static_cast<unsigned long long>(timeout_ns), 1,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -86,9 +86,9 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const GatherArgs a) {
 }
 
 // Waits on an mbarrier that nothing completes, with the library's bounded
-// wait: the wait runs out after `timeout_ns`, the status word records
+// wait (spinning or suspended): the wait runs out after `timeout_ns`, the status word records
 // FCC_ERR_TIMEOUT and the kernel returns.
-__global__ void wait_probe_kernel(int* status, unsigned long long timeout_ns) {
+__global__ void wait_probe_kernel(int* status, unsigned long long timeout_ns, int suspended) {
   __shared__ uint64_t bar;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
@@ -99,7 +99,10 @@ __global__ void wait_probe_kernel(int* status, unsigned long long timeout_ns) {
   __syncthreads();
   if (threadIdx.x == 0) {
     const ptx::Waiter W{&abort_flag, status, timeout_ns};
-    W.wait(&bar, 0);
+    if (suspended)
+      W.wait_suspended(&bar, 0);
+    else
+      W.wait(&bar, 0);
   }
   __syncthreads();
 }
@@ -160,8 +163,9 @@ cudaError_t launch_gather_rows_range(const void* const* X, int R, int64_t Ms, in
                     a);
 }
 
-cudaError_t launch_wait_probe(int* status, unsigned long long timeout_ns, cudaStream_t st) {
-  wait_probe_kernel<<<1, 32, 0, st>>>(status, timeout_ns);
+cudaError_t launch_wait_probe(int* status, unsigned long long timeout_ns, int suspended,
+                              cudaStream_t st) {
+  wait_probe_kernel<<<1, 32, 0, st>>>(status, timeout_ns, suspended);
   bump_launch_count(1);
   return cudaGetLastError();
 }

@@ -224,7 +224,8 @@ cudaError_t launch_gather_rows(const void* const* X, int R, int64_t Ms, int64_t 
 cudaError_t launch_gather_rows_range(const void* const* X, int R, int64_t Ms, int64_t K,
                                      void* dst, int64_t row_begin, int64_t row_end,
                                      cudaStream_t st);
-cudaError_t launch_wait_probe(int* status, unsigned long long timeout_ns, cudaStream_t st);
+cudaError_t launch_wait_probe(int* status, unsigned long long timeout_ns, int suspended,
+                              cudaStream_t st);
 
 // Shared host helpers (fcc_api.cu).
 int* device_status_ptr();

@@ -74,6 +74,13 @@ constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 constexpr float kCutPerStep = 1.6e-8f;
 constexpr float kHeavy = 0.125f;  // a teacher entry whose logit is also computed by itself
 
+// Up to this many tokens dl is kept as the sum of two bf16 numbers, the second
+// in the rows kSplit further on of its panels.  With few tokens there is no
+// averaging of dl's rounding in dW (one token: an error of up to 2^-8 of the
+// label's whole row), and the rows of the 128-row tile are free: dX's two halves
+// are rows of one product, dW's a second K step of a pass bound by its output.
+constexpr int kSplit = 32;
+
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
 // Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
 constexpr int threads_of(int kind) { return 64 + 32 * kEpiWarps + (kind == LK_FWD ? 64 : 0); }
@@ -184,7 +191,8 @@ struct LossParams {
   int R, T, D;
   int Vs;                  // vocabulary rows per rank
   int v0, vn;              // this piece: rows [v0, v0 + vn) of every rank (FWD: 0, Vs)
-  int tpad;                // rows of a dl panel: the tokens, to a multiple of 32
+  int tpad;                // rows of a dl panel: the tokens, to a multiple of 32 (split: 2 kSplit)
+  int split;               // GRAD, DL: dl in two halves, see kSplit
   int width;               // tile columns (FWD, DL: a multiple of 32), else kBN
   int tiles_m, tiles_n;    // tiles of one rank (GRAD: of dX, over all)
   int full_tiles;          // tiles run whole, round-robin (dX: the others are shared, see Shares)
@@ -221,7 +229,7 @@ struct LossParams {
   // DL
   const float* lse[FCC_MAX_RANKS];
   const float* dloss;
-  // dX: f32 sums [T][D] of whole tiles and of shared tiles' first parts, and
+  // dX: f32 sums [T][D] (split: [2 kSplit][D]) of whole tiles and of shared tiles' first parts, and
   // one [rows][kBN] block for each further part; first = 1: overwrite, else add
   float* acc;
   float* parts;
@@ -261,7 +269,7 @@ __device__ __forceinline__ Tile dw_tile_of(const LossParams& p, int t) {
   tl.shared = 0;
   tl.dw = true;
   tl.it_lo = 0;
-  tl.it_hi = (p.T + kBK - 1) / kBK;
+  tl.it_hi = p.split ? 2 : (p.T + kBK - 1) / kBK;
   p.dw_order.at(t, tl.mt, tl.nt);
   tl.rank = p.by_dw_tiles_m.div(tl.mt);
   tl.mt -= tl.rank * p.dw_tiles_m;
@@ -563,8 +571,8 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               phase ^= 1u;
             }
             if constexpr (kDw) {
-              ay += kBK;
-              by += kBK;
+              ay += p.split ? kSplit : kBK;
+              by += p.split ? 0 : kBK;
             } else if constexpr (KIND == LK_GRAD) {
               ay += p.tpad;
               by += kBK;
@@ -631,7 +639,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             // (dW: no MMA for 16 rows past the last token, which a short box
             // does not fill; the usual step has no such test, which the one
             // thread that issues would feel)
-            const int tokens = kDw ? p.T - it * kBK : kBK;
+            const int tokens = kDw ? p.T - (p.split ? 0 : it * kBK) : kBK;
             if (tokens > kBK - 16) {
 #pragma unroll
               for (int kk = 0; kk < kBK / 16; ++kk) mma(kk);
@@ -888,7 +896,22 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             buf_free();
             stage_bf16<false>(buf, lane, 0, v[0]);
             stage_bf16<false>(buf, lane, 1, v[1]);
-            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, end - c > 32 ? 2 : 1);
+            const int blocks = end - c > 32 ? 2 : 1;
+            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, blocks);
+            if (p.split && row0 < p.T) {  // what the rounding left
+#pragma unroll
+              for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const float x = __uint_as_float(v[b][k]);
+                  v[b][k] = __float_as_uint(
+                      x - __uint_as_float(ptx::pack_bf16x2(0.f, x) & 0xffff0000u));
+                }
+              buf_free();
+              stage_bf16<false>(buf, lane, 0, v[0]);
+              stage_bf16<false>(buf, lane, 1, v[1]);
+              store_dl(&p.mapO[tl.rank], col0 + c, row0 + kSplit, blocks);
+            }
           }
         }
         release_acc();
@@ -909,7 +932,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           }
         }
       } else if (!tl.dw) {
-        const bool row_ok = row < p.T;
+        const bool row_ok = p.split ? row < 2 * kSplit && row % kSplit < p.T : row < p.T;
         const int col0 = tl.nt * kBN;
         const int width = min(kBN, p.D - col0);
         const bool none = tl.it_lo >= tl.it_hi;  // (no steps of a short last piece: adds nothing)
@@ -1284,7 +1307,7 @@ struct FinishArgs {
   const float* acc;
   const float* parts;
   void* out[FCC_MAX_RANKS];
-  int T, D, R;
+  int T, D, R, split;
   int tile_m, full_tiles;
   Raster order;
   Shares shares;
@@ -1310,15 +1333,19 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ 
   for (int rr = r0 + (threadIdx.x >> 6); rr < r0 + kFinRows; rr += 4) {
     const long long row = static_cast<long long>(mt) * a.tile_m + rr;
     if (row >= a.T) return;
-    float4 x = __ldcs(reinterpret_cast<const float4*>(a.acc + row * a.D + col));
-#pragma unroll 4
-    for (int i = 1; i < n; ++i) {
-      const float4 y = __ldcs(reinterpret_cast<const float4*>(
-          a.parts + ((part0 + i - 1) * a.tile_m + rr) * kBN + c));
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](const float* src) {
+      const float4 y = __ldcs(reinterpret_cast<const float4*>(src));
       x.x += y.x;
       x.y += y.y;
       x.z += y.z;
       x.w += y.w;
+    };
+    for (int half = 0; half <= a.split; ++half) {  // (split: the rows kSplit on are dl's second half's)
+      add(a.acc + (row + half * kSplit) * a.D + col);
+#pragma unroll 4
+      for (int i = 1; i < n; ++i)
+        add(a.parts + ((part0 + i - 1) * a.tile_m + rr + half * kSplit) * kBN + c);
     }
     const uint2 o = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
     for (int r = 0; r < a.R; ++r)
@@ -1482,11 +1509,14 @@ struct Plan {
 
 constexpr size_t kPieceBytes = size_t(512) << 20;  // dl held at a time
 
+// Rows of a dl panel.
+int64_t tpad_of(int64_t T) { return T <= kSplit ? 2 * kSplit : cdiv(T, 32) * 32; }
+
 Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoothing, bool want_dx,
              int sms, const fcc_opts* o) {
   Plan p;
   size_t off = 0;
-  const int64_t Vs = V / R, tpad = cdiv(T, 32) * 32;
+  const int64_t Vs = V / R, tpad = tpad_of(T);
   if (K > 0) {
     p.hit_idx = off;
     off += up256(static_cast<size_t>(T) * K * 4);
@@ -1528,7 +1558,7 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     off += up256(static_cast<size_t>(R) * tpad * p.piece * 2);
     if (want_dx) {
       p.acc = off;
-      off += up256(static_cast<size_t>(T) * D * 4);
+      off += up256(static_cast<size_t>(T <= kSplit ? 2 * kSplit : T) * D * 4);
       // Blocks for the shared tiles' further parts: fewer than the shares and
       // the shared tiles together, each at most the CTAs (pairs).
       const int64_t tiles = cdiv(T, kBM) * cdiv(D, kBN);
@@ -1555,7 +1585,8 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
   p.npieces = pl.npieces;
   p.piece_tiles = pl.piece_tiles;
   p.start_ld = static_cast<long long>(c.R) * pl.npieces * pl.piece_tiles;
-  p.tpad = static_cast<int>(cdiv(c.T, 32) * 32);
+  p.split = c.T <= kSplit ? 1 : 0;
+  p.tpad = static_cast<int>(tpad_of(c.T));
   p.a_rows = static_cast<int>(std::min<int64_t>(c.T, kBM));
   p.k_rows = static_cast<int>(std::min<int64_t>(cdiv(c.T, 16) * 16, kBK));
   p.K = std::max(c.K, 1);
@@ -1724,6 +1755,7 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
   const int slots = slots_of(cg, sms);
   const int64_t tm = static_cast<int64_t>(kBM) * cg;
   p.width = kBN;
+  if (p.split) p.a_rows = kSplit + p.T;
   p.tiles_m = static_cast<int>(cdiv(c.T, tm));
   p.tiles_n = static_cast<int>(cdiv(c.D, kBN));
   p.order = raster_of(p.tiles_m, p.tiles_n, kGroupM);
@@ -1784,6 +1816,7 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     f.T = p.T;
     f.D = p.D;
     f.R = c.R;
+    f.split = p.split;
     f.tile_m = static_cast<int>(tm);
     f.order = p.order;
     f.full_tiles = p.full_tiles;

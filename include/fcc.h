@@ -377,9 +377,9 @@ fcc_status fcc_linear_xent(int R, const void *const *X, const void *const *W,
  * Ignored rows have no gradient, whatever their dloss holds.  dX or dW may be
  * NULL (not wanted).  The logits are computed again, a piece of every rank's
  * vocabulary at a time (opts->chunks pieces; 0 = as few as hold 512 MiB of
- * dx), and rounded to bf16 as dx; products accumulate in f32.  out_dtype is
- * FCC_BF16 (an f32 result of bf16 dx would promise digits it does not have).
- * Uses workspace (fcc_linear_loss_workspace_size with topk 0, grad 1).
+ * dx), and dx is rounded to bf16 (for up to 32 tokens, to a sum of two bf16
+ * numbers); products accumulate in f32.  out_dtype is FCC_BF16 (an f32 result
+ * of bf16 dx would promise digits it does not have).  Uses workspace (fcc_linear_loss_workspace_size with topk 0, grad 1).
  */
 fcc_status fcc_linear_xent_grad(int R, const void *const *X, const void *const *W,
                                 const int32_t *labels, const float *const *lse,
@@ -473,6 +473,9 @@ double fcc_interdecom_time(double G, double X, double alpha, int chunks);
  * fcc_stream_status() afterwards returns FCC_ERR_TIMEOUT.
  */
 fcc_status fcc_test_wait_timeout(int64_t timeout_ns, fcc_stream_t stream);
+
+/* Test support: the same with the suspended form of the wait that the losses' kernels use. */
+fcc_status fcc_test_suspended_wait_timeout(int64_t timeout_ns, fcc_stream_t stream);
 
 /*
  * Test support: launches the MoE grouped expert GEMM kernel (the in-kernel

@@ -206,6 +206,75 @@ def test_tile_shapes_and_pieces(pair, chunks):
     check(Case(1, 20, 513, 64, smoothing=0.1), fcc.make_opts(cta_pair=pair, chunks=chunks, max_ctas=3))
 
 
+@pytest.mark.parametrize("max_ctas", [1, 2, 5, 8, 11, 40])
+@pytest.mark.parametrize("chunks", [1, 3])
+def test_every_way_to_share_the_tiles(max_ctas, chunks):
+    """Few CTAs: whole rounds of dX tiles, shared ones with and without helpers,
+    last pieces shorter than the plan."""
+    o = fcc.make_opts(max_ctas=max_ctas, chunks=chunks)
+    for case in (Case(2, 300, 2 * 650, 648), Case(1, 100, 1500, 1160, K=6), Case(1, 20, 900, 520)):
+        check(case, o)
+
+
+def test_few_tokens_keep_the_gradients_exact():
+    """Up to 32 tokens dl is two bf16 numbers: dW is one rounding (2^-8) off, not two."""
+    for T in (1, 2, 31, 32):
+        for K in (0, 3):
+            c = Case(1, T, 400, 64, K=K)
+            _, lse = c.forward()
+            dX, dW = c.backward(lse)
+            gX, gW, tX, tW = c.oracle_backward()
+            # what is left of tX, tW without dl's rounding: below 2^-14 of the sums of magnitudes
+            X, W = c.f64()
+            l = losses.logits(X, W)
+            p = np.exp(l - losses.logsumexp(l)[:, None])
+            a = np.abs(c.dloss.numpy().astype(float))[:, None] * (p + 2.0 ** -10)
+            within(dX[0], gX, 2.0 ** -8 * np.abs(gX) + 2.0 ** -12 * (a @ np.abs(W)), f"dX {T} {K}")
+            within(dW[0], gW, 2.0 ** -8 * np.abs(gW) + 2.0 ** -12 * (a.T @ np.abs(X)), f"dW {T} {K}")
+
+
+@pytest.mark.parametrize("D", [64, 1024, 8192])
+def test_losses_hold_their_digits_over_long_rows(D):
+    """A label that stands out, and sums of up to 8192 terms that agree in sign:
+    the loss is off by less than 4e-6 (2^-18) of lse and logit; the tensor
+    cores alone, which cut off, would be off by 1.6e-8 per 16 terms, 8e-5 here."""
+    g = torch.Generator().manual_seed(D)
+    T, V = 200, 700
+    W = (torch.randn(V, D, generator=g) * 1.3 / D ** 0.5).bfloat16()
+    y = torch.randint(0, V, (T,), generator=g, dtype=torch.int32)
+    X = (torch.randn(T, D, generator=g) + 6 * W[y.long()].float()).bfloat16()
+    idx = y[:, None].contiguous()
+    rl, rs = losses.xent(X.double().numpy(), W.double().numpy(), y.numpy())
+    x, w = X.cuda(), W.cuda()
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    fcc.fcc_linear_xent(1, [x], [w], y.cuda(), T, V, D, [loss], [lse])
+    kd, ks = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    fcc.fcc_linear_distill(1, [x], [w], idx.cuda(), torch.zeros(T, 1, device="cuda"), T, V, D, 1, [kd], [ks])
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    for got in (loss, kd):
+        assert np.abs(to_f64(got) - rl).max() <= 2.0 ** -18 * (np.abs(rs).max() + 1)
+    for got in (lse, ks):
+        assert np.abs(to_f64(got) - rs).max() <= 2.0 ** -18 * (np.abs(rs).max() + 1)
+
+
+def test_a_suspended_wait_runs_out():
+    fcc.fcc_test_suspended_wait_timeout(2_000_000)  # 2 ms on a barrier nothing completes
+    assert fcc.fcc_stream_status() == fcc.FCC_ERR_TIMEOUT
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(Case(1, 30, 300, 64))
+
+
+def test_the_example_trains():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "train_head.py"), "--steps", "12"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "cross entropy" in r.stdout and "distillation" in r.stdout
+
+
 @pytest.mark.parametrize("K", [0, 9])
 def test_rows_without_targets(K):
     """All rows ignored: losses and gradients are exact zeros, whatever dloss holds."""
