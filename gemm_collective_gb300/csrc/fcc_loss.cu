@@ -12,20 +12,28 @@
 // with a, b, w_k per token (cross entropy: one target, its label).
 //
 // Forward, one GEMM over (token tile, vocabulary tile of any rank): each
-// epilogue thread owns one token's 256 logits of the tile in TMEM and reduces
-// them to a running maximum and sum (base 2), their plain sum when smoothing
-// asks for it, and the logits at the token's targets; one partial per (tile,
-// token) goes to memory and combine_kernel merges the partials of all ranks:
-// the all-reduce of the softmax statistics.
+// epilogue thread owns one token's logits of the tile in TMEM and reduces them
+// to a maximum and a sum (base 2), their plain sum when smoothing asks for it,
+// and the logits at the token's targets; one partial per (tile, token) goes to
+// memory and loss_combine_kernel merges the partials of all ranks: the
+// all-reduce of the softmax statistics.
 // Backward, per piece of the vocabulary: the same product again, whose
-// epilogue turns logits into dl (bf16) for the piece; then dX += dl W (the K
-// loop runs over all ranks: the all-reduce) and dW = dl^T X.  Only one piece
-// of dl is ever held.
+// epilogue turns logits into dl (bf16) for the piece; then, in one launch,
+// dX += dl W (the K loop runs over all ranks: the all-reduce) and dW = dl^T X.
+// Only one piece of dl is ever held.
 //
 // All products run on tcgen05 (bf16 x bf16 -> f32 in TMEM), fed by TMA through
 // an mbarrier ring: warp 0 loads, warp 1 issues the MMAs into one of two TMEM
-// accumulators, warps 2-5 are the epilogue of the other.  CG = 1: one CTA per
-// 128 x 256 tile; CG = 2: a CTA pair per 256 x 256 tile.
+// accumulators, warps 2-9 are the epilogue of the other.  CG = 1: one CTA per
+// 128 x 256 tile, a ring of 48 KiB stages; CG = 2: a CTA pair per 256 x 256
+// tile, 32 KiB stages.  Each CTA is alone on its SM and loops over tiles.
+//
+// What bounds it, measured (tensor pipe busy, 4096 tokens x 32768 x 4096):
+// forward 96 %, dl 95 %, dX 92 %, dW 92 %.  A training-sized call then runs at
+// the chip's power limit, where what the waiting warps do not issue counts: with
+// every wait suspended in hardware instead of spinning the forward pass of 8192
+// tokens x 131072 x 4096 took 4.89 ms, spinning 5.07.  A few tokens are bound
+// by reading W: 64 tokens x 131072 x 8192 in 327 us, 6.6 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -57,9 +65,10 @@ enum LossKind : int {
 };
 // Operand layouts: X and W rows are contiguous along D.  dl, the library's own,
 // is kept in panels of 64 vocabulary entries, [panel][token][64], tokens padded
-// to 32 with zeros: every box of dl that a product loads is one contiguous run
-// (row-major over the whole piece, a box's 128-byte rows lie a piece apart, and
-// the tensor cores were busy %DLROW% of dX and dW, against %DLPANEL% this way).
+// to 32 with zeros: every box of dl that a product loads is one contiguous run.
+// (Row-major over the whole piece, a box's 128-byte rows lie a piece apart: the
+// tensor pipe was busy 86 % of dX, against 92 % this way; 4096 tokens x 32768 x
+// 4096.)
 // Logits contract D (both operands K-major); dX contracts the vocabulary (dl
 // K-major, W MN-major); dW contracts the tokens (dl and X both MN-major).
 constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
@@ -79,7 +88,7 @@ constexpr float kHeavy = 0.125f;  // a teacher entry whose logit is also compute
 // averaging of dl's rounding in dW (one token: an error of up to 2^-8 of the
 // label's whole row), and the rows of the 128-row tile are free: dX's two halves
 // are rows of one product, dW's a second K step of a pass bound by its output.
-constexpr int kSplit = 32;
+constexpr int kSplit = 64;
 
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
 // Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
@@ -113,8 +122,8 @@ struct Cfg {
 // `ctas` CTAs (pairs).  Each of `groups` CTAs per tile takes `len` steps of
 // it, so that the CTAs of a group walk the same rows of dl and W side by side
 // (equal shares of the tiles' steps laid end to end start everywhere in k and
-// read dl and W from memory once per tile: 321 us against %DX% for 1999 tokens
-// x 50257 x 2048); the helpers, the CTAs left over, share the tiles' remaining
+// read dl and W from memory once per tile: 321 us against 224 for 1999 tokens x
+// 50257 x 2048); the helpers, the CTAs left over, share the tiles' remaining
 // tails, laid end to end.  A tile's parts are summed at the end in a fixed
 // order.
 struct Shares {
@@ -1302,7 +1311,7 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
 // ------------------------------------------------------------------ dX finish
 // dX[r] = bf16(acc + the further parts of shared tiles, in order) for every
 // rank.  A CTA takes kFinRows rows of a tile: 64 threads of 4 columns a row.
-constexpr int kFinRows = 8;
+constexpr int kFinRows = 4;
 struct FinishArgs {
   const float* acc;
   const float* parts;
@@ -1343,7 +1352,7 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ 
     };
     for (int half = 0; half <= a.split; ++half) {  // (split: the rows kSplit on are dl's second half's)
       add(a.acc + (row + half * kSplit) * a.D + col);
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 1; i < n; ++i)
         add(a.parts + ((part0 + i - 1) * a.tile_m + rr + half * kSplit) * kBN + c);
     }
@@ -1397,7 +1406,8 @@ int choose_width(int R, int64_t tiles_m, int64_t vn, int slots) {
 }
 
 // The shares of `rest` tiles of k steps over at most `slots` CTAs (pairs), of
-// four steps at least.
+// eight steps at least: shorter ones make more parts to sum than they save (64
+// tokens x 8000 x 1024: 35 us, against 53 with four and 42 with sixteen).
 Shares plan_shares(int rest, int k, int slots) {
   Shares s;
   std::memset(&s, 0, sizeof(s));
@@ -1406,7 +1416,7 @@ Shares plan_shares(int rest, int k, int slots) {
   const int64_t total = static_cast<int64_t>(rest) * k;
   s.tiles = rest;
   s.k = k;
-  s.ctas = static_cast<int>(std::max<int64_t>(rest, std::min<int64_t>(slots, total / 4)));
+  s.ctas = static_cast<int>(std::max<int64_t>(rest, std::min<int64_t>(slots, total / 8)));
   s.groups = s.ctas / rest;
   s.helpers = s.ctas - s.groups * rest;
   s.len = static_cast<int>(s.helpers > 0 ? cdiv(total, s.ctas) : cdiv(k, s.groups));

@@ -377,7 +377,7 @@ fcc_status fcc_linear_xent(int R, const void *const *X, const void *const *W,
  * Ignored rows have no gradient, whatever their dloss holds.  dX or dW may be
  * NULL (not wanted).  The logits are computed again, a piece of every rank's
  * vocabulary at a time (opts->chunks pieces; 0 = as few as hold 512 MiB of
- * dx), and dx is rounded to bf16 (for up to 32 tokens, to a sum of two bf16
+ * dx), and dx is rounded to bf16 (for up to 64 tokens, to a sum of two bf16
  * numbers); products accumulate in f32.  out_dtype is FCC_BF16 (an f32 result
  * of bf16 dx would promise digits it does not have).  Uses workspace (fcc_linear_loss_workspace_size with topk 0, grad 1).
  */
