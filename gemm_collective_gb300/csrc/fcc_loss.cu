@@ -712,7 +712,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       __syncwarp();
       if (lane == 0) {
         if constexpr (kPair)
-          ptx::mbar_arrive_cluster(tempty_leader0 + acc * 8);
+          ptx::mbar_arrive_cluster_tmem(tempty_leader0 + acc * 8);
         else
           ptx::mbar_arrive(&tempty[acc]);
       }
@@ -895,6 +895,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         // up to the end of its last panel.
         int end = ncols;
         if (KIND == LK_DL && tl.nt == p.tiles_n - 1) end = ((p.vn + 63) & ~63) - col0;
+        if (row0 >= p.T) end = 0;  // (no token in the warp's rows)
 #pragma unroll 1
         for (int c = 64 * half; c < end; c += 128) {
           uint32_t v[2][32];
@@ -946,7 +947,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       } else if (!tl.dw) {
         const bool row_ok = p.split ? row < 2 * kSplit && row % kSplit < p.T : row < p.T;
         const int col0 = tl.nt * kBN;
-        const int width = min(kBN, p.D - col0);
+        const int width = __any_sync(0xffffffffu, row_ok) ? min(kBN, p.D - col0) : 0;
         const bool none = tl.it_lo >= tl.it_hi;  // (no steps of a short last piece: adds nothing)
         if (!wait_tile()) break;
         float* dst = tl.part == 0
@@ -1314,9 +1315,12 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
 }
 
 // ------------------------------------------------------------------ dX finish
-// dX[r] = bf16(acc + the further parts of shared tiles, in order) for every
-// rank.  A CTA takes kFinRows rows of a tile: 64 threads of 4 columns a row.
-constexpr int kFinRows = 4;
+// dX[r] = bf16(acc + the further parts of shared tiles) for every rank.  64
+// threads of 4 columns take a row of a tile; a CTA has four such groups, for
+// four rows, or (SPLIT, for tiles of many parts: a few tokens' sums over the
+// whole vocabulary) for one row, each group with every fourth part.  The order
+// of the sums is fixed.  (The whole backward pass of 16 tokens x 131072 x 256, whose
+// one dX tile has 152 parts: 94 us with one group, 69 so.)
 struct FinishArgs {
   const float* acc;
   const float* parts;
@@ -1327,44 +1331,61 @@ struct FinishArgs {
   Shares shares;
 };
 
+template <bool SPLIT>
 __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ FinishArgs a) {
   ptx::griddep_wait();  // launched with programmatic stream serialization
   ptx::griddep_launch_dependents();
-  const int per = a.tile_m / kFinRows;
+  constexpr int kRows = SPLIT ? 1 : 4, kGroups = SPLIT ? 4 : 1;
+  __shared__ float4 red[SPLIT ? 256 : 1];
+  const int per = a.tile_m / kRows;
   const int t = blockIdx.x / per;
-  const int r0 = (blockIdx.x - t * per) * kFinRows;
+  const int group = threadIdx.x >> 6;
+  const int rr = (blockIdx.x - t * per) * kRows + (SPLIT ? 0 : group);
   int mt, nt;
   a.order.at(t, mt, nt);
+  const long long row = static_cast<long long>(mt) * a.tile_m + rr;
+  if (SPLIT && row >= a.T) return;  // (the whole CTA)
   const int c = (threadIdx.x & 63) * 4;
   const int col = nt * kBN + c;
+  const bool in = row < a.T && col + 4 <= a.D;
   int n = 1;
   long long part0 = 0;
   if (t >= a.full_tiles) {
     n = a.shares.parts(t - a.full_tiles);
     part0 = static_cast<long long>(t - a.full_tiles) * (a.shares.max_parts - 1);
   }
-  if (col + 4 > a.D) return;
-  for (int rr = r0 + (threadIdx.x >> 6); rr < r0 + kFinRows; rr += 4) {
-    const long long row = static_cast<long long>(mt) * a.tile_m + rr;
-    if (row >= a.T) return;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](const float* src) {
-      const float4 y = __ldcs(reinterpret_cast<const float4*>(src));
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in) {
+    for (int half = 0; half <= a.split; ++half) {  // (the rows kSplit on are dl's second half's)
+#pragma unroll 8
+      for (int i = SPLIT ? group : 0; i < n; i += kGroups) {
+        const float* src = i == 0 ? a.acc + (row + half * kSplit) * a.D + col
+                                  : a.parts + ((part0 + i - 1) * a.tile_m + rr + half * kSplit) * kBN + c;
+        const float4 y = __ldcs(reinterpret_cast<const float4*>(src));
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+    }
+  }
+  if constexpr (SPLIT) {
+    red[threadIdx.x] = x;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 y = red[64 * g + threadIdx.x];
       x.x += y.x;
       x.y += y.y;
       x.z += y.z;
       x.w += y.w;
-    };
-    for (int half = 0; half <= a.split; ++half) {  // (split: the rows kSplit on are dl's second half's)
-      add(a.acc + (row + half * kSplit) * a.D + col);
-#pragma unroll 8
-      for (int i = 1; i < n; ++i)
-        add(a.parts + ((part0 + i - 1) * a.tile_m + rr + half * kSplit) * kBN + c);
     }
-    const uint2 o = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
-    for (int r = 0; r < a.R; ++r)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out[r]) + row * a.D + col) = o;
   }
+  if (!in) return;
+  const uint2 o = make_uint2(ptx::pack_bf16x2(x.x, x.y), ptx::pack_bf16x2(x.z, x.w));
+  for (int r = 0; r < a.R; ++r)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out[r]) + row * a.D + col) = o;
 }
 
 // ------------------------------------------------------------------ host side
@@ -1836,9 +1857,10 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     f.order = p.order;
     f.full_tiles = p.full_tiles;
     f.shares = p.shares;
-    const int blocks = dx_tiles * (f.tile_m / kFinRows);
-    if (launch_pdl(dx_finish_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.st, 1u,
-                   f) != cudaSuccess)
+    const bool many = p.shares.max_parts > 8;
+    const int blocks = dx_tiles * (many ? f.tile_m : f.tile_m / 4);
+    if (launch_pdl(many ? dx_finish_kernel<true> : dx_finish_kernel<false>,
+                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.st, 1u, f) != cudaSuccess)
       return FCC_ERR_CUDA;
     ++launches;
   }

@@ -510,6 +510,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same where the waiter depends on no memory that this thread wrote, only on
+// its tensor-memory loads (complete, and ordered by tcgen05.fence before it):
+// release at CTA scope, which does not wait for the thread's stores to be
+// performed cluster-wide.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // 16 bytes of another CTA's shared memory (shared::cluster address from mapa).
 __device__ __forceinline__ float4 ld_shared_cluster_f4(uint32_t cluster_addr) {
   float4 v;
