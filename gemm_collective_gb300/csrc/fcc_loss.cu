@@ -82,6 +82,7 @@ constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 // to 34 % (of 256) of the forward pass.
 constexpr float kCutPerStep = 1.6e-8f;
 constexpr float kHeavy = 0.125f;  // a teacher entry whose logit is also computed by itself
+constexpr int kMaxHeavy = 8;      // (a token has at most so many: their sum is 1)
 
 // Up to this many tokens dl is kept as the sum of two bf16 numbers, the second
 // in the rows kSplit further on of its panels.  With few tokens there is no
@@ -138,6 +139,8 @@ struct Shares {
   __host__ __device__ __forceinline__ int helper_of(long long x) const {
     return static_cast<int>(((x + 1) * helpers - 1) / tails());
   }
+  // No tile is shared after all: as many CTAs as tiles.
+  __host__ __device__ __forceinline__ bool alone() const { return groups == 1 && tail <= 0; }
   // Parts of shared tile i.
   __host__ __device__ __forceinline__ int parts(int i) const {
     if (tail <= 0) return groups;
@@ -197,6 +200,7 @@ struct LossParams {
   CUtensorMap mapO[FCC_MAX_RANKS];  // DL: dl, box 32 tokens x 32; GRAD: dW, 32 rows x 64
   CUtensorMap mapA2[FCC_MAX_RANKS];  // GRAD: mapA, mapB of dX are dl and W, of dW these:
   CUtensorMap mapB2[FCC_MAX_RANKS];  // dl and X in boxes of k_rows tokens
+  CUtensorMap mapX[FCC_MAX_RANKS];   // GRAD: dX, box 32 x 64
   int R, T, D;
   int Vs;                  // vocabulary rows per rank
   int v0, vn;              // this piece: rows [v0, v0 + vn) of every rank (FWD: 0, Vs)
@@ -235,6 +239,7 @@ struct LossParams {
   const void* X[FCC_MAX_RANKS];   // the matrices themselves and the labels' logits
   const void* Wr[FCC_MAX_RANKS];  // (or the heavy entries') logits, uncapped, computed from them
   float* own_logit;        // [T, K]
+  const int16_t* heavy;    // [T, kMaxHeavy]: a token's heavy entries' places, then -1
   // DL
   const float* lse[FCC_MAX_RANKS];
   const float* dloss;
@@ -243,6 +248,7 @@ struct LossParams {
   float* acc;
   float* parts;
   int first;
+  int direct;              // dX tiles that one CTA sums to the end leave in bf16 here (last piece)
   int* status;
   unsigned long long timeout_ns;
 };
@@ -253,6 +259,7 @@ struct Tile {
   int part;          // dX: which part of a shared tile (0: goes to acc)
   int shared;        // dX: index among the shared tiles
   bool dw;           // GRAD: a tile of dW, else of dX
+  bool alone;        // dX: no other CTA has a part of the tile
 };
 
 template <int KIND>
@@ -262,6 +269,7 @@ __device__ __forceinline__ Tile tile_of(const LossParams& p, int t) {
   tl.part = 0;
   tl.shared = 0;
   tl.dw = false;
+  tl.alone = true;
   tl.it_lo = 0;
   tl.it_hi = p.k_iters;
   p.order.at(t, tl.mt, tl.nt);
@@ -277,6 +285,7 @@ __device__ __forceinline__ Tile dw_tile_of(const LossParams& p, int t) {
   tl.part = 0;
   tl.shared = 0;
   tl.dw = true;
+  tl.alone = true;
   tl.it_lo = 0;
   tl.it_hi = p.split ? 2 : (p.T + kBK - 1) / kBK;
   p.dw_order.at(t, tl.mt, tl.nt);
@@ -340,6 +349,7 @@ struct Work {
       tl = tile_of<KIND>(p, p.full_tiles + i);
       tl.shared = i;
       tl.part = part;
+      tl.alone = s.alone();
       // (a shorter last piece has fewer steps than planned, or none)
       tl.it_lo = min(lo, p.k_iters);
       tl.it_hi = min(lo + n, p.k_iters);
@@ -717,13 +727,14 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           ptx::mbar_arrive(&tempty[acc]);
       }
     };
-    // The staged columns leave by TMA, issued by one lane: dW, 64 columns to
-    // (x, y); dl, `blocks` blocks of 32 columns from piece column x on.
-    auto store_dw = [&](const CUtensorMap* map, int x, int y) {
+    // The staged columns leave by TMA, issued by one lane: dW and dX, 64 columns
+    // to (x, y) of each of `n` maps; dl, `blocks` blocks of 32 columns from piece
+    // column x on.
+    auto store_rows = [&](const CUtensorMap* maps, int n, int x, int y) {
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ptx::tma_store_2d(map, buf, x, y);
+        for (int r = 0; r < n; ++r) ptx::tma_store_2d(maps + r, buf, x, y);
         ptx::bulk_commit();
       }
     };
@@ -955,30 +966,62 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
                          : p.parts + (static_cast<long long>(tl.shared) * (p.shares.max_parts - 1) +
                                       tl.part - 1) * (TM * kBN) +
                                (cta * kBM + trow) * kBN;
+        if (p.direct && tl.alone) {
+          // The sum is complete: bf16 to every rank (the all-reduce).
 #pragma unroll 1
-        for (int c = 64 * half; c < width; c += 128) {
-          uint32_t v[64];
-          ptx::tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
-          ptx::tmem_ld_32x32b_x32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-          ptx::tmem_ld_wait();
-          if (c + 128 >= width) release_acc();
-          if (row_ok && (p.first || !none)) {
+          for (int c = 64 * half; c < width; c += 128) {
+            uint32_t v[2][32];
+            ptx::tmem_ld_32x32b_x32(taddr + c, v[0]);
+            ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
+            ptx::tmem_ld_wait();
+            if (c + 128 >= width) release_acc();
+            if (!p.first && row_ok) {
 #pragma unroll
-            for (int g = 0; g < 16; ++g) {
-              if (c + 4 * g + 4 > width) continue;
-              float4 x = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
-                                     __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
-              if (none) x = make_float4(0.f, 0.f, 0.f, 0.f);
-              // (one CTA adds to an element once per piece, so the sum's order
-              // is the pieces'; the additions need no answer)
-              float* o = dst + c + 4 * g;
-              if (p.first)
-                *reinterpret_cast<float4*>(o) = x;
-              else
-                ptx::red_add_v4_f32(o, x.x, x.y, x.z, x.w);
+              for (int b = 0; b < 2; ++b) {
+                float4 y[8];
+#pragma unroll
+                for (int g = 0; g < 8; ++g)
+                  y[g] = c + 32 * b + 4 * g + 4 <= width
+                             ? __ldcg(reinterpret_cast<const float4*>(dst + c + 32 * b + 4 * g))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  v[b][k] = __float_as_uint((none ? 0.f : __uint_as_float(v[b][k])) +
+                                            reinterpret_cast<const float*>(y)[k]);
+              }
             }
+            __syncwarp();
+            buf_free();
+            stage_bf16<true>(buf, lane, 0, v[0]);
+            stage_bf16<true>(buf, lane, 1, v[1]);
+            store_rows(p.mapX, p.R, col0 + c, row0);
           }
-          __syncwarp();
+        } else {
+#pragma unroll 1
+          for (int c = 64 * half; c < width; c += 128) {
+            uint32_t v[64];
+            ptx::tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t(*)[32]>(v));
+            ptx::tmem_ld_32x32b_x32(taddr + c + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+            ptx::tmem_ld_wait();
+            if (c + 128 >= width) release_acc();
+            if (row_ok && (p.first || !none)) {
+#pragma unroll
+              for (int g = 0; g < 16; ++g) {
+                if (c + 4 * g + 4 > width) continue;
+                float4 x = make_float4(__uint_as_float(v[4 * g]), __uint_as_float(v[4 * g + 1]),
+                                       __uint_as_float(v[4 * g + 2]), __uint_as_float(v[4 * g + 3]));
+                if (none) x = make_float4(0.f, 0.f, 0.f, 0.f);
+                // (one CTA adds to an element once per piece, so the sum's order
+                // is the pieces'; the additions need no answer)
+                float* o = dst + c + 4 * g;
+                if (p.first)
+                  *reinterpret_cast<float4*>(o) = x;
+                else
+                  ptx::red_add_v4_f32(o, x.x, x.y, x.z, x.w);
+              }
+            }
+            __syncwarp();
+          }
         }
         if (64 * half >= width) release_acc();
       } else {
@@ -997,7 +1040,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           stage_bf16<true>(buf, lane, 1, v[1]);
           // (columns past D, and rows past the piece, which are past the
           // shard, are not stored)
-          if (row0 < p.vn) store_dw(&p.mapO[tl.rank], col0 + c, p.v0 + row0);
+          if (row0 < p.vn) store_rows(&p.mapO[tl.rank], 1, col0 + c, p.v0 + row0);
         }
         if (64 * half >= width) release_acc();
       }
@@ -1009,51 +1052,82 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
     }
   } else {
     // ------------------------------------------ the targets' own logits (FWD)
-    // Two warps beside the GEMM take one token at a time and compute X_t . W_i
-    // in f32, with short chains of additions, for its label or its teacher
-    // entries of probability 1/8 or more: the logits that the loss takes from
-    // lse one by one, whose errors do not average out.  2 D products for each
-    // are hidden behind the 2 V D of the GEMM.
+    // Two warps beside the GEMM compute X_t . W_i in f32, with short chains of
+    // additions, for every token's label or its teacher entries of probability
+    // 1/8 or more: the logits that the loss takes from lse one by one, whose
+    // errors do not average out.  2 D products for each are hidden behind the
+    // 2 V D of the GEMM.  A lane holds a (token, entry); the warp computes four
+    // products at a time, so that their loads are in flight together (one at a
+    // time took longer than a GEMM over a small vocabulary).
     if constexpr (KIND == LK_FWD) {
       const int vecs = p.D / 8;
-      auto own_logit = [&](long long t, int y) {
-        const int r = y / p.Vs;
-        const uint4* x = reinterpret_cast<const uint4*>(p.X[r]) + t * vecs;
-        const uint4* w = reinterpret_cast<const uint4*>(p.Wr[r]) +
-                         static_cast<long long>(y - r * p.Vs) * vecs;
-        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int i = lane; i < vecs; i += 32) {
-          const uint4 a = __ldg(x + i), b = __ldg(w + i);
-          const uint32_t au[4] = {a.x, a.y, a.z, a.w}, bu[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[2 * k] = fmaf(__uint_as_float(au[k] << 16), __uint_as_float(bu[k] << 16), s[2 * k]);
-            s[2 * k + 1] = fmaf(__uint_as_float(au[k] & 0xffff0000u),
-                                __uint_as_float(bu[k] & 0xffff0000u), s[2 * k + 1]);
+      const int slots = p.labels != nullptr ? 1 : kMaxHeavy;   // entries of a token
+      const long long warps = 2 * static_cast<long long>(gridDim.x);
+      const int group = static_cast<int>(  // tokens of a warp at a time
+          min(static_cast<long long>(32 / slots), (p.T + warps - 1) / warps));
+      for (long long t0 = (2 * static_cast<long long>(blockIdx.x) + warp - 2 - kEpiWarps) * group;
+           t0 < p.T; t0 += warps * group) {
+        const long long t = t0 + lane / slots;
+        int y = -1;
+        long long at = t;
+        if (lane < group * slots && t < p.T) {
+          if (p.labels != nullptr) {
+            y = __ldg(p.labels + t);
+            if (!label_live(p, y)) y = -1;
+          } else {
+            const int k = __ldg(p.heavy + t * kMaxHeavy + lane % kMaxHeavy);
+            if (k >= 0) {
+              at = t * p.K + k;
+              y = __ldg(p.hit_idx + at);
+            }
           }
         }
-        float d = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+        unsigned left = __ballot_sync(0xffffffffu, y >= 0);
+        while (left != 0) {
+          const uint4* x[4];
+          const uint4* w[4];
+          int from[4];
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-        return d;
-      };
-      for (long long t = blockIdx.x * 2 + (warp - 2 - kEpiWarps); t < p.T; t += 2 * gridDim.x) {
-        if (p.labels != nullptr) {
-          const int y = __ldg(p.labels + t);
-          if (!label_live(p, y)) continue;
-          const float d = own_logit(t, y);
-          if (lane == 0) p.own_logit[t] = d;
-        } else {
-          for (int k0 = 0; k0 < p.K; k0 += 32) {
-            const bool in = k0 + lane < p.K;
-            const int id = in ? __ldg(p.hit_idx + t * p.K + k0 + lane) : INT_MAX;
-            const bool heavy = id != INT_MAX && __ldg(p.hit_q + t * p.K + k0 + lane) >= kHeavy;
-            for (unsigned left = __ballot_sync(0xffffffffu, heavy); left != 0; left &= left - 1) {
-              const int j = __ffs(left) - 1;
-              const float d = own_logit(t, __shfl_sync(0xffffffffu, id, j));
-              if (lane == 0) p.own_logit[t * p.K + k0 + j] = d;
+          for (int u = 0; u < 4; ++u) {
+            // (past the last one: the same again)
+            if (u == 0 || left != 0) {
+              from[u] = __ffs(left) - 1;
+              left &= left - 1;
+            } else {
+              from[u] = from[u - 1];
             }
+            const int yu = __shfl_sync(0xffffffffu, y, from[u]);
+            const int r = yu / p.Vs;
+            x[u] = reinterpret_cast<const uint4*>(p.X[r]) + (t0 + from[u] / slots) * vecs;
+            w[u] = reinterpret_cast<const uint4*>(p.Wr[r]) +
+                   static_cast<long long>(yu - r * p.Vs) * vecs;
+          }
+          float s[4][4] = {};
+          for (int i = lane; i < vecs; i += 32) {
+            uint4 a[4], b[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              a[u] = __ldg(x[u] + i);
+              b[u] = __ldg(w[u] + i);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint32_t au[4] = {a[u].x, a[u].y, a[u].z, a[u].w};
+              const uint32_t bu[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                s[u][k] = fmaf(__uint_as_float(au[k] << 16), __uint_as_float(bu[k] << 16), s[u][k]);
+                s[u][k] = fmaf(__uint_as_float(au[k] & 0xffff0000u),
+                               __uint_as_float(bu[k] & 0xffff0000u), s[u][k]);
+              }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float d = (s[u][0] + s[u][1]) + (s[u][2] + s[u][3]);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+            if (lane == from[u]) p.own_logit[at] = d;
           }
         }
       }
@@ -1091,7 +1165,9 @@ struct TeacherArgs {
   int32_t* hit_idx;
   float* hit_q;
   uint16_t* hit_start;  // [T][start_ld]
+  int16_t* heavy;       // [T][kMaxHeavy]: the places of entries of probability >= kHeavy
   long long start_ld;
+  FastDiv by_piece_tiles, by_npieces;
   int T, K, V, Vs;
   int npieces, piece_tiles, piece_rows, width;  // logit tiles of a rank
   float inv_tau;
@@ -1171,19 +1247,28 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const Teach
     }
   }
   __syncwarp();
+  if (lane < kMaxHeavy) a.heavy[row * kMaxHeavy + lane] = -1;
+  __syncwarp();
+  int heavies = 0;  // those found so far
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int place = lane * E + e, at = static_cast<int>(key[e] >> 8);
+    const float q = prob[w][key[e] & 255u];
     sorted[w][place] = at;
     if (place < a.K) {
       a.hit_idx[row * a.K + place] = at;
-      a.hit_q[row * a.K + place] = prob[w][key[e] & 255u];
+      a.hit_q[row * a.K + place] = q;
     }
+    const unsigned those = __ballot_sync(0xffffffffu, at != INT_MAX && q >= kHeavy);
+    const int mine = heavies + __popc(those & ((1u << lane) - 1u));
+    if ((those >> lane & 1u) && mine < kMaxHeavy)
+      a.heavy[row * kMaxHeavy + mine] = static_cast<int16_t>(place);
+    heavies += __popc(those);
   }
   __syncwarp();
   for (int t = lane; t < a.start_ld; t += 32) {
-    const int rp = t / a.piece_tiles;
-    const int r = rp / a.npieces;
+    const int rp = a.by_piece_tiles.div(t);
+    const int r = a.by_npieces.div(rp);
     const int col = min((rp - r * a.npieces) * a.piece_rows + (t - rp * a.piece_tiles) * a.width, a.Vs);
     const int first = r * a.Vs + col;
     int lo = 0;  // entries before `first`: all of the first lo, and maybe more
@@ -1326,7 +1411,7 @@ struct FinishArgs {
   const float* parts;
   void* out[FCC_MAX_RANKS];
   int T, D, R, split;
-  int tile_m, full_tiles;
+  int tile_m, full_tiles, first_tile;  // first_tile: those before it have left already
   Raster order;
   Shares shares;
 };
@@ -1338,9 +1423,9 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ 
   constexpr int kRows = SPLIT ? 1 : 4, kGroups = SPLIT ? 4 : 1;
   __shared__ float4 red[SPLIT ? 256 : 1];
   const int per = a.tile_m / kRows;
-  const int t = blockIdx.x / per;
+  const int t = a.first_tile + blockIdx.x / per;
   const int group = threadIdx.x >> 6;
-  const int rr = (blockIdx.x - t * per) * kRows + (SPLIT ? 0 : group);
+  const int rr = (blockIdx.x % per) * kRows + (SPLIT ? 0 : group);
   int mt, nt;
   a.order.at(t, mt, nt);
   const long long row = static_cast<long long>(mt) * a.tile_m + rr;
@@ -1535,7 +1620,7 @@ int usable_sms(const fcc_opts* o) {
 // Scratch layout.  Forward: partials, target logits; distillation also the
 // sorted teacher entries.  Backward: the piece's dl, the f32 sums of dX.
 struct Plan {
-  size_t hit_idx = 0, hit_q = 0, hit_start = 0, pick = 0, own_logit = 0, part = 0, part_sum = 0;
+  size_t hit_idx = 0, hit_q = 0, hit_start = 0, heavy = 0, pick = 0, own_logit = 0, part = 0, part_sum = 0;
   size_t dl = 0, acc = 0, parts = 0, total = 0;
   int cg = 1, width = kBN;  // logit tiles
   int nparts = 0;
@@ -1578,6 +1663,8 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
   if (K > 0) {
     p.hit_start = off;
     off += up256(static_cast<size_t>(T) * R * p.npieces * p.piece_tiles * 2);
+    p.heavy = off;
+    off += up256(static_cast<size_t>(T) * kMaxHeavy * 2);
   }
   if (!grad) {
     p.nparts = static_cast<int>(R * cdiv(Vs, p.width));
@@ -1632,6 +1719,7 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
     p.hit_idx = reinterpret_cast<int32_t*>(base + pl.hit_idx);
     p.hit_q = reinterpret_cast<float*>(base + pl.hit_q);
     p.hit_start = reinterpret_cast<uint16_t*>(base + pl.hit_start);
+    p.heavy = reinterpret_cast<int16_t*>(base + pl.heavy);
   }
   p.ignore_index = c.ignore_index;
   p.cap = c.softcap;
@@ -1658,6 +1746,9 @@ cudaError_t launch_teacher(const Call& c, const Plan& pl, char* base, int* statu
   a.inv_tau = 1.f / c.tau;
   a.status = status;
   a.hit_start = reinterpret_cast<uint16_t*>(base + pl.hit_start);
+  a.heavy = reinterpret_cast<int16_t*>(base + pl.heavy);
+  a.by_piece_tiles = fast_div(pl.piece_tiles);
+  a.by_npieces = fast_div(pl.npieces);
   a.start_ld = static_cast<long long>(c.R) * pl.npieces * pl.piece_tiles;
   a.Vs = static_cast<int>(c.V / c.R);
   a.npieces = pl.npieces;
@@ -1817,6 +1908,8 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
       return s;
     if (want_dw && (s = internal_encode_map(&p.mapO[r], dW[r], Vs, c.D, c.D, 32)) != FCC_OK)
       return s;
+    if (want_dx && (s = internal_encode_map(&p.mapX[r], dX[r], c.T, c.D, c.D, 32)) != FCC_OK)
+      return s;
     // dl's panels, one below another
     const char* d = base + pl.dl + static_cast<size_t>(r) * panels * p.tpad * 128;
     const int64_t dl_rows = panels * p.tpad;
@@ -1832,6 +1925,7 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     p_dl.piece = static_cast<int>(v0 / pl.piece);
     if (launch_loss_gemm<LK_DL>(p_dl, pl.cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
     p.first = v0 == 0 ? 1 : 0;
+    p.direct = want_dx && v0 + vn == Vs && !p.split ? 1 : 0;
     p.kb_per_rank = static_cast<int>(cdiv(vn, kBK));
     p.k_iters = c.R * p.kb_per_rank;
     if (want_dw) {
@@ -1843,7 +1937,9 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     if (launch_loss_gemm<LK_GRAD>(p, cg, sms, c.st) != cudaSuccess) return FCC_ERR_CUDA;
     launches += 2;
   }
-  if (want_dx) {
+  // (direct: nothing is left to sum but the shared tiles)
+  const int first_tile = p.direct ? p.full_tiles : 0;
+  if (want_dx && first_tile < dx_tiles && !(p.direct && p.shares.alone())) {
     FinishArgs f;
     std::memset(&f, 0, sizeof(f));
     f.acc = p.acc;
@@ -1856,9 +1952,10 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     f.tile_m = static_cast<int>(tm);
     f.order = p.order;
     f.full_tiles = p.full_tiles;
+    f.first_tile = first_tile;
     f.shares = p.shares;
     const bool many = p.shares.max_parts > 8;
-    const int blocks = dx_tiles * (many ? f.tile_m : f.tile_m / 4);
+    const int blocks = (dx_tiles - first_tile) * (many ? f.tile_m : f.tile_m / 4);
     if (launch_pdl(many ? dx_finish_kernel<true> : dx_finish_kernel<false>,
                    dim3(static_cast<unsigned>(blocks)), dim3(256), 0, c.st, 1u, f) != cudaSuccess)
       return FCC_ERR_CUDA;
