@@ -104,17 +104,22 @@ template <int KIND, int CG>
 struct Cfg {
   static constexpr int kTileM = kBM * CG;
   static constexpr int kBNcta = kBN / CG;                  // B columns this CTA holds
-  static constexpr int kStages = (CG == 2 ? 7 : 4) - (stages_out(KIND) && CG == 2 ? 1 : 0);
+  // GRAD: stages of full size.  FWD, DL: as many as the tile's rows and width
+  // leave room for (LossParams), up to kMaxStages: a few words' or tokens' tiles
+  // are bound by the loads, of which more are then in flight (64 tokens x 131072
+  // x 8192: 327 -> 313 us).
+  static constexpr int kMaxStages = KIND == LK_GRAD ? (CG == 2 ? 6 : 4) : 16;
   static constexpr uint32_t kBBytes = kBK * kBNcta * 2;    // 32 or 16 KiB
   static constexpr uint32_t kStageBytes = kABytes + kBBytes;
   static constexpr uint32_t kOut = stages_out(KIND) ? kEpiWarps * kOutBytes : 0;
+  static constexpr uint32_t kRing = 7 * 32768 - kOut;      // bytes for the stages
+  static_assert(KIND != LK_GRAD || kMaxStages * kStageBytes <= kRing, "ring");
   // Instruction descriptor of a tile `width` columns wide.
   __device__ static constexpr uint32_t idesc(int width, bool a_mn) {
     return ptx::idesc_bf16_f32(kTileM, width, a_mn, b_mn(KIND));
   }
-  static constexpr int kSmem = 1024 + kStages * static_cast<int>(kStageBytes) +
-                               static_cast<int>(kOut) + (2 * kStages + 5) * 8 + 16 +
-                               (KIND == LK_FWD ? 128 * 12 : 0);
+  static constexpr int kSmem = 1024 + static_cast<int>(kRing + kOut) + (2 * kMaxStages + 5) * 8 +
+                               16 + (KIND == LK_FWD ? 128 * 12 : 0);
   static_assert(kSmem <= 232448, "shared memory per CTA");
 };
 
@@ -214,6 +219,7 @@ struct LossParams {
   int dw_tiles_m, dw_tiles;  // dW: row tiles of one rank, tiles over all
   Shares shares;           // DX: the tiles past full_tiles, by the first piece's K steps
   int a_rows;              // rows of an A box (K-major A: fewer than 128 when T is)
+  uint32_t stages, a_size, stage_size;  // FWD, DL: the ring (a_size: the A box, to 1 KiB)
   int k_rows;              // DW: tokens of a K step (fewer than 64 when T is)
   Raster order, dw_order;  // of the logit or dX tiles, and of the dW tiles
   FastDiv by_tiles_n, by_dw_tiles_m;  // tile columns / dW tile rows of a rank
@@ -456,18 +462,19 @@ template <int KIND, int CG>
 __global__ void __launch_bounds__(threads_of(KIND), 1)
 loss_gemm_kernel(const __grid_constant__ LossParams p) {
   using C = Cfg<KIND, CG>;
-  constexpr int kStages = C::kStages;
   constexpr int TM = C::kTileM;
   constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint8_t* sA = smem;
-  uint8_t* sB = smem + kStages * kABytes;
-  uint8_t* sO = sB + kStages * C::kBBytes;  // DL, DW: the epilogue warps' staging blocks
+  // The ring: stage s at s * stage_size, its A and, a_size on, its B.
+  const uint32_t kStages = KIND == LK_GRAD ? C::kMaxStages : p.stages;
+  const uint32_t a_size = KIND == LK_GRAD ? kABytes : p.a_size;
+  const uint32_t stage_size = KIND == LK_GRAD ? C::kStageBytes : p.stage_size;
+  uint8_t* sO = smem + C::kRing;  // DL, GRAD: the epilogue warps' staging blocks
   uint64_t* full = reinterpret_cast<uint64_t*>(sO + C::kOut);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* empty = full + C::kMaxStages;
+  uint64_t* tfull = empty + C::kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* mma_done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
@@ -481,7 +488,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
   const int npairs = gridDim.x / CG;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < C::kMaxStages; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
@@ -565,8 +572,8 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           }
           for (int it = tl.it_lo; it < tl.it_hi; ++it) {
             if (!W.wait_suspended(&empty[stage], phase ^ 1u)) return false;
-            uint8_t* a_dst = sA + stage * kABytes;
-            uint8_t* b_dst = sB + stage * C::kBBytes;
+            uint8_t* a_dst = smem + stage * stage_size;
+            uint8_t* b_dst = a_dst + a_size;
             if (!kPair || cta == 0) ptx::mbar_arrive_expect_tx(&full[stage], CG * stage_bytes);
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
               if constexpr (kPair)
@@ -635,17 +642,17 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         auto k_loop = [&](auto mn) {
           constexpr bool kDw = decltype(mn)::value;
           const uint32_t idesc = C::idesc(bn_cta * CG, kDw);
-          const uint64_t a_desc0 = ptx::smem_desc_sw128(ptx::smem_addr(sA), kDw ? kBoxBytes : 16, 1024);
+          const uint64_t a_desc0 = ptx::smem_desc_sw128(ptx::smem_addr(smem), kDw ? kBoxBytes : 16, 1024);
           const uint64_t b_desc0 =
-              ptx::smem_desc_sw128(ptx::smem_addr(sB), b_mn(KIND) ? kBoxBytes : 16, 1024);
+              ptx::smem_desc_sw128(ptx::smem_addr(smem) + a_size, b_mn(KIND) ? kBoxBytes : 16, 1024);
           for (int it = tl.it_lo; it < tl.it_hi; ++it) {
             if (!W.wait_suspended(&full[stage], phase)) return false;
             ptx::tc_fence_after();
             // The stage's descriptors; a K step of 16 on is 32 B within the
             // swizzled row (K-major) or 2 KiB (MN-major, 64-wide boxes 8 KiB
             // apart), added to the address field.
-            const uint64_t ad = a_desc0 + stage * (kABytes >> 4);
-            const uint64_t bd = b_desc0 + stage * (C::kBBytes >> 4);
+            const uint64_t ad = a_desc0 + stage * (stage_size >> 4);
+            const uint64_t bd = b_desc0 + stage * (stage_size >> 4);
             auto mma = [&](int kk) {
               const uint32_t accum = (it > tl.it_lo || kk > 0) ? 1u : 0u;
               const uint64_t a_kk = ad + kk * ((kDw ? 2048 : 32) >> 4);
@@ -1499,21 +1506,24 @@ int choose_cg(const fcc_opts* o, int64_t rows, int64_t single_tiles, int sms) {
   return rows > kBM && single_tiles > sms ? 2 : 1;
 }
 
-// Width of the logit tiles, a multiple of 32: the widest of the least (rounds
-// of tiles x width), counting 16 columns per tile for what does not depend on
-// the width.  One token on 32000 words: 143 tiles of 224 columns in one round,
-// not 125 of 256; a few thousand words spread over all SMs in tiles of 32.
+// Width of the logit tiles, a multiple of 32: the widest within 5 % of the least
+// (rounds of tiles x clocks per 16 of D).  An MMA takes about 82 + 0.18 width
+// clocks (a 128-wide one 0.81 of a 256-wide one's), so few rounds count most;
+// where each tile of W is read by one CTA only (one row of tiles), its share of
+// the memory bandwidth, 21 bytes per clock, is what counts: one token on 32000
+// words takes 143 tiles of 224 columns in one round, not 125 of 256 (48 us
+// against 54); 64 tokens on 131072 words four rounds of 224, not nine of 96 (313
+// against 325).
 int choose_width(int R, int64_t tiles_m, int64_t vn, int slots) {
-  int best = kBN;
-  int64_t least = INT64_MAX;
-  for (int w = kBN; w >= 32; w -= 32) {
-    const int64_t cost = cdiv(tiles_m * R * cdiv(vn, w), slots) * (w + 16);
-    if (cost < least) {
-      least = cost;
-      best = w;
-    }
-  }
-  return best;
+  auto cost = [&](int w) {
+    const double mma = 82 + 0.18 * w, mem = tiles_m == 1 ? w * 32 / 21.0 : 0;
+    return static_cast<double>(cdiv(tiles_m * R * cdiv(vn, w), slots)) * std::max(mma, mem);
+  };
+  double least = cost(kBN);
+  for (int w = kBN - 32; w >= 32; w -= 32) least = std::min(least, cost(w));
+  int w = kBN;
+  while (cost(w) > 1.05 * least) w -= 32;
+  return w;
 }
 
 // The shares of `rest` tiles of k steps over at most `slots` CTAs (pairs), of
@@ -1556,6 +1566,12 @@ cudaError_t launch_loss_gemm(LossParams& p, int cg, int sms, cudaStream_t st) {
     if (kGroupM * static_cast<int64_t>(p.R) * p.tiles_n > (1ll << 30)) return cudaErrorInvalidValue;
     p.order = raster_of(p.tiles_m, p.R * p.tiles_n, kGroupM);
     p.by_tiles_n = fast_div(p.tiles_n);
+    // (the MMA reads 128 rows of A from every stage, whatever lies past its box)
+    p.a_size = static_cast<uint32_t>(cdiv(p.a_rows, 8) * 1024);
+    p.stage_size = p.a_size + static_cast<uint32_t>(p.width / cg) * kBK * 2;
+    const uint32_t ring = cg == 2 ? Cfg<KIND, 2>::kRing : Cfg<KIND, 1>::kRing;
+    p.stages = std::min<uint32_t>((ring - kABytes) / p.stage_size + 1, ring / p.stage_size);
+    p.stages = std::min<uint32_t>(p.stages, cg == 2 ? Cfg<KIND, 2>::kMaxStages : Cfg<KIND, 1>::kMaxStages);
   } else {
     busy = std::max({p.full_tiles, p.shares.groups * p.shares.tiles + p.shares.helpers, p.dw_tiles});
   }
