@@ -866,12 +866,16 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             // Targets in the chunk; those before it are the other half's.
             while (tg.next < vc) targets_advance(tg);
             while (tg.next < vend) {
+              // v[at] by halving: 31 selections
               const int at = tg.next - vc;
-              float x = 0.f;
+              uint32_t h[16];
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (k == at) x = __uint_as_float(v[k]);
-              p.pick[row * p.K + tg.cur] = x;
+              for (int k = 0; k < 16; ++k) h[k] = at & 16 ? v[k + 16] : v[k];
+#pragma unroll
+              for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+                for (int k = 0; k < n; ++k) h[k] = at & n ? h[k + n] : h[k];
+              p.pick[row * p.K + tg.cur] = __uint_as_float(h[0]);
               targets_advance(tg);
             }
           } else {
