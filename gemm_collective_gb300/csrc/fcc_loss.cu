@@ -919,33 +919,25 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         if (KIND == LK_DL && tl.nt == p.tiles_n - 1) end = ((p.vn + 63) & ~63) - col0;
         if (row0 >= p.T) end = 0;  // (no token in the warp's rows)
 #pragma unroll 1
-        for (int c = 64 * half; c < end; c += 128) {
-          uint32_t v[2][32];
-          ptx::tmem_ld_32x32b_x32(taddr + c, v[0]);
-          ptx::tmem_ld_32x32b_x32(taddr + c + 32, v[1]);
+        for (int c = 64 * half; c < end; c += (c & 32) ? 96 : 32) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(taddr + c, v);
           ptx::tmem_ld_wait();
           const int nc = ncols - c;
-          if (KIND == LK_DL || nc > 0) chunk(v[0], c, nc);
-          if (KIND == LK_DL || nc > 32) chunk(v[1], c + 32, nc - 32);
+          if (KIND == LK_DL || nc > 0) chunk(v, c, nc);
           if constexpr (KIND == LK_DL) {
             buf_free();
-            stage_bf16<false>(buf, lane, 0, v[0]);
-            stage_bf16<false>(buf, lane, 1, v[1]);
-            const int blocks = end - c > 32 ? 2 : 1;
-            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, blocks);
+            stage_bf16<false>(buf, lane, 0, v);
+            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, 1);
             if (p.split && row0 < p.T) {  // what the rounding left
 #pragma unroll
-              for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const float x = __uint_as_float(v[b][k]);
-                  v[b][k] = __float_as_uint(
-                      x - __uint_as_float(ptx::pack_bf16x2(0.f, x) & 0xffff0000u));
-                }
+              for (int k = 0; k < 32; ++k) {
+                const float x = __uint_as_float(v[k]);
+                v[k] = __float_as_uint(x - __uint_as_float(ptx::pack_bf16x2(0.f, x) & 0xffff0000u));
+              }
               buf_free();
-              stage_bf16<false>(buf, lane, 0, v[0]);
-              stage_bf16<false>(buf, lane, 1, v[1]);
-              store_dl(&p.mapO[tl.rank], col0 + c, row0 + kSplit, blocks);
+              stage_bf16<false>(buf, lane, 0, v);
+              store_dl(&p.mapO[tl.rank], col0 + c, row0 + kSplit, 1);
             }
           }
         }
