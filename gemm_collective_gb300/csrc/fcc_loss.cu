@@ -487,11 +487,11 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
   const int pair = blockIdx.x / CG;
   const int npairs = gridDim.x / CG;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kMaxStages; ++s) {
-      ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 1);
-    }
+  if (threadIdx.x < kStages) {
+    ptx::mbar_init(&full[threadIdx.x], 1);
+    ptx::mbar_init(&empty[threadIdx.x], 1);
+    ptx::fence_mbar_init();
+  } else if (threadIdx.x == 32) {
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&tfull[b], 1);
       ptx::mbar_init(&tempty[b], kEpiWarps * CG);  // every epilogue warp of the pair
@@ -1443,18 +1443,29 @@ __global__ void __launch_bounds__(256) dx_finish_kernel(const __grid_constant__ 
     part0 = static_cast<long long>(t - a.full_tiles) * (a.shares.max_parts - 1);
   }
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& y) {
+    x.x += y.x;
+    x.y += y.y;
+    x.z += y.z;
+    x.w += y.w;
+  };
   if (in) {
+    const long long step = static_cast<long long>(a.tile_m) * kBN;  // from part to part
     for (int half = 0; half <= a.split; ++half) {  // (the rows kSplit on are dl's second half's)
-#pragma unroll 8
-      for (int i = SPLIT ? group : 0; i < n; i += kGroups) {
-        const float* src = i == 0 ? a.acc + (row + half * kSplit) * a.D + col
-                                  : a.parts + ((part0 + i - 1) * a.tile_m + rr + half * kSplit) * kBN + c;
-        const float4 y = __ldcs(reinterpret_cast<const float4*>(src));
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+      if (!SPLIT || group == 0)
+        add(__ldcs(reinterpret_cast<const float4*>(a.acc + (row + half * kSplit) * a.D + col)));
+      const float* src = a.parts + part0 * step + static_cast<long long>(rr + half * kSplit) * kBN + c;
+      int i = SPLIT ? group : 0;
+      for (; i + 7 * kGroups < n - 1; i += 8 * kGroups) {  // (eight loads in flight)
+        float4 y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          y[j] = __ldcs(reinterpret_cast<const float4*>(src + (i + j * kGroups) * step));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) add(y[j]);
       }
+#pragma unroll 4
+      for (; i < n - 1; i += kGroups) add(__ldcs(reinterpret_cast<const float4*>(src + i * step)));
     }
   }
   if constexpr (SPLIT) {
