@@ -197,6 +197,16 @@ Raster raster_of(int tiles_m, int tiles_n, int group) {
   r.last_height = fast_div(tiles_m - r.last_first);
   return r;
 }
+
+// A few tokens' products read W once each, and the next product reads it again
+// (forward, dl, dX, the next forward).  Evicted by age, a W larger than the L2
+// leaves nothing to hit; so a fixed part of its lines (the hardware's choice by
+// address) is held as usual and the rest marked to go first.  48 MB of W of 262
+// (96 tokens x 32000 x 4096): backward 159 -> 151 us, 526 MB 272 -> 268; 32 or 64
+// MB the same within 1 us, 96 MB 154.  Below kKeepFrom bytes of W it loses (100 MB:
+// 87 -> 88), past kKeepTo too (2.1 GB: 961 -> 974; 820 MB: 393 -> 390).
+constexpr double kKeepBytes = 48e6, kKeepFrom = 128e6, kKeepTo = 1e9;
+
 constexpr int kGroupM = 16;  // against 8: forward 5.33 -> 5.18 ms, backward unchanged; 32: slower
 
 struct LossParams {
@@ -223,6 +233,7 @@ struct LossParams {
   int k_rows;              // DW: tokens of a K step (fewer than 64 when T is)
   Raster order, dw_order;  // of the logit or dX tiles, and of the dW tiles
   FastDiv by_tiles_n, by_dw_tiles_m;  // tile columns / dW tile rows of a rank
+  float keep;              // the share of W's lines that the L2 is to hold, 0: no hint
   // tokens' targets: labels (cross entropy), or per token K sorted vocabulary
   // indices (INT_MAX past the last) and their teacher probabilities
   const int32_t* labels;
@@ -546,6 +557,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       // (a pair's bytes are counted on the leader's barriers)
       const uint32_t full0 = kPair ? ptx::mapa(ptx::smem_addr(full), 0) : 0u;
       bool ok = true;
+      const uint64_t policy = kPair || !(p.keep > 0) ? 0 : ptx::policy_keep(p.keep);
       while (ok && work.next(tl)) {
         const int m0 = tl.mt * TM + static_cast<int>(cta) * kBM;  // this CTA's A rows
         const int n0 = tl.nt * (bn_cta * CG) + static_cast<int>(cta) * bn_cta;  // and B columns
@@ -581,15 +593,21 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               else
                 ptx::tma_load_2d(dst, map, &full[stage], x, y);
             };
+            auto load_w = [&](uint8_t* dst, const CUtensorMap* map, int x, int y) {
+              if (!kPair && !kDw && p.keep > 0)
+                ptx::tma_load_2d_hint(dst, map, &full[stage], x, y, policy);
+              else
+                load(dst, map, x, y);
+            };
             load(a_dst, ma, ax, ay);
             if constexpr (kDw) load(a_dst + kBoxBytes, ma, ax, ay + p.tpad);
             if constexpr (b_mn(KIND)) {
               // W rows of the piece (dX) or tokens (dW) down, D across
 #pragma unroll
               for (int i = 0; i < C::kBNcta / 64; ++i)
-                load(b_dst + i * kBoxBytes, mb, n0 + 64 * i, by);
+                load_w(b_dst + i * kBoxBytes, mb, n0 + 64 * i, by);
             } else {
-              load(b_dst, mb, ax, p.v0 + n0);
+              load_w(b_dst, mb, ax, p.v0 + n0);
             }
             ++loads;
             if (++stage == kStages) {
@@ -1582,6 +1600,9 @@ cudaError_t launch_loss_gemm(LossParams& p, int cg, int sms, cudaStream_t st) {
   } else {
     busy = std::max({p.full_tiles, p.shares.groups * p.shares.tiles + p.shares.helpers, p.dw_tiles});
   }
+  const double w_bytes = 2.0 * p.R * p.vn * p.D;
+  p.keep = p.tiles_m == 1 && w_bytes > kKeepFrom && w_bytes < kKeepTo
+               ? static_cast<float>(kKeepBytes / w_bytes) : 0.f;
   const int grid = cg * static_cast<int>(std::min<int64_t>(slots, busy));
   return cg == 2 ? launch_kind<KIND, 2>(p, grid, st) : launch_kind<KIND, 1>(p, grid, st);
 }

@@ -240,6 +240,15 @@ __device__ __forceinline__ void tma_load_2d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// The fraction `keep` of the lines as usual, the others to be evicted first.
+__device__ __forceinline__ uint64_t policy_keep(float keep) {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_normal.L2::evict_first.b64 %0, %1;"
+               : "=l"(p)
+               : "f"(keep));
+  return p;
+}
+
 __device__ __forceinline__ uint64_t policy_evict_last() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
