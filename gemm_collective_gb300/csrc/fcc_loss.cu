@@ -29,11 +29,11 @@
 // tile, 32 KiB stages.  Each CTA is alone on its SM and loops over tiles.
 //
 // What bounds it, measured (tensor pipe busy, 4096 tokens x 32768 x 4096):
-// forward 96 %, dl 95 %, dX 92 %, dW 92 %.  A training-sized call then runs at
+// forward 96 %, dl 96 %, dX 94 %, dW 93 %.  A training-sized call then runs at
 // the chip's power limit, where what the waiting warps do not issue counts: with
 // every wait suspended in hardware instead of spinning the forward pass of 8192
 // tokens x 131072 x 4096 took 4.89 ms, spinning 5.07.  A few tokens are bound
-// by reading W: 64 tokens x 131072 x 8192 in 327 us, 6.6 TB/s.
+// by reading W: 64 tokens x 131072 x 8192 in 306-313 us, 6.9 TB/s.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -94,8 +94,8 @@ constexpr int kSplit = 64;
 constexpr int kEpiWarps = 8;   // two per TMEM lane quarter, each with every other 64 columns
 // Warps: producer, MMA, epilogue; FWD two more for the labels' own logits.
 constexpr int threads_of(int kind) { return 64 + 32 * kEpiWarps + (kind == LK_FWD ? 64 : 0); }
-// A warp's staging: 32 rows x 64 bf16 (dW: one block, 128-byte swizzle; dl:
-// two of 32 columns, 64-byte swizzle, so that a tile may end after either).
+// A warp's staging: 32 rows x 64 bf16 (dX, dW: 128-byte swizzle; dl: half of it,
+// 32 columns, 64-byte swizzle).
 constexpr uint32_t kOutBytes = 32 * 128;
 // bf16 results leave by TMA stores from shared memory.
 constexpr bool stages_out(int kind) { return kind != LK_FWD; }
@@ -380,7 +380,7 @@ struct Work {
 };
 
 // 32 f32 columns of each lane's row as bf16 into the warp's staging: half 0 / 1
-// of 64 columns (WIDE, 128-byte swizzle) or a block of 32 (64-byte swizzle), in
+// of 64 columns (WIDE, 128-byte swizzle) or all of 32 (64-byte swizzle), in
 // 16-byte pieces without bank conflicts.
 template <bool WIDE>
 __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
@@ -393,7 +393,7 @@ __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
     w.z = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
     w.w = ptx::pack_bf16x2(__uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
     const int at = WIDE ? lane * 128 + (((half * 4 + g) ^ (lane & 7)) << 4)
-                        : half * 2048 + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4);
+                        : lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4);
     *reinterpret_cast<uint4*>(buf + at) = w;
   }
 }
@@ -753,8 +753,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
       }
     };
     // The staged columns leave by TMA, issued by one lane: dW and dX, 64 columns
-    // to (x, y) of each of `n` maps; dl, `blocks` blocks of 32 columns from piece
-    // column x on.
+    // to (x, y) of each of `n` maps; dl, 32 columns from piece column x on.
     auto store_rows = [&](const CUtensorMap* maps, int n, int x, int y) {
       ptx::fence_proxy_async_smem();
       __syncwarp();
@@ -763,12 +762,11 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         ptx::bulk_commit();
       }
     };
-    auto store_dl = [&](const CUtensorMap* map, int x, int row, int blocks) {
+    auto store_dl = [&](const CUtensorMap* map, int x, int row) {
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        for (int b = 0; b < blocks; ++b, x += 32)
-          ptx::tma_store_2d(map, buf + 2048 * b, x & 63, (x >> 6) * p.tpad + row);
+        ptx::tma_store_2d(map, buf, x & 63, (x >> 6) * p.tpad + row);
         ptx::bulk_commit();
       }
     };
@@ -946,7 +944,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
           if constexpr (KIND == LK_DL) {
             buf_free();
             stage_bf16<false>(buf, lane, 0, v);
-            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0, 1);
+            if (row0 < p.T) store_dl(&p.mapO[tl.rank], col0 + c, row0);
             if (p.split && row0 < p.T) {  // what the rounding left
 #pragma unroll
               for (int k = 0; k < 32; ++k) {
@@ -955,7 +953,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               }
               buf_free();
               stage_bf16<false>(buf, lane, 0, v);
-              store_dl(&p.mapO[tl.rank], col0 + c, row0 + kSplit, 1);
+              store_dl(&p.mapO[tl.rank], col0 + c, row0 + kSplit);
             }
           }
         }
