@@ -148,6 +148,8 @@ def _ptrs(seq):
         return None
     if isinstance(seq, ctypes.Array):  # built once by ptr_array()
         return seq
+    if not isinstance(seq, (list, tuple)):
+        seq = list(seq)  # (an iterator can be walked only once)
     try:
         vals = [x.data_ptr() for x in seq]
     except AttributeError:
