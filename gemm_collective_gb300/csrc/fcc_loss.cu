@@ -398,10 +398,58 @@ __device__ __forceinline__ void stage_bf16(uint8_t* buf, int lane, int half,
   }
 }
 
-// c tanh(x / c) = c - 2c / (1 + e^{2x/c}), by the approximate exponential and
-// reciprocal: off by about c 2^-22 (an exponential past the range gives +-c).
-__device__ __forceinline__ float soft_cap(float x, float cap, float inv_cap) {
-  return fmaf(-2.f * cap, ptx::rcp_approx(1.f + ptx::ex2_approx(x * (2.f * kLog2e * inv_cap))), cap);
+// l = c tanh(x / c) of a lane's 32 logits, to 2^-20 of l for any c.  |x| < c/2:
+// the Taylor series x (1 - w/3 + 2 w^2/15 - ...), w = (x/c)^2, to w^6 (the first
+// term left out is 9e-8 of x).  Past it c - 2c / (1 + e^{2|x|/c}) with the sign of
+// x, by the approximate exponential and reciprocal (an exponential past the range
+// gives +-c); near zero that form would be off by c 2^-23, whatever x is.  A
+// warp's chunk is hardly ever past c/2, and the series alone, without special
+// functions, is also the faster form.  An element's result does not depend on the
+// others': both paths compute the series with the same roundings.
+__device__ __forceinline__ float soft_cap_series(float w) {
+  float s = fmaf(w, 21844.f / 6081075.f, -1382.f / 155925.f);
+  s = fmaf(s, w, 62.f / 2835.f);
+  s = fmaf(s, w, -17.f / 315.f);
+  s = fmaf(s, w, 2.f / 15.f);
+  s = fmaf(s, w, -1.f / 3.f);
+  return fmaf(s, w, 1.f);
+}
+__device__ __forceinline__ void soft_cap(uint32_t (&v)[32], float cap, float inv_cap) {
+  float far = 0.f;  // (a NaN is passed over: it stays one in either path)
+#pragma unroll
+  for (int k = 0; k < 32; k += 2)
+    far = ptx::max3(far, fabsf(__uint_as_float(v[k])), fabsf(__uint_as_float(v[k + 1])));
+  if (__all_sync(0xffffffffu, far * inv_cap < 0.5f)) {
+    const uint64_t inv2 = ptx::f32x2_pack(inv_cap, inv_cap);
+    auto both = [](float a) { return ptx::f32x2_pack(a, a); };
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const uint64_t x = ptx::f32x2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+      const uint64_t u = ptx::f32x2_mul(x, inv2);
+      const uint64_t w = ptx::f32x2_mul(u, u);
+      uint64_t s = ptx::f32x2_fma(w, both(21844.f / 6081075.f), both(-1382.f / 155925.f));
+      s = ptx::f32x2_fma(s, w, both(62.f / 2835.f));
+      s = ptx::f32x2_fma(s, w, both(-17.f / 315.f));
+      s = ptx::f32x2_fma(s, w, both(2.f / 15.f));
+      s = ptx::f32x2_fma(s, w, both(-1.f / 3.f));
+      s = ptx::f32x2_fma(s, w, both(1.f));
+      float y0, y1;
+      ptx::f32x2_unpack(ptx::f32x2_mul(x, s), y0, y1);
+      v[k] = __float_as_uint(y0);
+      v[k + 1] = __float_as_uint(y1);
+    }
+  } else {
+    const float step = 2.f * kLog2e * inv_cap;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float x = __uint_as_float(v[k]);
+      const float u = __fmul_rn(x, inv_cap);
+      const float near = __fmul_rn(x, soft_cap_series(__fmul_rn(u, u)));
+      const float rest = ptx::rcp_approx(1.f + ptx::ex2_approx(fabsf(x) * step));
+      const float past = copysignf(fmaf(-2.f * cap, rest, cap), x);
+      v[k] = __float_as_uint(fabsf(u) < 0.5f ? near : past);
+    }
+  }
 }
 
 // (m, s) of both: base-2 maximum and sum.
@@ -834,11 +882,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               v[k + 1] = __float_as_uint(x1);
             }
           }
-          if (p.cap > 0.f) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              v[k] = __float_as_uint(soft_cap(__uint_as_float(v[k]), p.cap, p.inv_cap));
-          }
+          if (p.cap > 0.f) soft_cap(v, p.cap, p.inv_cap);
           const int vc = vcol0 + c, vend = vc + min(32, nc);
           if constexpr (KIND == LK_FWD) {
             if (nc < 32) {

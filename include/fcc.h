@@ -344,7 +344,8 @@ fcc_status fcc_ring_attention(int R, const void *const *Q, const void *const *K,
  * every rank holds a copy of the tokens' hidden states, and the softmax
  * statistics are all-reduced:
  *   x_v = X[r][t] . W[r][v - r*V/R]   (f32)
- *   l_v = x_v, or softcap * tanh(x_v / softcap) when softcap > 0
+ *   l_v = x_v, or softcap * tanh(x_v / softcap) when softcap > 0 (the cap's own
+ *         error is below 2^-20 of l_v, whatever softcap)
  *   lse[t]  = log sum_v exp(l_v)
  *   loss[t] = lse - (1 - smoothing) l_y - smoothing / V * sum_v l_v
  *             + z_weight * lse^2,                     y = labels[t]
