@@ -17,8 +17,10 @@
 // and the logits at the token's targets; one partial per (tile, token) goes to
 // memory and loss_combine_kernel merges the partials of all ranks: the
 // all-reduce of the softmax statistics.
-// Backward, per piece of the vocabulary: the same product again, whose
-// epilogue turns logits into dl (bf16) for the piece; then, in one launch,
+// Backward: target_logit_kernel computes the logits of the labels (or of a
+// teacher's heavy entries) by themselves, as the forward pass did; then, per
+// piece of the vocabulary, the same product again, whose epilogue turns logits
+// into dl (bf16) for the piece; then, in one launch,
 // dX += dl W (the K loop runs over all ranks: the all-reduce) and dW = dl^T X.
 // Only one piece of dl is ever held.
 //
@@ -247,15 +249,15 @@ struct LossParams {
   int ignore_index;
   float cap, inv_cap;      // soft cap, 0 = none
   float c2;                // log2(e) / tau
-  float grow;              // FWD: what the tensor core's sums lose on average, see kCutPerStep
+  float grow;              // what the tensor core's sums lose on average, see kCutPerStep
   float tau, smoothing, z;
   // FWD
   float2* part;            // [R * tiles_n][T]: base-2 maximum and sum
   float* part_sum;         // the same layout: sum of the logits (smoothing), or NULL
   float* pick;             // [T, K] logits at the targets
-  const void* X[FCC_MAX_RANKS];   // the matrices themselves and the labels' logits
-  const void* Wr[FCC_MAX_RANKS];  // (or the heavy entries') logits, uncapped, computed from them
-  float* own_logit;        // [T, K]
+  const void* X[FCC_MAX_RANKS];   // the matrices themselves and the labels' (or the heavy
+  const void* Wr[FCC_MAX_RANKS];  // entries') logits computed from them, DL: capped
+  float* own_logit;               // [T, K]
   const int16_t* heavy;    // [T, kMaxHeavy]: a token's heavy entries' places, then -1
   // DL
   const float* lse[FCC_MAX_RANKS];
@@ -452,6 +454,18 @@ __device__ __forceinline__ void soft_cap(uint32_t (&v)[32], float cap, float inv
   }
 }
 
+// v[at] by halving: 31 selections.
+__device__ __forceinline__ float pick32(const uint32_t (&v)[32], int at) {
+  uint32_t h[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) h[k] = at & 16 ? v[k + 16] : v[k];
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int k = 0; k < n; ++k) h[k] = at & n ? h[k + n] : h[k];
+  return __uint_as_float(h[0]);
+}
+
 // (m, s) of both: base-2 maximum and sum.
 __device__ __forceinline__ void merge(float& m, float& s, float m1, float s1) {
   const float mn = fmaxf(m, m1);
@@ -466,14 +480,16 @@ struct Token {
   int y;       // the label, or the place of the first target at or past the tile
   int first;   // DL, teacher: the token's first target (INT_MAX: it has none)
   float lse, g;
+  float own;   // DL, labels: the label's logit by itself
 };
 
 template <int KIND>
 __device__ __forceinline__ Token token_of(const LossParams& p, const Tile& tl, long long row) {
-  Token k{0, INT_MAX, 0.f, 0.f};
+  Token k{0, INT_MAX, 0.f, 0.f, 0.f};
   if (row >= p.T) return k;
   if (p.labels != nullptr) {
     k.y = __ldg(p.labels + row);
+    if (KIND == LK_DL) k.own = __ldg(p.own_logit + row);
   } else {
     k.y = __ldg(p.hit_start + row * p.start_ld +
                 (tl.rank * p.npieces + p.piece) * p.piece_tiles + tl.nt);
@@ -870,17 +886,15 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
         float m2 = -INFINITY, sum = 0.f, lsum = 0.f;  // FWD: base-2 maximum, sum; plain sum
         // One chunk of 32 columns from c on, of which nc > 0 exist.
         auto chunk = [&](uint32_t (&v)[32], int c, int nc) {
-          if constexpr (KIND == LK_FWD) {
-            const uint64_t grow2 = ptx::f32x2_pack(p.grow, p.grow);
+          const uint64_t grow2 = ptx::f32x2_pack(p.grow, p.grow);
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float x0, x1;
-              ptx::f32x2_unpack(
-                  ptx::f32x2_mul(ptx::f32x2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
-                                 grow2), x0, x1);
-              v[k] = __float_as_uint(x0);
-              v[k + 1] = __float_as_uint(x1);
-            }
+          for (int k = 0; k < 32; k += 2) {
+            float x0, x1;
+            ptx::f32x2_unpack(
+                ptx::f32x2_mul(ptx::f32x2_pack(__uint_as_float(v[k]), __uint_as_float(v[k + 1])),
+                               grow2), x0, x1);
+            v[k] = __float_as_uint(x0);
+            v[k + 1] = __float_as_uint(x1);
           }
           if (p.cap > 0.f) soft_cap(v, p.cap, p.inv_cap);
           const int vc = vcol0 + c, vend = vc + min(32, nc);
@@ -926,16 +940,7 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
             // Targets in the chunk; those before it are the other half's.
             while (tg.next < vc) targets_advance(tg);
             while (tg.next < vend) {
-              // v[at] by halving: 31 selections
-              const int at = tg.next - vc;
-              uint32_t h[16];
-#pragma unroll
-              for (int k = 0; k < 16; ++k) h[k] = at & 16 ? v[k + 16] : v[k];
-#pragma unroll
-              for (int n = 8; n > 0; n >>= 1)
-#pragma unroll
-                for (int k = 0; k < n; ++k) h[k] = at & n ? h[k + n] : h[k];
-              p.pick[row * p.K + tg.cur] = __uint_as_float(h[0]);
+              p.pick[row * p.K + tg.cur] = pick32(v, tg.next - vc);
               targets_advance(tg);
             }
           } else {
@@ -945,10 +950,29 @@ loss_gemm_kernel(const __grid_constant__ LossParams p) {
               const float pv = ptx::ex2_approx(fmaf(__uint_as_float(v[k]), p.c2, -off2));
               d[k] = fmaf(ca, pv, -cb);
             }
+            // Targets.  A label's or heavy entry's logit known by itself takes the
+            // place of the tensor core's, as it did in lse: of a confident token
+            // p - 1 leaves little but the difference of the two.
             while (tg.next < vc) targets_advance(tg);
             while (tg.next < vend) {
               const int at = tg.next - vc;
-              const float w = p.labels != nullptr ? cw : cw * __ldg(p.hit_q + row * p.K + tg.cur);
+              float w = cw, l = tok.own;
+              bool exact = p.labels != nullptr;
+              if (!exact) {
+                const float q = __ldg(p.hit_q + row * p.K + tg.cur);
+                l = __ldg(p.own_logit + row * p.K + tg.cur);  // (unset if not heavy)
+                w = cw * q;
+                exact = q >= kHeavy;
+              }
+              if (exact) {
+                // (of an index given twice, the second time changes nothing)
+                const float x = pick32(v, at);
+                w -= ca * (ptx::ex2_approx(fmaf(l, p.c2, -off2)) -
+                           ptx::ex2_approx(fmaf(x, p.c2, -off2)));
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (k == at) v[k] = __float_as_uint(l);
+              }
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (k == at) d[k] -= w;
@@ -1343,6 +1367,82 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const Teach
   }
 }
 
+// ------------------------------------------------------------ target logits
+// The backward pass's own logits of the labels or heavy entries, capped: X_t .
+// W_i in f32 with short chains of additions, as the forward pass's side warps
+// compute them.  There is no product to hide behind, so a token is given
+// 2^log_warps warps of a CTA's eight, enough for up to four vectors of a row a
+// thread, all in flight at once.  Bound by reading the rows.
+struct TargetArgs {
+  const void* X[FCC_MAX_RANKS];
+  const void* W[FCC_MAX_RANKS];
+  const int32_t* labels;
+  const int32_t* hit_idx;
+  const int16_t* heavy;
+  float* own_logit;
+  float cap;
+  int T, D, K, V, Vs, ignore_index, log_warps;
+};
+
+__global__ void __launch_bounds__(256) target_logit_kernel(const __grid_constant__ TargetArgs a) {
+  ptx::griddep_wait();  // launched with programmatic stream serialization
+  ptx::griddep_launch_dependents();
+  __shared__ float sums[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int group = 32 << a.log_warps;  // threads of a token
+  const int sub = threadIdx.x & (group - 1);
+  const long long t = (static_cast<long long>(blockIdx.x) << (3 - a.log_warps)) +
+                      (warp >> a.log_warps);
+  const int vecs = a.D / 8;
+  const int entries = a.labels != nullptr ? 1 : kMaxHeavy;
+  for (int j = 0; j < entries; ++j) {
+    int y = -1;
+    long long at = t;
+    if (t < a.T) {
+      if (a.labels != nullptr) {
+        y = __ldg(a.labels + t);
+        if (y == a.ignore_index || y >= a.V) y = -1;
+      } else {
+        const int k = __ldg(a.heavy + t * kMaxHeavy + j);
+        if (k >= 0) {
+          at = t * a.K + k;
+          y = __ldg(a.hit_idx + at);
+        }
+      }
+    }
+    // (a token's heavy entries come first, then -1)
+    if (!__syncthreads_or(y >= 0)) break;
+    float s[4] = {};
+    if (y >= 0) {
+      const int r = y / a.Vs;
+      const uint4* x = reinterpret_cast<const uint4*>(a.X[r]) + t * vecs;
+      const uint4* w =
+          reinterpret_cast<const uint4*>(a.W[r]) + static_cast<long long>(y - r * a.Vs) * vecs;
+#pragma unroll 4
+      for (int i = sub; i < vecs; i += group) {
+        const uint4 b = __ldg(x + i), c = __ldg(w + i);
+        const uint32_t bu[4] = {b.x, b.y, b.z, b.w};
+        const uint32_t cu[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s[k] = fmaf(__uint_as_float(bu[k] << 16), __uint_as_float(cu[k] << 16), s[k]);
+          s[k] = fmaf(__uint_as_float(bu[k] & 0xffff0000u), __uint_as_float(cu[k] & 0xffff0000u),
+                      s[k]);
+        }
+      }
+    }
+    float d = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    if (lane == 0) sums[warp] = d;
+    __syncthreads();
+    if (sub == 0 && y >= 0) {
+      for (int i = 1; i < 1 << a.log_warps; ++i) d += sums[warp + i];
+      a.own_logit[at] = a.cap > 0.f ? a.cap * tanhf(d / a.cap) : d;
+    }
+  }
+}
+
 // ------------------------------------------------------------------- combine
 // Merges the tiles' partials of a token over all ranks (in a fixed order) and
 // writes its lse and loss to every rank.  A CTA of 256 threads takes `tok`
@@ -1703,8 +1803,8 @@ int usable_sms(const fcc_opts* o) {
   return o != nullptr && o->max_ctas > 0 ? std::min(sms, o->max_ctas) : sms;
 }
 
-// Scratch layout.  Forward: partials, target logits; distillation also the
-// sorted teacher entries.  Backward: the piece's dl, the f32 sums of dX.
+// Scratch layout.  Target logits; distillation also the sorted teacher entries.
+// Forward: partials.  Backward: the piece's dl, the f32 sums of dX.
 struct Plan {
   size_t hit_idx = 0, hit_q = 0, hit_start = 0, heavy = 0, pick = 0, own_logit = 0, part = 0, part_sum = 0;
   size_t dl = 0, acc = 0, parts = 0, total = 0;
@@ -1752,11 +1852,11 @@ Plan plan_of(int R, int64_t T, int64_t V, int64_t D, int K, bool grad, bool smoo
     p.heavy = off;
     off += up256(static_cast<size_t>(T) * kMaxHeavy * 2);
   }
+  p.own_logit = off;
+  off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
   if (!grad) {
     p.nparts = static_cast<int>(R * cdiv(Vs, p.width));
     p.pick = off;
-    off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
-    p.own_logit = off;
     off += up256(static_cast<size_t>(T) * std::max(K, 1) * 4);
     p.part = off;
     off += up256(static_cast<size_t>(p.nparts) * T * 8);
@@ -1807,6 +1907,11 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
     p.hit_start = reinterpret_cast<uint16_t*>(base + pl.hit_start);
     p.heavy = reinterpret_cast<int16_t*>(base + pl.heavy);
   }
+  p.own_logit = reinterpret_cast<float*>(base + pl.own_logit);
+  for (int r = 0; r < c.R; ++r) {
+    p.X[r] = c.X[r];
+    p.Wr[r] = c.W[r];
+  }
   p.ignore_index = c.ignore_index;
   p.cap = c.softcap;
   p.inv_cap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
@@ -1847,6 +1952,31 @@ cudaError_t launch_teacher(const Call& c, const Plan& pl, char* base, int* statu
                     dim3(32 * kTeacherWarps), 0, c.st, 1u, a);
 }
 
+// The labels' or heavy entries' own logits, for the backward pass.
+cudaError_t launch_targets(const Call& c, const LossParams& p) {
+  TargetArgs a;
+  std::memset(&a, 0, sizeof(a));
+  for (int r = 0; r < c.R; ++r) {
+    a.X[r] = c.X[r];
+    a.W[r] = c.W[r];
+  }
+  a.labels = p.labels;
+  a.hit_idx = p.hit_idx;
+  a.heavy = p.heavy;
+  a.own_logit = p.own_logit;
+  a.cap = p.cap;
+  a.T = p.T;
+  a.D = p.D;
+  a.K = p.K;
+  a.V = static_cast<int>(c.V);
+  a.Vs = p.Vs;
+  a.ignore_index = p.ignore_index;
+  while (a.log_warps < 3 && (128 << a.log_warps) < p.D / 8) ++a.log_warps;
+  const int64_t tokens = 8 >> a.log_warps;  // of a CTA
+  return launch_pdl(target_logit_kernel, dim3(static_cast<unsigned>(cdiv(c.T, tokens))), dim3(256),
+                    0, c.st, 1u, a);
+}
+
 // Tensor maps of the logit product: X rows and W rows, both K-major.
 fcc_status logit_maps(LossParams& p, const Call& c, const Plan& pl) {
   for (int r = 0; r < c.R; ++r) {
@@ -1880,11 +2010,6 @@ fcc_status forward(const Call& c, float* const* loss, float* const* lse) {
   p.part = reinterpret_cast<float2*>(base + pl.part);
   p.part_sum = c.smoothing > 0.f ? reinterpret_cast<float*>(base + pl.part_sum) : nullptr;
   p.pick = reinterpret_cast<float*>(base + pl.pick);
-  p.own_logit = reinterpret_cast<float*>(base + pl.own_logit);
-  for (int r = 0; r < c.R; ++r) {
-    p.X[r] = c.X[r];
-    p.Wr[r] = c.W[r];
-  }
   if ((s = logit_maps(p, c, pl)) != FCC_OK) return s;
   uint64_t launches = 2;
   if (c.K > 0) {
@@ -1959,6 +2084,8 @@ fcc_status backward(const Call& c, const float* const* lse, const float* dloss, 
     if (launch_teacher(c, pl, base, status) != cudaSuccess) return FCC_ERR_CUDA;
     ++launches;
   }
+  if (launch_targets(c, base_p) != cudaSuccess) return FCC_ERR_CUDA;
+  ++launches;
   LossParams p_dl = base_p, p = base_p;
   if ((s = logit_maps(p_dl, c, pl)) != FCC_OK) return s;
   // Gradient tiles: a CTA pair each when there are more than 128 tokens.

@@ -62,3 +62,72 @@ def test_capped_logits_that_are_not_finite(cap):
     assert torch.isnan(lse[0][7])
     rest = [t for t in range(T) if t != 7]
     assert torch.isfinite(lse[0][rest]).all() and torch.isfinite(loss[0][rest]).all()
+
+
+def _confident(T, D, l, second, sparse, seed):
+    """X, W, labels: token t's product with its label 2t is about l, with 2t + 1 `second` times
+    that, with all others near 0.  Dense: every term of the label's product is positive;
+    sparse: only one is not zero."""
+    g = torch.Generator().manual_seed(seed)
+    V = 2 * T + 40
+    if sparse:
+        W, X = torch.zeros(V, D), torch.zeros(T, D)
+        at = (torch.arange(T) * 37) % D
+        X[torch.arange(T), at] = 5.0
+        W[2 * torch.arange(T), at] = l / 5.0
+    else:
+        W = torch.randn(V, D, generator=g) / D ** 0.5
+        X = W[0:2 * T:2] * (l / (W[0:2 * T:2] ** 2).sum(1, keepdim=True))
+    W[1:2 * T:2] = W[0:2 * T:2] * second
+    return X.bfloat16(), W.bfloat16(), 2 * torch.arange(T, dtype=torch.int32), V
+
+
+@pytest.mark.parametrize("K,cap", [(0, 0.0), (1, 0.0), (0, 40.0)])
+@pytest.mark.parametrize("T", [1, 5, 100])
+@pytest.mark.parametrize("sparse", [False, True])
+@pytest.mark.parametrize("D,l,rest", [(4096, 22.0, 1e-3), (8192, 25.0, 1e-3), (8192, 25.0, 1e-4)])
+def test_a_confident_tokens_gradient_keeps_its_digits(D, l, rest, sparse, T, K, cap):
+    """dl at a label of probability p is p - 1, so that an error e of its logit against lse
+    is an error e / (1 - p) of dl.  The label's logit is summed in f32 by 256 threads
+    (D / 2048 vectors of 8, four sums each: D / 1024 additions, then 2 + 5 + 3, and a cap's
+    2^-20 of it): off by (10 + D / 1024) 2^-24 of sum |x w|; lse by 2^-20 (2 + |lse|).
+    The bound of the other columns is the header's."""
+    uncap = (lambda a: cap * np.arctanh(a / cap)) if cap else (lambda a: a)
+    second = uncap(l + np.log(rest)) / uncap(l)
+    X, W, y, V = _confident(T, D, uncap(l), second, sparse, 7 * T + D)
+    Xd, Wd, yn = X.double().numpy(), W.double().numpy(), y.numpy()
+    x, w = X.cuda(), W.cuda()
+    up = torch.ones(T, device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dX, dW = torch.empty_like(x), torch.empty_like(w)
+    if K:
+        i, q = y[:, None].contiguous().cuda(), torch.zeros(T, 1, device="cuda")
+        fcc.fcc_linear_distill(1, [x], [w], i, q, T, V, D, 1, [loss], [lse], softcap=cap)
+        fcc.fcc_linear_distill_grad(1, [x], [w], i, q, [lse], up, T, V, D, 1, [dX], [dW], softcap=cap)
+    else:
+        fcc.fcc_linear_xent(1, [x], [w], y.cuda(), T, V, D, [loss], [lse], softcap=cap)
+        fcc.fcc_linear_xent_grad(1, [x], [w], y.cuda(), [lse], up, T, V, D, [dX], [dW], softcap=cap)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    d = losses.xent_dlogits(Xd, Wd, yn, np.ones(T), softcap=cap)
+    rl, rs = losses.xent(Xd, Wd, yn, softcap=cap)
+    lg = losses.logits(Xd, Wd, cap)
+    p = np.exp(lg - rs[:, None])
+    rows = np.arange(T)
+    assert (1 - p[rows, yn] < 10 * rest).all() and (1 - p[rows, yn] > 1e-5).all()
+    mags = np.abs(Xd) @ np.abs(Wd).T
+    err = D * 2.0 ** -23 * mags
+    err[rows, yn] = (10 + D / 1024) * 2.0 ** -24 * mags[rows, yn]
+    err += 2.0 ** -20 * np.abs(lg) * (cap > 0)
+    tl = 2.0 ** -20 * (2 + np.abs(rs)) + (p * err).sum(1)
+    ed = p * (err + tl[:, None] + 2.0 ** -20)
+    if cap:  # (the factor 1 - (l / cap)^2 and its own error)
+        f = 1 - (lg / cap) ** 2
+        raw_d = np.abs(d / f)
+        ed = ed * f + raw_d * (2 * np.abs(lg) / cap ** 2 * err + 2.0 ** -22)
+    ed = ed + np.abs(d) * (2.0 ** -16 if T <= 64 else 2.0 ** -8)
+    gX, gW = losses.gradients(d, Xd, Wd)
+    tW = ed.T @ np.abs(Xd) + T * 2.0 ** -23 * (np.abs(d).T @ np.abs(Xd))
+    tX = ed @ np.abs(Wd) + V * 2.0 ** -23 * (np.abs(d) @ np.abs(Wd))
+    at = yn  # the labels' rows of dW: dl at the label times the token's X
+    within(dW[at], gW[at], (tW + 2.0 ** -8 * (np.abs(gW) + tW))[at], "dW at the labels")
+    within(dX, gX, tX + 2.0 ** -8 * (np.abs(gX) + tX), "dX")
