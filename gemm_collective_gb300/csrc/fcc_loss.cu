@@ -76,13 +76,19 @@ enum LossKind : int {
 constexpr bool b_mn(int kind) { return kind == LK_GRAD; }
 
 // The tensor core cuts its accumulator off instead of rounding it, once for
-// every 16 of D, so a logit comes out smaller by about 1.6e-8 of itself per
-// step: 4.2e-6 at D = 4096, 8.3e-6 at 8192, measured on sums whose terms agree
-// in sign, and as much on average on sums of random terms (in expectation a
-// partial sum is the same part of the final one).  The forward pass multiplies
-// it back.  Adding up shorter chains in registers costs 4 % (chains of 1024)
-// to 34 % (of 256) of the forward pass.
+// every 16 of D, so a logit comes out too small.  By how much depends on the
+// terms; measured on this chip, of the logit, per 16 of D: 1.4e-8 to 1.6e-8 where
+// the products have random signs and outweigh their sum, as a head's do, at
+// every D from 1024 to 131072; 0 where a single product is not zero; 4e-8 to
+// 9e-8 where all products are positive; up to 1.6e-7 where the first outweighs
+// the sum of the rest.  Every logit is multiplied by what the first kind loses
+// (8.2e-6 at D = 8192): that is an error of as much where nothing was cut off, and
+// a part of the loss where more was.  No D past the measured ones adds to it, so
+// it is 1.3e-4 at most.  Adding up shorter chains in registers needs no such
+// assumption; it costs 4 % (chains of 1024) to 34 % (of 256) of the forward pass.
+// The logits that a loss takes from lse one by one are summed by themselves.
 constexpr float kCutPerStep = 1.6e-8f;
+constexpr int64_t kCutSteps = 131072 / 16;
 constexpr float kHeavy = 0.125f;  // a teacher entry whose logit is also computed by itself
 constexpr int kMaxHeavy = 8;      // (a token has at most so many: their sum is 1)
 
@@ -1917,7 +1923,7 @@ void common_params(LossParams& p, const Call& c, const Plan& pl, char* base, int
   p.inv_cap = c.softcap > 0.f ? 1.f / c.softcap : 0.f;
   p.tau = c.tau;
   p.c2 = static_cast<float>(1.4426950408889634 / c.tau);
-  p.grow = 1.f + kCutPerStep * static_cast<float>(cdiv(c.D, 16));
+  p.grow = 1.f + kCutPerStep * static_cast<float>(std::min(cdiv(c.D, 16), kCutSteps));
   p.smoothing = c.smoothing;
   p.z = c.z;
   p.status = status;

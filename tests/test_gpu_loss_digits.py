@@ -131,3 +131,25 @@ def test_a_confident_tokens_gradient_keeps_its_digits(D, l, rest, sparse, T, K, 
     at = yn  # the labels' rows of dW: dl at the label times the token's X
     within(dW[at], gW[at], (tW + 2.0 ** -8 * (np.abs(gW) + tW))[at], "dW at the labels")
     within(dX, gX, tX + 2.0 ** -8 * (np.abs(gX) + tX), "dX")
+
+
+@pytest.mark.parametrize("D", [1024, 8192, 1 << 17, 1 << 20])
+def test_rows_that_nothing_is_cut_off_from(D):
+    """Logits of a single product each, which the tensor core's sum holds exactly: what the
+    forward pass multiplies back, 1.6e-8 for every 16 of D up to 131072, is then the
+    error itself and bounds it (and 2^-20 (2 + |lse|) for lse's own rounding)."""
+    T, V = 8, 24
+    X, W = torch.zeros(T, D), torch.zeros(V, D)
+    at = (torch.arange(T) * 1037) % D
+    X[torch.arange(T), at] = 2.0
+    W[torch.arange(T), at] = 100.0 + torch.arange(T)   # (the largest logits: word t for token t)
+    X, W = X.bfloat16(), W.bfloat16()
+    y = torch.arange(T, dtype=torch.int32) + T         # (labels elsewhere)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    fcc.fcc_linear_xent(1, [X.cuda()], [W.cuda()], y.cuda(), T, V, D, [loss], [lse])
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    rl, rs = losses.xent(X.double().numpy(), W.double().numpy(), y.numpy())
+    tol = (1.6e-8 * (min(D, 1 << 17) / 16) * rs + 2.0 ** -20 * (2 + rs))
+    within(lse, rs, tol, "lse")
+    within(loss, rl, tol, "loss")
+
