@@ -1536,9 +1536,13 @@ __global__ void __launch_bounds__(256) loss_combine_kernel(const CombineArgs a) 
         const int id = __ldg(a.hit_idx + at);
         const float q = id != INT_MAX ? __ldg(a.hit_q + at) : 0.f;
         if (q == 0.f) continue;  // (an entry of probability 0 adds nothing)
-        // (an index given twice is in the sum once)
-        const bool again = k > 0 && __ldg(a.hit_idx + at - 1) == id && __ldg(a.hit_q + at - 1) >= kHeavy;
-        gap += q * (logf(q) + target(at, q >= kHeavy, !again));
+        // (an index given often is in the sum once: with its first heavy entry,
+        // whatever lies between)
+        const bool exact = q >= kHeavy;
+        bool again = false;
+        for (long long o = at - 1; exact && !again && o >= t * a.K && __ldg(a.hit_idx + o) == id; --o)
+          again = __ldg(a.hit_q + o) >= kHeavy;
+        gap += q * (logf(q) + target(at, exact, !again));
       }
     }
   }

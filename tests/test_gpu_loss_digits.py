@@ -153,3 +153,27 @@ def test_rows_that_nothing_is_cut_off_from(D):
     within(lse, rs, tol, "lse")
     within(loss, rl, tol, "loss")
 
+
+@pytest.mark.parametrize("q", [(0.5, 0.05, 0.45), (0.05, 0.5, 0.45), (0.3, 0.02, 0.02, 0.3, 0.03, 0.33),
+                               (0.2,) * 5])
+def test_an_index_given_often_is_in_the_sum_once(q):
+    """Heavy entries of one index with light ones between them: the sum takes the logit that
+    is known by itself once.  Its f32 sum over 32 lanes of D / 8 products has at most D / 128
+    + 7 additions, each off by 2^-24 of sum |x w|."""
+    T, D, K = 6, 8192, len(q) + 2
+    X, W, y, V = _confident(T, D, 25.0, 0.7, False, 3)
+    idx = torch.stack([torch.cat([y[t:t + 1].repeat(len(q)), torch.tensor([(t + 5) % V, -1])])
+                       for t in range(T)]).int()
+    te = torch.log(torch.tensor([[*q, 0.01, 1.0]])).repeat(T, 1)
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    fcc.fcc_linear_distill(1, [X.cuda()], [W.cuda()], idx.cuda(), te.cuda(), T, V, D, K, [loss], [lse])
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    Xd, Wd = X.double().numpy(), W.double().numpy()
+    rl, rs = losses.distill(Xd, Wd, idx.numpy(), te.numpy())
+    mags = np.abs(Xd) @ np.abs(Wd).T
+    p = np.exp(losses.logits(Xd, Wd) - rs[:, None])
+    err = D * 2.0 ** -23 * mags
+    err[np.arange(T), y.numpy()] *= (D / 128 + 7) / (2 * D)
+    tl = (p * err).sum(1) + 2.0 ** -20 * (2 + rs)
+    within(lse, rs, tl, "lse")
+
