@@ -1784,7 +1784,8 @@ fcc_status check_call(const Call& c) {
   for (int r = 0; r < c.R; ++r)
     if (!al(c.X[r], 16) || !al(c.W[r], 16)) return FCC_ERR_INVALID;
   if (c.in != FCC_BF16 && c.in != FCC_F16 && c.in != FCC_F32) return FCC_ERR_INVALID;
-  if (!(c.softcap >= 0.f) || std::isinf(c.softcap)) return FCC_ERR_INVALID;
+  // (a cap's double and reciprocal, a temperature's square: normal numbers)
+  if (!(c.softcap == 0.f || (c.softcap >= 0x1p-126f && c.softcap <= 0x1p126f))) return FCC_ERR_INVALID;
   if (c.K == 0) {
     if (!al(c.labels, 4)) return FCC_ERR_INVALID;
     if (!(c.smoothing >= 0.f && c.smoothing < 1.f)) return FCC_ERR_INVALID;
@@ -1792,7 +1793,7 @@ fcc_status check_call(const Call& c) {
   } else {
     if (c.K < 1 || c.K > FCC_MAX_TEACHER) return FCC_ERR_INVALID;
     if (!al(c.teacher_idx, 4) || !al(c.teacher, 4)) return FCC_ERR_INVALID;
-    if (!(c.tau > 0.f) || std::isinf(c.tau)) return FCC_ERR_INVALID;
+    if (!(c.tau >= 0x1p-63f && c.tau <= 0x1p63f)) return FCC_ERR_INVALID;
   }
   const fcc_opts* o = c.opts;
   if (o != nullptr) {

@@ -356,9 +356,9 @@ fcc_status fcc_ring_attention(int R, const void *const *Q, const void *const *K,
  * X[r]: [T,D] bf16 (the same values in every rank; entries may be one
  * buffer); W[r]: [V/R,D] bf16; labels: [T] int32 (device); loss[r], lse[r]:
  * [T] f32.  T, V >= 1 (any, odd ones too), V % R == 0, D % 8 == 0,
- * 0 <= smoothing < 1, z_weight >= 0.  Logits that are not finite give a loss
- * that is not.  The label's logit is summed in f32 by itself; the others come
- * from the tensor cores, whose sums lose a little of themselves: they are scaled
+ * 0 <= smoothing < 1, z_weight >= 0, softcap 0 or from 2^-126 to 2^126.
+ * Logits that are not finite give a loss that is not.  The label's logit is
+ * summed in f32 by itself; the others come from the tensor cores, whose sums lose a little of themselves: they are scaled
  * by what sums of random products lose (1.6e-8 for every 16 of D, up to D =
  * 131072), and are off by as much where nothing was lost, by up to 8e-8 for
  * every 16 of D where all of a logit's products are positive and 1.5e-7 where
@@ -404,8 +404,8 @@ fcc_status fcc_linear_xent_grad(int R, const void *const *X, const void *const *
  * either and records FCC_ERR_INVALID.  An index given twice counts twice.
  * The gradient is dl_v = dloss temperature (exp(l_v / temperature - lse)
  * - sum_k q_k [v = i_k]).  teacher_idx, teacher_logits: [T,topk] int32 / f32
- * (device), 1 <= topk <= FCC_MAX_TEACHER, in any order; temperature > 0.  All
- * else as in fcc_linear_xent and fcc_linear_xent_grad.
+ * (device), 1 <= topk <= FCC_MAX_TEACHER, in any order; temperature from 2^-63
+ * to 2^63.  All else as in fcc_linear_xent and fcc_linear_xent_grad.
  */
 fcc_status fcc_linear_distill(int R, const void *const *X, const void *const *W,
                               const int32_t *teacher_idx, const float *teacher_logits, int64_t T,
