@@ -27,8 +27,9 @@
 // All products run on tcgen05 (bf16 x bf16 -> f32 in TMEM), fed by TMA through
 // an mbarrier ring: warp 0 loads, warp 1 issues the MMAs into one of two TMEM
 // accumulators, warps 2-9 are the epilogue of the other.  CG = 1: one CTA per
-// 128 x 256 tile, a ring of 48 KiB stages; CG = 2: a CTA pair per 256 x 256
-// tile, 32 KiB stages.  Each CTA is alone on its SM and loops over tiles.
+// tile of 128 rows; CG = 2: a CTA pair per tile of 256.  dX and dW tiles are 256
+// wide, in stages of 48 (pair: 32) KiB a CTA; logit tiles and their stages are
+// sized by the call.  Each CTA is alone on its SM and loops over tiles.
 //
 // What bounds it, measured (tensor pipe busy, 4096 tokens x 32768 x 4096):
 // forward 96 %, dl 96 %, dX 94 %, dW 93 %.  A training-sized call then runs at
@@ -1378,7 +1379,10 @@ __global__ void __launch_bounds__(32 * kTeacherWarps) teacher_kernel(const Teach
 // W_i in f32 with short chains of additions, as the forward pass's side warps
 // compute them.  There is no product to hide behind, so a token is given
 // 2^log_warps warps of a CTA's eight, enough for up to four vectors of a row a
-// thread, all in flight at once.  Bound by reading the rows.
+// thread, all in flight at once.  Bound by reading the rows, and by its launch
+// for few: 96 tokens x 4096 5-7 us, 4096 tokens x 4096 with a teacher's entries
+// 22 us (four entries at a time, for more loads in flight, took 36: 128
+// registers, two CTAs to an SM).
 struct TargetArgs {
   const void* X[FCC_MAX_RANKS];
   const void* W[FCC_MAX_RANKS];

@@ -358,11 +358,12 @@ fcc_status fcc_ring_attention(int R, const void *const *Q, const void *const *K,
  * [T] f32.  T, V >= 1 (any, odd ones too), V % R == 0, D % 8 == 0,
  * 0 <= smoothing < 1, z_weight >= 0, softcap 0 or from 2^-126 to 2^126.
  * Logits that are not finite give a loss that is not.  The label's logit is
- * summed in f32 by itself; the others come from the tensor cores, whose sums lose a little of themselves: they are scaled
- * by what sums of random products lose (1.6e-8 for every 16 of D, up to D =
- * 131072), and are off by as much where nothing was lost, by up to 8e-8 for
- * every 16 of D where all of a logit's products are positive and 1.5e-7 where
- * the first outweighs the rest (measured on a GB300).  Repeatable (a fixed order of summation).  Uses workspace
+ * summed in f32 by itself; the others come from the tensor cores, whose sums
+ * lose a little of themselves: they are scaled by what sums of random products
+ * lose (1.6e-8 for every 16 of D, up to D = 131072), and are off by as much where
+ * nothing was lost, by up to 8e-8 for every 16 of D where all of a logit's
+ * products are positive and 1.5e-7 where the first outweighs the rest (measured
+ * on a GB300).  Repeatable (a fixed order of summation).  Uses workspace
  * (fcc_linear_loss_workspace_size with topk 0, grad 0).  opts->algo: AUTO or
  * FUSED; the environment's FCC_ALGO and FCC_CHUNKS do not apply.
  */
@@ -380,12 +381,15 @@ fcc_status fcc_linear_xent(int R, const void *const *X, const void *const *W,
  *   dx_v = dl_v, times 1 - (l_v / softcap)^2 when softcap > 0
  *   dX[r]  = sum over all ranks s of dx_s @ W[s]   ([T,D] bf16, to every rank)
  *   dW[r]  = dx_r^T @ X[r]                         ([V/R,D] bf16)
- * Ignored rows have no gradient, whatever their dloss holds.  dX or dW may be
- * NULL (not wanted).  The logits are computed again, a piece of every rank's
- * vocabulary at a time (opts->chunks pieces; 0 = as few as hold 512 MiB of
- * dx), and dx is rounded to bf16 (for up to 64 tokens, to a sum of two bf16
- * numbers); products accumulate in f32.  out_dtype is FCC_BF16 (an f32 result
- * of bf16 dx would promise digits it does not have).  Uses workspace (fcc_linear_loss_workspace_size with topk 0, grad 1).
+ * Ignored rows have no gradient, whatever their dloss holds; their rows of X
+ * must be finite all the same, for dx's zeros multiply them in dW.  dX or dW may
+ * be NULL (not wanted).  The logits are computed again, a piece of every rank's
+ * vocabulary at a time (opts->chunks pieces; 0 = as few as hold 512 MiB of dx),
+ * scaled as in the forward pass and the label's summed by itself; dx is rounded
+ * to bf16 (for up to 64 tokens, to a sum of two bf16 numbers); products
+ * accumulate in f32.  out_dtype is FCC_BF16: gradients that are added up over
+ * several calls are rounded in each.  Uses workspace
+ * (fcc_linear_loss_workspace_size with topk 0, grad 1).
  */
 fcc_status fcc_linear_xent_grad(int R, const void *const *X, const void *const *W,
                                 const int32_t *labels, const float *const *lse,
@@ -405,7 +409,8 @@ fcc_status fcc_linear_xent_grad(int R, const void *const *X, const void *const *
  * The gradient is dl_v = dloss temperature (exp(l_v / temperature - lse)
  * - sum_k q_k [v = i_k]).  teacher_idx, teacher_logits: [T,topk] int32 / f32
  * (device), 1 <= topk <= FCC_MAX_TEACHER, in any order; temperature from 2^-63
- * to 2^63.  All else as in fcc_linear_xent and fcc_linear_xent_grad.
+ * to 2^63.  All else as in fcc_linear_xent and fcc_linear_xent_grad, with the
+ * entries of probability 1/8 or more in the label's place.
  */
 fcc_status fcc_linear_distill(int R, const void *const *X, const void *const *W,
                               const int32_t *teacher_idx, const float *teacher_logits, int64_t T,
