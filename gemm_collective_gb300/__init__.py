@@ -30,7 +30,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 # ----------------------------------------------------------------- constants
-FCC_BF16, FCC_F16, FCC_F32 = 0, 1, 2
+FCC_BF16, FCC_F16, FCC_F32, FCC_E4M3 = range(4)
 (FCC_OK, FCC_ERR_INVALID, FCC_ERR_UNSUPPORTED, FCC_ERR_CUDA, FCC_ERR_CAPACITY,
  FCC_ERR_TIMEOUT, FCC_ERR_WORKSPACE) = range(7)
 (FCC_ALGO_AUTO, FCC_ALGO_FUSED, FCC_ALGO_UNFUSED, FCC_ALGO_INTERDECOM,
@@ -61,6 +61,49 @@ def make_opts(algo=FCC_ALGO_AUTO, deterministic=1, chunks=0, max_ctas=0, timeout
     ph = phase_ns.data_ptr() if hasattr(phase_ns, "data_ptr") else phase_ns
     return fcc_opts(algo, deterministic, chunks, max_ctas, timeout_ns, ws, workspace_bytes,
                     cta_pair, ph)
+
+
+class fcc_cache(ctypes.Structure):
+    _fields_ = [
+        ("K", ctypes.c_void_p),
+        ("V", ctypes.c_void_p),
+        ("K_exp", ctypes.c_void_p),
+        ("V_exp", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("d", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+    ]
+
+
+class fcc_batch(ctypes.Structure):
+    _fields_ = [
+        ("start", ctypes.c_void_p),
+        ("len", ctypes.c_void_p),
+        ("table", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int64),
+        ("T", ctypes.c_int64),
+        ("B", ctypes.c_int),
+    ]
+
+
+def make_cache(K, V, pages, page_size, H, d, dtype=FCC_BF16, K_exp=None, V_exp=None) -> fcc_cache:
+    """The description of a paged cache: one pool of keys and one of values for each rank.
+
+    Made once and passed to every call; like ptr_array() it holds addresses only,
+    and the tensors must stay alive while it is in use."""
+    arrays = [None if x is None else ptr_array(x) for x in (K, V, K_exp, V_exp)]
+    c = fcc_cache(*(None if a is None else ctypes.addressof(a) for a in arrays), pages, page_size,
+                  H, d, dtype)
+    c.arrays = arrays  # (the structure holds their addresses)
+    c.ranks = min((len(a) for a in arrays if a is not None), default=0)
+    return c
+
+
+def make_batch(start, len, table, T, B, max_pages) -> fcc_batch:
+    """The description of a step's sequences (int32 arrays on the device): see fcc_batch in fcc.h."""
+    return fcc_batch(_addr(start), _addr(len), _addr(table), max_pages, T, B)
 
 
 class FccError(RuntimeError):
@@ -123,6 +166,13 @@ _distill_grad = _sig("fcc_linear_distill_grad", _I,
                       _OPTS, _P])
 _loss_ws = _sig("fcc_linear_loss_workspace_size", ctypes.c_size_t,
                 [_I, _I64, _I64, _I64, _I, _I, _OPTS])
+_CACHE, _BATCH = ctypes.POINTER(fcc_cache), ctypes.POINTER(fcc_batch)
+_append = _sig("fcc_cache_append", _I, [_I, _P, _P, _I64, _CACHE, _BATCH, _I, _OPTS, _P])
+_gather = _sig("fcc_cache_gather", _I, [_I, _CACHE, _BATCH, _P, _P, _I64, _I, _OPTS, _P])
+_paged = _sig("fcc_paged_attention", _I,
+              [_I, _P, _I64, _CACHE, _BATCH, _I, _P, _I64, _P, _F, _I64, _I, _I, _OPTS, _P])
+_paged_ws = _sig("fcc_paged_attention_workspace_size", ctypes.c_size_t,
+                 [_I, _I64, _I, _I, _I, _I64, _OPTS])
 _launches = _sig("fcc_launch_count", ctypes.c_uint64, [])
 _version = _sig("fcc_version", ctypes.c_char_p, [])
 _wait_timeout = _sig("fcc_test_wait_timeout", _I, [_I64, _P])
@@ -296,6 +346,37 @@ def fcc_linear_distill_grad(R, X, W, teacher_idx, teacher_logits, lse, dloss, T,
 
 def fcc_linear_loss_workspace_size(R, T, V, D, topk=0, grad=False, opts=None) -> int:
     return int(_loss_ws(R, T, V, D, topk, 1 if grad else 0, _opts(opts)))
+
+
+def _cache(c, R):
+    # a cache described for fewer ranks would be read past its arrays' end
+    if c is not None and hasattr(c, "ranks") and c.ranks < R:
+        raise FccError(FCC_ERR_INVALID, f"a cache of {c.ranks} ranks in a call for {R}")
+    return c
+
+
+def fcc_cache_append(R, K, V, cache, batch, ld=0, in_dtype=FCC_BF16, opts=None, stream=None):
+    """Writes a step's keys and values ([T, H, d] per rank) into the paged cache."""
+    _check(_append(R, _ptrs(K), _ptrs(V), ld, _cache(cache, R), batch, in_dtype, _opts(opts),
+                   _stream(stream)), "fcc_cache_append")
+
+
+def fcc_cache_gather(R, cache, batch, K, V, ld=0, out_dtype=FCC_BF16, opts=None, stream=None):
+    """Reads a step's positions back out of the cache into K, V ([T, H, d] per rank)."""
+    _check(_gather(R, _cache(cache, R), batch, _ptrs(K), _ptrs(V), ld, out_dtype, _opts(opts),
+                   _stream(stream)), "fcc_cache_gather")
+
+
+def fcc_paged_attention(R, Q, cache, batch, Hq, O, lse=None, scale=0.0, window=0, ldq=0, ldo=0,
+                        in_dtype=FCC_BF16, out_dtype=FCC_BF16, opts=None, stream=None):
+    """Attention of a step's rows (Q: [T, Hq, d] per rank) over the cache's pages."""
+    _check(_paged(R, _ptrs(Q), ldq, _cache(cache, R), batch, Hq, _ptrs(O), ldo, _ptrs(lse), scale,
+                  window, in_dtype, out_dtype, _opts(opts), _stream(stream)),
+           "fcc_paged_attention")
+
+
+def fcc_paged_attention_workspace_size(R, T, B, Hq, H, d, opts=None) -> int:
+    return int(_paged_ws(R, T, B, Hq, H, d, _opts(opts)))
 
 
 def fcc_choose_algo(op, R, M, N, K, sms=0, max_ctas=0) -> int:

@@ -64,7 +64,9 @@ typedef struct CUstream_st *fcc_stream_t;
 #define FCC_MAX_TABLES 256  /* embedding tables per call */
 #define FCC_MAX_TEACHER 256 /* teacher entries per token (distillation) */
 
-typedef enum { FCC_BF16 = 0, FCC_F16 = 1, FCC_F32 = 2 } fcc_dtype;
+/* FCC_E4M3 (one sign, four exponent and three mantissa bits, no infinities) is a
+ * type of the paged cache's contents only. */
+typedef enum { FCC_BF16 = 0, FCC_F16 = 1, FCC_F32 = 2, FCC_E4M3 = 3 } fcc_dtype;
 
 typedef enum {
   FCC_OK = 0,
@@ -428,6 +430,108 @@ fcc_status fcc_linear_distill_grad(int R, const void *const *X, const void *cons
 /* Scratch bytes of the four calls above (topk 0: cross entropy). */
 size_t fcc_linear_loss_workspace_size(int R, int64_t T, int64_t V, int64_t D, int topk, int grad,
                                       const fcc_opts *opts);
+
+/*
+ * A paged cache of keys and values, and the sequences of one step that use it.
+ * Heads are split over the ranks: rank r holds H key/value heads of every
+ * sequence in its own two pools.  The sequences, their lengths and their page
+ * tables are the same for every rank.  Position j of sequence b lies in row
+ * j % page_size of page table[b][j / page_size].
+ *
+ * Pools of dtype FCC_BF16 hold the values themselves.  Pools of dtype FCC_E4M3
+ * hold x / 2^k rounded to e4m3 (nearest, ties to even), with one k for each
+ * position and head, kept as the byte k + 127 in K_exp / V_exp: the least power
+ * of two (k >= -64) for which the row's largest finite |x| is at most 448 * 2^k.
+ * A power of two costs a floating-point code no digits and makes reading back
+ * exact.  A value that is not finite becomes NaN.  A row of zeros has k = -64;
+ * values below about 2^-73 become zero.
+ */
+typedef struct {
+  void *const *K;        /* R pools [pages, H, page_size, d] of `dtype` */
+  void *const *V;
+  uint8_t *const *K_exp; /* FCC_E4M3: R arrays [pages, H, page_size]; else ignored */
+  uint8_t *const *V_exp;
+  int64_t pages;         /* 1 .. 2^31 - 1 */
+  int page_size;         /* a power of two, 1 .. 65536 */
+  int H;                 /* key/value heads of one rank, 1 .. 1024 */
+  int d;                 /* 64 or 128 (others: FCC_ERR_UNSUPPORTED) */
+  fcc_dtype dtype;       /* FCC_BF16 or FCC_E4M3 */
+} fcc_cache;
+
+/*
+ * Rows start[b] .. start[b+1] - 1 of the step's token arrays belong to sequence
+ * b and are its newest positions: row start[b] + i is position
+ * len[b] - n + i, n = start[b+1] - start[b].  Rows behind start[B] belong to
+ * nobody and are left alone.  The three arrays lie on the device (4-byte
+ * aligned) and are read by the kernels only, so a captured call can be replayed
+ * with other contents.  What they say is checked there: a step with
+ * start[b+1] < start[b], start[b] < 0 or start[b+1] > T, with len[b] < n, with
+ * more positions than max_pages pages hold or with a page outside [0, pages)
+ * among those it needs records FCC_ERR_INVALID in the status word, and nothing
+ * is read or written there (fcc_paged_attention says what its results are then).
+ */
+typedef struct {
+  const int32_t *start;  /* [B + 1] */
+  const int32_t *len;    /* [B]: positions of each sequence, this step's included */
+  const int32_t *table;  /* [B, max_pages]; entries past a sequence's last page are not read */
+  int64_t max_pages;     /* 1 .. 2^31 - 1 */
+  int64_t T;             /* rows of the step's token arrays, 1 .. 2^31 - 1 */
+  int B;                 /* sequences, 1 .. 65536 */
+} fcc_batch;
+
+/*
+ * Writes the keys and values of a step's rows into the cache.  K[r], V[r]:
+ * [T, H, d] bf16, rows ld elements apart (0: H * d; ld % 8 == 0), so that they
+ * may be parts of one fused projection's output.  Two rows of a call must not
+ * have the same place in the pools (sequences that share a page write to
+ * different rows of it, or to copies).  No workspace.
+ */
+fcc_status fcc_cache_append(int R, const void *const *K, const void *const *V, int64_t ld,
+                            const fcc_cache *cache, const fcc_batch *batch, fcc_dtype in,
+                            const fcc_opts *opts, fcc_stream_t stream);
+
+/*
+ * The reverse: reads the rows' positions back into K[r], V[r] ([T, H, d] bf16,
+ * rows ld elements apart), as code * 2^k where the cache is e4m3 (exact down to
+ * bf16's subnormal numbers, rounded there).  With start[b+1] - start[b] = len[b] whole
+ * sequences come back.  Rows of a sequence that is not valid are left alone, and so
+ * are rows whose page is not.  No workspace.
+ */
+fcc_status fcc_cache_gather(int R, const fcc_cache *cache, const fcc_batch *batch, void *const *K,
+                            void *const *V, int64_t ld, fcc_dtype out, const fcc_opts *opts,
+                            fcc_stream_t stream);
+
+/*
+ * Attention of a step's rows over the cache, whose pages already hold the
+ * rows' own keys and values (fcc_cache_append first).  Every rank has Hq query
+ * heads; head h reads key/value head h / (Hq / H).  For the row at position p:
+ *   s_j = scale * Q[r][t][h] . K[j],  j <= p, and j > p - window if window > 0
+ *   O[r][t][h] = sum_j softmax_j(s) V[j],   lse[r][t][h] = log sum_j exp(s_j)
+ * Positions that a row does not see do not touch it, whatever their keys and
+ * values hold.  Q[r], O[r]: [T, Hq, d] bf16, rows ldq / ldo elements apart (0:
+ * Hq * d; multiples of 8): O[r] is the A of fcc_gemv_ar or fcc_gemm_ar for
+ * the output projection.  lse: NULL, or R arrays [T, Hq] f32.  scale: 0 means
+ * 1 / sqrt(d), otherwise finite and positive.  Hq % H == 0, Hq <= 1024.
+ * Scores, maxima, sums and O's accumulators are f32; the probabilities enter
+ * the product with V in 16 bits (bf16, relative to a running maximum; where the
+ * rows are few and the cache is e4m3, f16).  Repeatable (a fixed order of summation).
+ * A sequence with len[b] < n has no visible positions; a row with none has
+ * O = 0, lse = -inf.  Where a needed page is not valid, or lies past
+ * max_pages, its positions are left out.  Both record FCC_ERR_INVALID.
+ * One token or many: a step with up to 16 query rows to a sequence and
+ * key/value head on average (T * Hq / H <= 16 B) is read as few rows over many
+ * positions, any other one in tiles of 128 rows; both take every step.
+ * Uses workspace (fcc_paged_attention_workspace_size).  A call made while its
+ * stream is being captured must bring its own (FCC_ERR_WORKSPACE): the pool may
+ * move before the graph is replayed.  Graphs and streams that run at the same time
+ * need one each.
+ */
+fcc_status fcc_paged_attention(int R, const void *const *Q, int64_t ldq, const fcc_cache *cache,
+                               const fcc_batch *batch, int Hq, void *const *O, int64_t ldo,
+                               float *const *lse, float scale, int64_t window, fcc_dtype in,
+                               fcc_dtype out, const fcc_opts *opts, fcc_stream_t stream);
+size_t fcc_paged_attention_workspace_size(int R, int64_t T, int B, int Hq, int H, int64_t d,
+                                          const fcc_opts *opts);
 
 /* Scratch bytes a call needs (for opts->workspace); 0 if none. */
 size_t fcc_workspace_size(fcc_op op, int R, int64_t M, int64_t N, int64_t K,
