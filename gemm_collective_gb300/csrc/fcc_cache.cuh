@@ -36,7 +36,8 @@ __device__ __forceinline__ void record_invalid(int* status) {
   if (status != nullptr) atomicCAS(status, 0, 1 /* FCC_ERR_INVALID */);
 }
 
-// A sequence of the step: rows [s, s + n) of the token arrays, L positions.
+// A sequence of the step: rows [s, s + n) of the token arrays, L positions (n where
+// it has fewer, which leaves it without any: ok is false).
 struct Seq {
   int s, n, L;
   bool rows_ok;   // the rows lie inside the token arrays
@@ -51,6 +52,7 @@ __device__ __forceinline__ Seq load_seq(const StepArgs& a, int b) {
   q.rows_ok = q.s >= 0 && e >= q.s && e <= a.T;
   q.n = q.rows_ok ? e - q.s : 0;
   q.ok = q.rows_ok && q.L >= q.n;
+  if (!q.ok) q.L = q.n;
   return q;
 }
 
