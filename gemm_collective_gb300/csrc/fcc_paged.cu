@@ -70,16 +70,6 @@ struct Few {
   }
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -107,23 +97,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Two e4m3 codes (the low 16 bits) as a pair of f16: exact.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(codes));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
-  if constexpr (F16) return pack_f16x2(lo, hi);
-  return ptx::pack_bf16x2(lo, hi);
 }
 
 // A walk over a CTA's run of units: item after item, each from unit k to unit end.
@@ -188,9 +161,6 @@ struct Sums {
     for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], f[(i >> 1) & 1], o[i]);
   }
 };
-
-// 2^(x - ref), 0 for x = -inf.
-__device__ __forceinline__ float ex2_from(float x, float ref) { return x == -INFINITY ? 0.f : ptx::ex2_approx(x - ref); }
 
 template <int D, bool E4M3>
 __device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int item, int tiles, int j, int lane,
@@ -722,6 +692,15 @@ size_t few_rows_ws_bytes(int64_t d, int ctas) {
   return header_bytes(ctas) + 2 * static_cast<size_t>(ctas) * part;
 }
 
+// Up to 16 rows to a sequence and key/value head on average: the tensor cores'
+// tiles of 128 rows would be mostly empty, and their latency is what a short
+// item waits for.
+bool few_rows(int64_t T, int B, int G) { return T * G <= static_cast<int64_t>(kRowTile) * B; }
+
+size_t paged_ws_bytes(int64_t T, int B, int G, int64_t d, int ctas) {
+  return few_rows(T, B, G) ? few_rows_ws_bytes(d, ctas) : tiles_ws_bytes(d, B, ctas);
+}
+
 int usable_sms(const fcc_opts* o) {
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -744,7 +723,7 @@ size_t fcc_paged_attention_workspace_size(int R, int64_t T, int B, int Hq, int H
   if (R < 1 || R > FCC_MAX_RANKS || T < 1 || B < 1 || H < 1 || Hq < H || Hq % H != 0 ||
       (d != 64 && d != 128))
     return 0;
-  return few_rows_ws_bytes(d, usable_sms(opts));
+  return paged_ws_bytes(T, B, Hq / H, d, usable_sms(opts));
 }
 
 fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const fcc_cache* cache,
@@ -785,10 +764,12 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
     if (capture != cudaStreamCaptureStatusNone) return FCC_ERR_WORKSPACE;
   }
   const int ctas = usable_sms(opts);
+  a.G = Hq / cache->H;
   void* ws = nullptr;
   int sms = 0;
   unsigned long long timeout_ns = 0;
-  const fcc_status s = internal_prepare(opts, few_rows_ws_bytes(cache->d, ctas), &ws, &a.status, &sms, &timeout_ns);
+  const fcc_status s = internal_prepare(opts, paged_ws_bytes(batch->T, batch->B, a.G, cache->d, ctas), &ws,
+                                        &a.status, &sms, &timeout_ns);
   if (s != FCC_OK) return s;
   for (int r = 0; r < R; ++r) {
     a.Q[r] = static_cast<const char*>(Q[r]);
@@ -799,16 +780,18 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   a.ldo = ldo;
   a.R = R;
   a.Hq = Hq;
-  a.G = Hq / cache->H;
   a.window = window == 0 ? INT_MAX : static_cast<int>(std::min<int64_t>(window, INT_MAX));
   a.scale_log2 = static_cast<float>((scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->d))) *
                                     1.4426950408889634);
   a.ws = static_cast<char*>(ws);
   const bool e4m3 = cache->dtype == FCC_E4M3;
-  const cudaError_t e = cache->d == 128 ? (e4m3 ? launch_few<128, true>(a, ctas, st) : launch_few<128, false>(a, ctas, st))
-                                        : (e4m3 ? launch_few<64, true>(a, ctas, st) : launch_few<64, false>(a, ctas, st));
+  const bool few = few_rows(batch->T, batch->B, a.G);
+  const cudaError_t e =
+      !few ? launch_tiles(a, e4m3, ctas, timeout_ns, st)
+      : cache->d == 128 ? (e4m3 ? launch_few<128, true>(a, ctas, st) : launch_few<128, false>(a, ctas, st))
+                        : (e4m3 ? launch_few<64, true>(a, ctas, st) : launch_few<64, false>(a, ctas, st));
   if (e != cudaSuccess) return FCC_ERR_CUDA;
-  bump_launch_count(2);
+  bump_launch_count(few ? 2 : 3);
   return FCC_OK;
 }
 

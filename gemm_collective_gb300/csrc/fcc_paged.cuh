@@ -2,6 +2,7 @@
 #pragma once
 
 #include "fcc_cache.cuh"
+#include "fcc_ptx.cuh"
 
 namespace fcc {
 
@@ -20,5 +21,42 @@ struct PagedArgs {
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
+
+// 2^(x - ref), 0 for x = -inf.
+__device__ __forceinline__ float ex2_from(float x, float ref) {
+  return x == -INFINITY ? 0.f : ptx::ex2_approx(x - ref);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two e4m3 codes (the low 16 bits) as a pair of f16: exact.
+__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (F16) return pack_f16x2(lo, hi);
+  return ptx::pack_bf16x2(lo, hi);
+}
+
+// Tiles of 128 rows on the tensor cores' own memory (fcc_paged_tiles.cu).
+size_t tiles_ws_bytes(int64_t d, int B, int ctas);
+cudaError_t launch_tiles(const PagedArgs& a, bool e4m3, int ctas, unsigned long long timeout_ns,
+                         cudaStream_t st);
 
 }  // namespace fcc
