@@ -70,6 +70,16 @@ struct Few {
   }
 };
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -754,8 +764,10 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   if (in != FCC_BF16 || out != FCC_BF16) return FCC_ERR_UNSUPPORTED;
   if (opts != nullptr && opts->algo != FCC_ALGO_AUTO && opts->algo != FCC_ALGO_FUSED)
     return FCC_ERR_UNSUPPORTED;
-  // a rank's tiles of 16 rows are counted in 32 bits
-  if (static_cast<int64_t>(R) * (batch->T * Hq / kRowTile + static_cast<int64_t>(cache->H) * batch->B) > INT_MAX)
+  // rows (tokens times a group's heads) and tiles of 16 of them are counted in 32 bits
+  const int64_t rows = batch->T * (Hq / cache->H);
+  if (rows > INT_MAX - 256 ||
+      static_cast<int64_t>(R) * cache->H * (rows / kRowTile + batch->B) > INT_MAX)
     return FCC_ERR_INVALID;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (opts == nullptr || opts->workspace == nullptr) {
@@ -780,6 +792,8 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   a.ldo = ldo;
   a.R = R;
   a.Hq = Hq;
+  while ((1 << a.g_shift) < a.G) ++a.g_shift;
+  a.g_mul = static_cast<uint32_t>(((uint64_t{1} << (31 + a.g_shift)) + a.G - 1) / a.G);
   a.window = window == 0 ? INT_MAX : static_cast<int>(std::min<int64_t>(window, INT_MAX));
   a.scale_log2 = static_cast<float>((scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->d))) *
                                     1.4426950408889634);

@@ -18,6 +18,14 @@ struct PagedArgs {
   float scale_log2;            // scale * log2(e)
   int* status;
   char* ws;
+  uint32_t g_mul, g_shift;     // rows / G for rows < 2^31: see by_g()
+  int boxes;                   // pages come by TMA
+
+  // x / G by multiplication: g_mul = ceil(2^(31 + g_shift) / G) with 2^(g_shift - 1) < G
+  // <= 2^g_shift is exact for x < 2^31.
+  __device__ __forceinline__ int by_g(int x) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * g_mul) >> (31 + g_shift));
+  }
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -25,16 +33,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // 2^(x - ref), 0 for x = -inf.
 __device__ __forceinline__ float ex2_from(float x, float ref) {
   return x == -INFINITY ? 0.f : ptx::ex2_approx(x - ref);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Two e4m3 codes (the low 16 bits) as a pair of f16: exact.

@@ -14,16 +14,17 @@
 //   S_t = Q_t K_j^T;  P_t = 2^(S_t c - ref), in 16 bits over S_t's first columns;
 //   O_t += P_t V_j, A from TMEM.
 // A row's reference is raised (and its O_t rescaled) only when a block's maximum
-// passes it by 8 (log2 units).  The two tiles alternate on the tensor core: one
+// passes it by far.  The two tiles alternate on the tensor core: one
 // tile's exponentials run under the other's products.  A new item's queries are
 // loaded, and its first S computed, before the old one's O has been stored.
 //
 // Warps: 0-3 and 4-7 softmax and output of tiles A and B (a thread owns a row and
 // its 128 columns), 8-11 load keys and values, 12 issues the products.  The
 // loaders look up every position's page for itself (any page size), bf16 rows go
-// by cp.async into the swizzled tile.  e4m3 rows pass through registers and become
-// f16 there, exactly; their powers of two enter at the exponent (see
-// fcc_paged.cu): t = 2^a (S c) + b, P = 2^(t - ref), l += P 2^-b.
+// by TMA into the swizzled tile, 32 positions to a warp.  e4m3 rows pass through registers and become
+// f16 there, times their powers of two relative to the largest, 2^A of the keys and
+// 2^B of the values, of each 32 positions; those enter at the exponent (see
+// fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
 // Shared memory (128-byte swizzle): Q_t and four slots of [128 rows][D] 16-bit
 // values in atoms of 64 columns, K_0, V_0, K_1, V_1, ... in the slots; K is the
 // K-major and V the MN-major B operand of the same layout.
@@ -33,6 +34,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cstring>
 
 namespace fcc {
 namespace {
@@ -43,14 +45,26 @@ constexpr int kBlock = 128;                    // positions of a block
 constexpr int kSlots = 4;
 constexpr int kCols = 4;                       // blocks whose column constants are kept
 constexpr uint32_t kAtom = 128 * 128;
-constexpr float kRaise = 8.f;
+// A row's reference is raised when a block's maximum passes it by this much (log2
+// units).  bf16 has f32's exponents: P may grow far, and the raise (which rescales O_t
+// in tensor memory) can wait for the next block.  A row whose sums overflow all the
+// same (2^127 within one block) is not finite at the end and is computed again.  f16
+// ends at 2^16: there the maximum is taken before the exponentials.
+template <bool E4M3>
+constexpr float kRaise = E4M3 ? 8.f : 32.f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;                // S_t at 128 t, O_t at 256 + 128 t
 constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;
 constexpr int kThreads = 512;                  // 16 warps: 8 softmax, 4 loading, 1 issuing, 3 idle
-// Registers: 512 x 128 at launch = 256 x 192 + 128 x 72 + 128 x 56 afterwards.
-constexpr int kRegsSoftmax = 192, kRegsLoad = 72, kRegsIssue = 56;
-static_assert(256 * kRegsSoftmax + 128 * kRegsLoad + 128 * kRegsIssue == kThreads * 128);
+// Registers: the launch's 512 x 128 are dealt out anew, to 256 softmax threads, 128
+// loading ones (which hold an e4m3 block's pieces in flight) and the issuing warp's
+// 128.  Next to nothing may spill: what shared memory leaves of the L1 is too small to
+// hold it (200 bytes a thread made a 2048-row prompt three times as slow).
+template <bool E4M3>
+struct Regs {
+  static constexpr int kSoftmax = E4M3 ? 144 : 176, kLoad = E4M3 ? 128 : 80, kIssue = E4M3 ? 96 : 80;
+  static_assert(256 * kSoftmax + 128 * kLoad + 128 * kIssue <= kThreads * 128);
+};
 constexpr int kMaxCtas = 512;
 
 struct Start {                                 // where a CTA's run begins
@@ -65,13 +79,16 @@ struct Header {                                // of the item that a CTA begins 
 struct Layout {
   size_t starts, headers, units, parts, part_bytes, total;
 };
+// References, sums, then [D / 4][256] float4.
+template <int D>
+constexpr size_t kPartBytes = kPairRows * static_cast<size_t>(D + 2) * 4;
 __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   Layout l;
   l.starts = 256;
   l.headers = l.starts + static_cast<size_t>(ctas) * sizeof(Start);
   l.units = l.headers + static_cast<size_t>(ctas) * sizeof(Header);
   l.parts = (l.units + static_cast<size_t>(B) * 8 + 255) & ~size_t{255};
-  l.part_bytes = kPairRows * static_cast<size_t>(d + 2) * 4;   // references, sums, [D / 4][256] float4
+  l.part_bytes = kPairRows * static_cast<size_t>(d + 2) * 4;
   l.total = l.parts + 2 * static_cast<size_t>(ctas) * l.part_bytes;
   return l;
 }
@@ -81,21 +98,21 @@ struct Totals {                                // at the workspace's start
 };
 
 __device__ __forceinline__ int pairs_of(const PagedArgs& a, const Seq& q) {
-  return static_cast<int>((static_cast<long long>(q.n) * a.G + kPairRows - 1) / kPairRows);
+  return (q.n * a.G + (kPairRows - 1)) / kPairRows;   // (T * G stays below 2^31 - 256)
 }
 
 // Blocks [j0, j1) that rows [first, last] of a sequence see.
 struct Range {
   int j0, j1;
 };
-__device__ __forceinline__ Range blocks_of(const PagedArgs& a, const Seq& q, long long first, long long last) {
+__device__ __forceinline__ Range blocks_of(const PagedArgs& a, const Seq& q, int first, int last) {
   if (!q.ok) return Range{0, 1};               // (one, of which nothing is seen)
-  const int p0 = q.L - q.n + static_cast<int>(first / a.G), p1 = q.L - q.n + static_cast<int>(last / a.G);
+  const int p0 = q.L - q.n + a.by_g(first), p1 = q.L - q.n + a.by_g(last);
   return Range{max(0, p0 - a.window + 1) / kBlock, p1 / kBlock + 1};
 }
 __device__ __forceinline__ Range pair_blocks(const PagedArgs& a, const Seq& q, int pair) {
-  const long long first = static_cast<long long>(pair) * kPairRows;
-  return blocks_of(a, q, first, min(static_cast<long long>(q.n) * a.G, first + kPairRows) - 1);
+  const int first = pair * kPairRows;
+  return blocks_of(a, q, first, min(q.n * a.G - first, kPairRows) + first - 1);
 }
 
 constexpr int kPlanThreads = 1024;
@@ -103,15 +120,13 @@ constexpr int kFewPairs = 8;                   // up to here a thread counts a s
 
 // Counts the blocks of all items and finds where each CTA's run begins.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PagedArgs a, int grid) {
-  __shared__ long long s_scan[32], s_off[kMaxCtas];
-  __shared__ int s_b[kMaxCtas];
+  __shared__ long long s_scan[32];
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Layout lay = layout_of(a.pool.d, a.step.B, grid);
   long long* units = reinterpret_cast<long long*>(a.ws + lay.units);
   const long long rh = static_cast<long long>(a.R) * a.pool.H;
-  long long np_all = 0;
   for (int b0 = warp * 32; b0 < a.step.B; b0 += kPlanThreads) {
     const int b = b0 + lane;
     Seq q{0, 0, 0, false, false};
@@ -121,7 +136,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       q = load_seq(a.step, b);
       if (!q.ok) record_invalid(a.status);
       np = pairs_of(a, q);
-      np_all += np;
       if (np <= kFewPairs)
         for (int p = 0; p < np; ++p) {
           const Range g = pair_blocks(a, q, p);
@@ -162,27 +176,29 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     total += s_scan[i];
   }
   const long long ctas = min(static_cast<long long>(grid), total);
-  if (mine > 0) {
-    // runs c with from <= c total / ctas < from + mine
-    long long c = (from * ctas + total - 1) / total;
-    while (c > 0 && (c - 1) * total / ctas >= from) --c;
-    while (c * total / ctas < from) ++c;
-    long long at = from;
-    int b = b_first;
-    for (; c < ctas; ++c) {
-      const long long u = c * total / ctas;
-      if (u >= from + mine) break;
-      while (u >= at + units[b]) at += units[b++];
-      s_b[c] = b;
-      s_off[c] = u - at;
-    }
+  // (from here on units[b] is the sum of the blocks before sequence b)
+  for (int b = b_first; b < b_last; ++b) {
+    const long long n = units[b];
+    units[b] = from;
+    from += n;
   }
   __syncthreads();
   Start* starts = reinterpret_cast<Start*>(a.ws + lay.starts);
   for (int c = warp; c < ctas; c += 32) {
-    const int b = s_b[c];
-    const long long each = units[b] / rh;
-    long long rest = s_off[c] % each;
+    const long long u = c * total / ctas;
+    // the last sequence whose blocks begin at or before u
+    int b = 0;
+    for (int count = a.step.B; count > 1;) {
+      const int step = (count + 31) >> 5, i = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, i < count && units[b + i] <= u);
+      const int k = 31 - __clz(m);
+      b += k * step;
+      count = min(step, count - k * step);
+    }
+    const long long off = u - units[b];
+    const long long each = ((b + 1 < a.step.B ? units[b + 1] : total) - units[b]) / rh;
+    const int at_rh = static_cast<int>(off / each);
+    long long rest = off - at_rh * each;
     const Seq q = load_seq(a.step, b);
     const int np = pairs_of(a, q);
     for (int p0 = 0; p0 < np; p0 += 32) {
@@ -201,7 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const unsigned m = __ballot_sync(0xffffffffu, rest < incl);
       if (m != 0) {
         if (lane == __ffs(m) - 1)
-          starts[c] = Start{b, static_cast<int>(s_off[c] / each), p, static_cast<int>(rest - (incl - n))};
+          starts[c] = Start{b, at_rh, p, static_cast<int>(rest - (incl - n))};
         break;
       }
       rest -= __shfl_sync(0xffffffffu, incl, 31);
@@ -218,9 +234,10 @@ struct Walk {
   int ja, jb;                                  // the CTA's part of them
   long long left;                              // blocks of the CTA behind this item's
   int lo[2], hi[2];                            // tile t's blocks of [ja, jb): none if lo >= hi
+  bool more;                                   // there is such an item
 
   __device__ __forceinline__ void take(const PagedArgs& a, int skip) {
-    const long long rows = static_cast<long long>(q.n) * a.G, first = static_cast<long long>(pair) * kPairRows;
+    const int rows = q.n * a.G, first = pair * kPairRows;
     const Range g = pair_blocks(a, q, pair);
     j0 = g.j0;
     j1 = g.j1;
@@ -230,22 +247,22 @@ struct Walk {
     left -= n;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const long long r0 = first + t * kTileRows;
+      const int r0 = first + t * kTileRows;
       lo[t] = hi[t] = 0;
       if (r0 >= rows) continue;
-      const Range s = blocks_of(a, q, r0, min(rows, r0 + kTileRows) - 1);
+      const Range s = blocks_of(a, q, r0, min(rows - r0, kTileRows) + r0 - 1);
       lo[t] = max(ja, s.j0);
       hi[t] = min(jb, s.j1);
     }
   }
   __device__ __forceinline__ bool begin(const PagedArgs& a, const Start& s, long long units) {
+    left = units;
+    if (left <= 0) return false;               // (s says nothing then)
     b = s.b;
     rh = s.rh;
     pair = s.pair;
     q = load_seq(a.step, b);
     pairs = pairs_of(a, q);
-    left = units;
-    if (left <= 0) return false;
     take(a, s.j);
     return true;
   }
@@ -273,27 +290,80 @@ struct Walk {
   __device__ __forceinline__ int head(const PagedArgs& a) const { return rh % a.pool.H; }
 };
 
-// Column constants of a block: for position i its key's power 2^a, its value's
-// exponent b and 2^-b; which positions the pages hold.
-struct Columns {
-  float ka[kBlock], vb[kBlock], vi[kBlock];
+// A warp's walk, kept in shared memory (the softmax threads have no registers to
+// spare): lane 0 takes the steps.  The softmax warps also keep the item before.
+struct alignas(16) WarpWalk {
+  Walk now, old;
+  __device__ __forceinline__ void begin(const PagedArgs& a, const Start& s, long long units, int lane) {
+    if (lane == 0) now.more = now.begin(a, s, units);
+    __syncwarp();
+  }
+  __device__ __forceinline__ void next(const PagedArgs& a, int lane) {
+    __syncwarp();                              // (every lane has read what it needs)
+    if (lane == 0) {
+      old = now;
+      now.more = now.next_item(a);
+    }
+    __syncwarp();
+  }
+};
+constexpr int kWalks = 13;
+
+// What the softmax warps need to know of a block's columns, for each 32 of them: e4m3
+// the largest powers of two of their keys and values; which positions the pages hold.
+struct alignas(16) Columns {
+  float ka[4], vb[4], vi[4];                   // 2^A, B and 2^-B
   uint32_t there[4];
+  uint32_t wide[4];                            // powers too far apart for f16, see f16_power()
 };
 
-constexpr int kBars = 2 * kSlots + kCols + 2 + 2 + 2 + 2 + 1;
+// 2^(byte - top) in f16 (both halves), 0 below what f16 holds.  An e4m3 code times it
+// stays within f16 and is off by 2^-25 at most, so a row whose power is up to 2^20
+// below its group's largest keeps its own digits to 2^-12 of its maximum (224 and
+// more in codes).  Rows further below are `wide`: their tile is computed again row by
+// row.  (Byte 63 holds what is nearly zero on its own.)
+__device__ __forceinline__ uint32_t f16_power(int byte, int top) {
+  const int k = byte - top;
+  const uint32_t h = k >= -14 ? static_cast<uint32_t>(15 + k) << 10 : k >= -24 ? 1u << (24 + k) : 0u;
+  return h | (h << 16);
+}
+__device__ __forceinline__ bool too_wide(int byte, int top) { return byte < top - 20 && byte > 63; }
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// This CTA's run of blocks.
+struct alignas(16) Run {
+  long long units;                             // of all CTAs
+  long long from, left;                        // the first of this one, and how many
+  char* parts;
+  Header* header;
+  Start start;
+  int ctas;
+};
+
+constexpr int kStageRow = 80;                  // 64 bytes of output and 16 that keep lanes apart
+constexpr int kBars = 2 * kSlots + kCols + 2 + 2 + 4 + 2 + 1;
 
 template <int D>
 constexpr uint32_t kTileBytes = (D / 64) * kAtom;
 template <int D>
-constexpr int kSmem = 1024 + (2 + kSlots) * static_cast<int>(kTileBytes<D>) + kCols * static_cast<int>(sizeof(Columns)) + kBars * 8 + 16;
+constexpr int kSmem = 1024 + (2 + kSlots) * static_cast<int>(kTileBytes<D>) + kCols * static_cast<int>(sizeof(Columns)) +
+                      kWalks * static_cast<int>(sizeof(WarpWalk)) + 8 * 32 * kStageRow +
+                      static_cast<int>(sizeof(Run)) + kBars * 8 + 16;
 static_assert(kSmem<128> <= 232448, "shared memory per CTA");
 
-__device__ __forceinline__ uint64_t desc_kmajor(uint32_t base, int kk) {
-  return ptx::smem_desc_sw128(base + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024);
+// A descriptor's address field counts 16 bytes: the K steps of 16 are added to the
+// operand's own descriptor.
+__device__ __forceinline__ uint64_t desc_of(const uint8_t* tile, uint32_t lbo) {
+  uint64_t d = ptx::smem_desc_sw128(ptx::smem_addr(tile), lbo, 1024);
+  asm volatile("" : "+l"(d));                  // (the steps are added where they are used, not kept)
+  return d;
 }
-__device__ __forceinline__ uint64_t desc_mnmajor(uint32_t base, int kk) {
-  return ptx::smem_desc_sw128(base + kk * 2048, kAtom, 1024);
-}
+__host__ __device__ constexpr uint32_t step_kmajor(int kk) { return ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4; }
+__host__ __device__ constexpr uint32_t step_mnmajor(int kk) { return (kk * 2048) >> 4; }
 // The byte of 16-byte chunk `chunk` (8 values) of a tile's row.
 __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return (chunk >> 3) * kAtom + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
@@ -320,58 +390,10 @@ __device__ __forceinline__ void tmem_ld_wait_regs(uint32_t (&v)[32]) {
                : "memory");
 }
 
-// 32 scores of a row: y = t - ref for columns col .. col + 31, and p = 2^y as 16-bit
-// pairs.  MASK: columns whose bit in `seen` is clear get p = 0.
-template <bool E4M3, bool MASK>
-__device__ __forceinline__ void exponentials(const uint32_t (&x)[32], float c, float ref, const Columns& cc, int col,
-                                             uint32_t seen, uint32_t* pk, uint64_t (&l2)[4], float (&mx)[4]) {
-  const uint64_t c2 = ptx::f32x2_pack(c, c), r2 = ptx::f32x2_pack(-ref, -ref);
-#pragma unroll
-  for (int k = 0; k < 32; k += 4) {
-    float4 ka, vb, vi;
-    if constexpr (E4M3) {
-      ka = *reinterpret_cast<const float4*>(&cc.ka[col + k]);
-      vb = *reinterpret_cast<const float4*>(&cc.vb[col + k]);
-      vi = *reinterpret_cast<const float4*>(&cc.vi[col + k]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const uint64_t x2 = ptx::f32x2_pack(__uint_as_float(x[k + i]), __uint_as_float(x[k + i + 1]));
-      uint64_t y2;
-      if constexpr (E4M3) {
-        const uint64_t ka2 = i == 0 ? ptx::f32x2_pack(ka.x, ka.y) : ptx::f32x2_pack(ka.z, ka.w);
-        const uint64_t vb2 = i == 0 ? ptx::f32x2_pack(vb.x, vb.y) : ptx::f32x2_pack(vb.z, vb.w);
-        y2 = ptx::f32x2_fma(ptx::f32x2_mul(x2, c2), ka2, ptx::f32x2_add(vb2, r2));
-      } else {
-        y2 = ptx::f32x2_fma(x2, c2, r2);
-      }
-      float y0, y1;
-      ptx::f32x2_unpack(y2, y0, y1);
-      if constexpr (MASK) {
-        if (!(seen >> (k + i) & 1)) y0 = -INFINITY;
-        if (!(seen >> (k + i + 1) & 1)) y1 = -INFINITY;
-      }
-      const int n = (k + i) / 2 & 3;
-      mx[n] = ptx::max3(mx[n], y0, y1);
-      const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
-      if constexpr (E4M3)
-        l2[n] = ptx::f32x2_fma(ptx::f32x2_pack(p0, p1), i == 0 ? ptx::f32x2_pack(vi.x, vi.y) : ptx::f32x2_pack(vi.z, vi.w), l2[n]);
-      else
-        l2[n] = ptx::f32x2_add(l2[n], ptx::f32x2_pack(p0, p1));
-      pk[(k + i) / 2] = pack16<E4M3>(p0, p1);
-    }
-  }
-}
-
-__device__ __forceinline__ float sum4(const uint64_t (&v)[4]) {
-  float s[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float a, b;
-    ptx::f32x2_unpack(v[i], a, b);
-    s[i] = a + b;
-  }
-  return (s[0] + s[1]) + (s[2] + s[3]);
+__device__ __forceinline__ float sum2(const uint64_t (&v)[2]) {
+  float a, b;
+  ptx::f32x2_unpack(ptx::f32x2_add(v[0], v[1]), a, b);
+  return a + b;
 }
 
 // The place of column group c4 (4 values) of a row in a partial result.
@@ -381,7 +403,8 @@ __device__ __forceinline__ float4* part_at(char* part, int c4, int row) {
 
 // One row over positions [from, to], computed again by a warp from the definition:
 // lanes hold D / 32 columns each.  Rows whose sums are not finite come here, because
-// in a product with P = 0 a value that is not finite reaches rows that do not see it.
+// in a product with P = 0 a value that is not finite reaches rows that do not see it,
+// and rows that saw powers too far apart.
 template <int D, bool E4M3>
 __device__ __forceinline__ void row_again(const PagedArgs& a, int b, int r, int h, int head, int64_t t, int from, int to, int lane,
                                        float (&o)[D / 32], float& ref, float& l) {
@@ -427,8 +450,12 @@ __device__ __forceinline__ void row_again(const PagedArgs& a, int b, int r, int 
   }
 }
 
+struct PoolMaps {                              // bf16 pools with pages of 16 rows and more
+  CUtensorMap K[FCC_MAX_RANKS], V[FCC_MAX_RANKS];
+};
+
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ PagedArgs a, unsigned long long timeout_ns) {
+__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PoolMaps maps, unsigned long long timeout_ns) {
   constexpr uint32_t kTile = kTileBytes<D>;
   constexpr uint32_t kFormat = E4M3 ? 0u : (1u << 7) | (1u << 10);   // f16 or bf16 operands
   constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
@@ -441,13 +468,16 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   uint8_t* sQ = smem;
   uint8_t* sR = sQ + 2 * kTile;
   Columns* cols = reinterpret_cast<Columns*>(sR + kSlots * kTile);
-  uint64_t* r_full = reinterpret_cast<uint64_t*>(cols + kCols);  // [kSlots], four loading warps
+  WarpWalk* walks = reinterpret_cast<WarpWalk*>(cols + kCols);
+  uint8_t* stages = reinterpret_cast<uint8_t*>(walks + kWalks);
+  Run* run = reinterpret_cast<Run*>(stages + 8 * 32 * kStageRow);
+  uint64_t* r_full = reinterpret_cast<uint64_t*>(run + 1);  // [kSlots], four loading warps
   uint64_t* r_empty = r_full + kSlots;         // [kSlots]
   uint64_t* c_full = r_empty + kSlots;         // [kCols], four loading warps
   uint64_t* q_full = c_full + kCols;           // [2]: Q_t written, the tile's four softmax warps
   uint64_t* s_full = q_full + 2;               // [2]: S_t complete
-  uint64_t* p_full = s_full + 2;               // [2]: P_t written (and O_t rescaled)
-  uint64_t* o_full = p_full + 2;               // [2]: an item's products of tile t complete
+  uint64_t* p_full = s_full + 2;               // [2][2]: half of P_t written (and O_t rescaled)
+  uint64_t* o_full = p_full + 4;               // [2]: an item's products of tile t complete
   uint64_t* mma_done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -462,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&q_full[t], 4);
       ptx::mbar_init(&s_full[t], 1);
-      ptx::mbar_init(&p_full[t], 4);
+      ptx::mbar_init(&p_full[2 * t], 4);
+      ptx::mbar_init(&p_full[2 * t + 1], 4);
       ptx::mbar_init(&o_full[t], 1);
     }
     ptx::mbar_init(mma_done, 1);
@@ -480,14 +511,20 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   const ptx::Waiter W{abort_flag, a.status, timeout_ns};
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  const Layout lay = layout_of(D, a.step.B, gridDim.x);
-  const Totals tot = *reinterpret_cast<const Totals*>(a.ws);
-  Header* const headers = reinterpret_cast<Header*>(a.ws + lay.headers);
-  if (threadIdx.x == 0) headers[blockIdx.x] = Header{0, 0, 0, 0};
-  const bool busy = static_cast<int>(blockIdx.x) < tot.ctas;
-  const long long u0 = busy ? blockIdx.x * tot.units / tot.ctas : 0;
-  const long long u1 = busy ? (blockIdx.x + 1) * tot.units / tot.ctas : 0;
-  const Start start = busy ? reinterpret_cast<const Start*>(a.ws + lay.starts)[blockIdx.x] : Start{0, 0, 0, 0};
+  if (threadIdx.x == 0) {
+    const Layout lay = layout_of(D, a.step.B, gridDim.x);
+    const Totals tot = *reinterpret_cast<const Totals*>(a.ws);
+    reinterpret_cast<Header*>(a.ws + lay.headers)[blockIdx.x] = Header{0, 0, 0, 0};
+    const int c = blockIdx.x;
+    run->units = tot.units;
+    run->ctas = tot.ctas;
+    run->from = c < tot.ctas ? c * tot.units / tot.ctas : 0;
+    run->left = c < tot.ctas ? (c + 1) * tot.units / tot.ctas - run->from : 0;
+    if (c < tot.ctas) run->start = reinterpret_cast<const Start*>(a.ws + lay.starts)[c];
+    run->parts = a.ws + lay.parts;
+    run->header = reinterpret_cast<Header*>(a.ws + lay.headers) + c;
+  }
+  __syncthreads();
 
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(0xffffffffu, W.wait(bar, parity) ? 1 : 0) != 0;
@@ -495,69 +532,63 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 
   if (warp >= 12) {
     // ----------------------------------------------------------- MMA issue
-    regs_dec<kRegsIssue>();
-    if (warp == 12 && lane == 0 && busy) {
-      Walk w;
+    regs_dec<Regs<E4M3>::kIssue>();
+    if (warp == 12 && lane == 0) {
+      // (what the loop over blocks needs is in registers: this thread's own instructions
+      // stand between one product and the next)
+      Walk& w = walks[12].now;
       bool any = false, ok = true;
-      bool more = w.begin(a, start, u1 - u0);
-      uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-      uint32_t u = 0;                          // ring position of the item's first K
+      bool more = w.begin(a, run->start, run->left);
+      uint32_t q_phase = 0, p_phase = 0;       // bit t: the parity that Q_t / P_t will complete
+      uint32_t u = 0;                          // ring position of the block's K, V is at u + 1
+      const uint64_t qd0 = desc_of(sQ, 16), kd0 = desc_of(sR, 16), vd0 = desc_of(sR, kAtom);
+      // O_t += P_t V, the V at ring position `pos`.
+      auto issue_pv = [&](int t, uint32_t pos, bool first) -> bool {
+        const uint64_t vd = vd0 + (pos % kSlots) * (kTile >> 4);
+        const uint32_t pa = tmem_base + t * 128, o = tmem_base + kColO + t * 128;
+        const uint32_t parity = p_phase >> t & 1u;
+        if (!W.wait(&p_full[2 * t], parity)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          ptx::mma_f16_tmem_a(o, pa + kk * 8, vd + step_mnmajor(kk), kIdescO, (!first || kk > 0) ? 1u : 0u);
+        if (!W.wait(&p_full[2 * t + 1], parity)) return false;
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int kk = 4; kk < 8; ++kk) ptx::mma_f16_tmem_a(o, pa + kk * 8, vd + step_mnmajor(kk), kIdescO, 1u);
+        p_phase ^= 1u << t;
+        return true;
+      };
+      auto issue_s = [&](int t) {
+        const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (u % kSlots) * (kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ptx::mma_f16(tmem_base + t * 128, qd + step_kmajor(kk), kd + step_kmajor(kk), kIdescS, kk > 0 ? 1u : 0u);
+        ptx::mma_commit(&s_full[t]);
+      };
       while (more && ok) {
-        bool first[2] = {true, true};          // O_t holds nothing of this item yet
-        uint32_t pend[2] = {0, 0};                      // ring position of the V whose product is next
-        bool pending[2] = {false, false};
-        for (int t = 0; t < 2 && ok; ++t)
-          if (w.active(t)) ok = W.wait(&q_full[t], nq[t]++ & 1u);
-        auto issue_pv = [&](int t) -> bool {
-          const uint32_t pos = pend[t];
-          pending[t] = false;
-          if (!W.wait(&r_full[pos % kSlots], (pos / kSlots) & 1u)) return false;
-          if (!W.wait(&p_full[t], np[t] & 1u)) return false;
-          ++np[t];
+        const int ja = w.ja, jb = w.jb, lo0 = w.lo[0], hi0 = w.hi[0], lo1 = w.lo[1], hi1 = w.hi[1];
+        any = true;
+        if (lo0 < hi0) ok = W.wait(&q_full[0], q_phase & 1u), q_phase ^= 1u;
+        if (ok && lo1 < hi1) ok = W.wait(&q_full[1], q_phase >> 1 & 1u), q_phase ^= 2u;
+        // one step more than there are blocks: the last one's P V
+        for (int j = ja; j <= jb && ok; ++j, u += 2) {
+          if (j < jb && !(ok = W.wait(&r_full[u % kSlots], u / kSlots & 1u))) break;
+          if (j > ja && !(ok = W.wait(&r_full[(u - 1) % kSlots], (u - 1) / kSlots & 1u))) break;
           ptx::tc_fence_after();
-          const uint32_t va = ptx::smem_addr(sR + (pos % kSlots) * kTile);
-#pragma unroll
-          for (int kk = 0; kk < kBlock / 16; ++kk)
-            ptx::mma_f16_tmem_a(tmem_base + kColO + t * 128, tmem_base + t * 128 + kk * 8, desc_mnmajor(va, kk), kIdescO,
-                                (!first[t] || kk > 0) ? 1u : 0u);
-          first[t] = false;
-          any = true;
-          return true;
-        };
-        for (int j = w.ja; j < w.jb && ok; ++j, u += 2) {
-          if (!(ok = W.wait(&r_full[u % kSlots], (u / kSlots) & 1u))) break;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (ok && pending[t]) ok = issue_pv(t);
-            if (ok && w.sees(j, t)) {
-              const uint32_t qa = ptx::smem_addr(sQ + t * kTile), ka = ptx::smem_addr(sR + (u % kSlots) * kTile);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                ptx::mma_f16(tmem_base + t * 128, desc_kmajor(qa, kk), desc_kmajor(ka, kk), kIdescS, kk > 0 ? 1u : 0u);
-              ptx::mma_commit(&s_full[t]);
-              any = true;
-              pending[t] = true;
-              pend[t] = u + 1;
-            }
-          }
-          if (!ok) break;
+          if (j > lo0 && j <= hi0 && !(ok = issue_pv(0, u - 1, j == lo0 + 1))) break;
+          if (j >= lo0 && j < hi0) issue_s(0);
+          if (j > lo1 && j <= hi1 && !(ok = issue_pv(1, u - 1, j == lo1 + 1))) break;
+          if (j >= lo1 && j < hi1) issue_s(1);
           // K_j is free once both tiles' S are done, V_{j-1} once both P V are
-          ptx::mma_commit(&r_empty[u % kSlots]);
-          if (j > w.ja) ptx::mma_commit(&r_empty[(u - 1) % kSlots]);
+          if (j < jb) ptx::mma_commit(&r_empty[u % kSlots]);
+          if (j > ja) ptx::mma_commit(&r_empty[(u - 1) % kSlots]);
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          if (ok && pending[t]) ok = issue_pv(t);
-        if (ok) {
-          // (a V that no tile's last block used has to have arrived all the same)
-          ok = W.wait(&r_full[(u - 1) % kSlots], ((u - 1) / kSlots) & 1u);
-          ptx::mma_commit(&r_empty[(u - 1) % kSlots]);
-          for (int t = 0; t < 2; ++t)
-            if (w.active(t)) ptx::mma_commit(&o_full[t]);
-          any = true;
-        }
-        more = ok && w.next_item(a);
+        if (!ok) break;
+        u -= 2;                                // (the step more had no block)
+        if (lo0 < hi0) ptx::mma_commit(&o_full[0]);
+        if (lo1 < hi1) ptx::mma_commit(&o_full[1]);
+        more = w.next_item(a);
       }
       if (any) {
         ptx::mma_commit(mma_done);
@@ -568,53 +599,80 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     // ------------------------------------------------------------- loading
     // Warp 8 + i brings positions 32 i .. 32 i + 31 of each block.  A lane looks up
     // one of them, a block ahead.
-    regs_dec<kRegsLoad>();
+    regs_dec<Regs<E4M3>::kLoad>();
     const int wl = warp - 8;
     constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kN = 32 / kAtOnce;
     const int chunk = lane % kLanes;
-    if (busy) {
-      Walk w;
-      bool more = w.begin(a, start, u1 - u0);
+    if (run->left > 0) {
+      WarpWalk& ww = walks[warp];
+      Walk& w = ww.now;
+      ww.begin(a, run->start, run->left, lane);
       int j = w.ja;                            // the block that is looked up next
-      int page = -1, in_page = 0, nr = 0, nh = 0;
-      bool have = false;                       // a block has been looked up
+      int page = -1, in_page = 0, r = 0, h = 0;  // this lane's position in the block looked up last
+      bool have = false;
       auto look_up = [&]() {
-        have = more;
+        have = w.more;
         page = -1;
-        if (!more) return;
-        const long long rows = min(static_cast<long long>(w.q.n) * a.G, (w.pair + 1ll) * kPairRows);
-        const int last = w.q.ok ? w.q.L - w.q.n + static_cast<int>((rows - 1) / a.G) : -1;
+        if (!have) return;
         const long long pos = static_cast<long long>(j) * kBlock + 32 * wl + lane;
-        nr = w.rank(a);
-        nh = w.head(a);
-        if (pos <= last) {
+        r = w.rank(a);
+        h = w.head(a);
+        if (w.q.ok && pos < w.q.L) {
           page = page_of(a.step, a.pool.pages, w.b, static_cast<int>(pos >> a.pool.log2P));
           in_page = static_cast<int>(pos) & ((1 << a.pool.log2P) - 1);
-          // (positions before every row's window were given back, perhaps)
-          if (page < 0 && pos > static_cast<long long>(w.q.L - w.q.n + static_cast<int>(static_cast<long long>(w.pair) * kPairRows / a.G)) - a.window)
-            record_invalid(a.status);
+          if (page < 0) {
+            // (positions that no row sees need no page: before every row's window, or
+            // behind the last row)
+            const int first = w.q.L - w.q.n + a.by_g(w.pair * kPairRows);
+            const int last = w.q.L - w.q.n + a.by_g(min(w.q.n * a.G - w.pair * kPairRows, kPairRows) + w.pair * kPairRows - 1);
+            if (pos <= last && pos > static_cast<long long>(first) - a.window) record_invalid(a.status);
+          }
         }
         if (++j == w.jb) {
-          more = w.next_item(a);
+          ww.next(a, lane);
           j = w.ja;
         }
       };
-      look_up();
-      uint32_t u = 0;
+      // Number of this lane's position's row in its rank's pools, -1 for none.
+      auto row_of = [&]() -> int64_t {
+        return page < 0 ? -1 : ((static_cast<int64_t>(page) * a.pool.H + h) << a.pool.log2P) + in_page;
+      };
+      uint32_t u = 0, blk = 0;
       bool ok = true;
-      while (have && ok) {
-        const int64_t row = page < 0 ? -1 : ((static_cast<int64_t>(page) * a.pool.H + nh) << a.pool.log2P) + in_page;
-        const int r = nr;
+      auto wait_slot = [&]() -> bool { return wait_warp(&r_empty[u % kSlots], ((u / kSlots) & 1u) ^ 1u); };
+      // (called once the block's key slot is free: the products of the block that had
+      // these constants four blocks ago were issued before the slot was handed back)
+      uint32_t fk = 0, fv = 0;                 // e4m3: this lane's position's factors
+      auto constants = [&](int64_t row, int ke, int ve) {
+        Columns& cc = cols[blk % kCols];
         const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
-        uint32_t ke = 127, ve = 127;
         if constexpr (E4M3) {
-          if (row >= 0) {
-            ke = a.pool.Ke[r][row];
-            ve = a.pool.Ve[r][row];
+          ke = min(ke, 254);
+          ve = min(ve, 254);
+          const int A = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? ke : 1));
+          const int B = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? ve : 1));
+          const bool wide = __any_sync(0xffffffffu, row >= 0 && (too_wide(ke, A) || too_wide(ve, B)));
+          fk = f16_power(ke, A);
+          fv = f16_power(ve, B);
+          if (lane == 0) {
+            cc.ka[wl] = __int_as_float(A << 23);
+            cc.vb[wl] = static_cast<float>(B - 127);
+            cc.vi[wl] = __int_as_float((254 - B) << 23);
+            cc.wide[wl] = wide;
           }
         }
-        uint4 x[kN];
-        auto fetch = [&](const char* pool) {   // e4m3: into registers
+        if (lane == 0) {
+          cc.there[wl] = there;
+          ptx::mbar_arrive(&c_full[blk % kCols]);
+        }
+        ++blk;
+      };
+      look_up();
+      if constexpr (E4M3) {
+        // A block's keys are fetched into registers while the block before's values
+        // are converted, and the other way round.
+        uint4 xk[kN], xv[kN];
+        auto fetch = [&](uint4 (&x)[kN], const char* pool, int64_t row) {
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
             const int64_t src = __shfl_sync(0xffffffffu, row, i * kAtOnce + lane / kLanes);
@@ -622,79 +680,102 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             if (src >= 0) x[i] = *reinterpret_cast<const uint4*>(pool + src * kRow + chunk * 16);
           }
         };
-        if constexpr (E4M3) fetch(a.pool.K[r]);
-        look_up();
+        auto convert = [&](const uint4 (&x)[kN], uint32_t power) {
+          uint8_t* dst = sR + (u % kSlots) * kTile;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++u) {
-          const uint32_t slot = u % kSlots;
-          if (!(ok = wait_warp(&r_empty[slot], ((u / kSlots) & 1u) ^ 1u))) break;
-          if (kv == 0) {
-            // (the block that used these constants four blocks ago is done: its
-            // products were issued before the slot's last occupant was handed back)
-            const uint32_t blk = u / 2;
-            Columns& cc = cols[blk % kCols];
-            if constexpr (E4M3) {
-              const int ev = min(static_cast<int>(ve), 254), i = 32 * wl + lane;
-              cc.ka[i] = __int_as_float(static_cast<int>(ke) << 23);
-              cc.vb[i] = static_cast<float>(ev - 127);
-              cc.vi[i] = __int_as_float((254 - ev) << 23);
-            }
-            if (lane == 0) cc.there[wl] = there;
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&c_full[blk % kCols]);
+          for (int i = 0; i < kN; ++i) {
+            const int tok = 32 * wl + i * kAtOnce + lane / kLanes;
+            const uint32_t f = __shfl_sync(0xffffffffu, power, tok & 31);
+            auto f16 = [&](uint32_t codes) { return mul_f16x2(f16x2_of_e4m3(codes), f); };
+            *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk)) =
+                make_uint4(f16(x[i].x), f16(x[i].x >> 16), f16(x[i].y), f16(x[i].y >> 16));
+            *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk + 1)) =
+                make_uint4(f16(x[i].z), f16(x[i].z >> 16), f16(x[i].w), f16(x[i].w >> 16));
           }
-          uint8_t* dst = sR + slot * kTile;
-          if constexpr (E4M3) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&r_full[u % kSlots]);
+          ++u;
+        };
+        int64_t row = row_of();
+        int ke = 1, ve = 1;
+        auto fetch_exps = [&]() {
+          if (row >= 0) {
+            ke = a.pool.Ke[r][row];
+            ve = a.pool.Ve[r][row];
+          }
+        };
+        bool full = have;
+        if (full) {
+          fetch(xk, a.pool.K[r], row);
+          fetch(xv, a.pool.V[r], row);
+          fetch_exps();
+        }
+        while (full) {
+          look_up();                           // the next block
+          if (!(ok = wait_slot())) break;
+          constants(row, ke, ve);
+          convert(xk, fk);
+          row = row_of();
+          if (have) {
+            fetch(xk, a.pool.K[r], row);
+            fetch_exps();
+          }
+          if (!(ok = wait_slot())) break;
+          convert(xv, fv);
+          if (have) fetch(xv, a.pool.V[r], row);
+          full = have;
+        }
+      } else {
+        // A warp's 32 positions come by TMA, a box of a page's rows and 64 columns at a
+        // time, if they are all there (kBoxes: pages of 16 rows and more); otherwise,
+        // at a sequence's end, through registers, with zeros for what is not.
+        const int box = min(32, 1 << a.pool.log2P);
+        while (have) {
+          const int64_t row = row_of();
+          const int page_now = page, in_page_now = in_page, rr = r, hh = h;
+          const bool boxes = a.boxes && __all_sync(0xffffffffu, page >= 0);
+          look_up();
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              const int tok = 32 * wl + i * kAtOnce + lane / kLanes;
-              uint4 lo, hi;
-              lo.x = f16x2_of_e4m3(x[i].x);
-              lo.y = f16x2_of_e4m3(x[i].x >> 16);
-              lo.z = f16x2_of_e4m3(x[i].y);
-              lo.w = f16x2_of_e4m3(x[i].y >> 16);
-              hi.x = f16x2_of_e4m3(x[i].z);
-              hi.y = f16x2_of_e4m3(x[i].z >> 16);
-              hi.z = f16x2_of_e4m3(x[i].w);
-              hi.w = f16x2_of_e4m3(x[i].w >> 16);
-              *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk)) = lo;
-              *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk + 1)) = hi;
-            }
-            if (kv == 0) fetch(a.pool.V[r]);
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&r_full[slot]);
-          } else {
-            const char* pool = kv == 0 ? a.pool.K[r] : a.pool.V[r];
-            const uint32_t d32 = ptx::smem_addr(dst);
+          for (int kv = 0; kv < 2; ++kv, ++u) {
+            if (!(ok = wait_slot())) break;
+            if (kv == 0) constants(row, 0, 0);
+            uint8_t* dst = sR + (u % kSlots) * kTile;
+            uint64_t* bar = &r_full[u % kSlots];
+            if (boxes) {
+              if (lane == 0) ptx::mbar_arrive_expect_tx(bar, 32 * D * 2);
+              __syncwarp();                    // the bytes are expected before any arrive
+              if ((lane & (box - 1)) == 0) {
+                const CUtensorMap* map = kv == 0 ? &maps.K[rr] : &maps.V[rr];
 #pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              const int tok = i * kAtOnce + lane / kLanes;
-              const int64_t src = __shfl_sync(0xffffffffu, row, tok);
-              cp_async16(d32 + tile_at(32 * wl + tok, chunk), pool + max(src, static_cast<int64_t>(0)) * kRow + chunk * 16, src >= 0);
-            }
-            cp_async_commit();
-            // the slot filled two steps ago: every lane's loads have arrived
-            if (u >= 2) {
-              cp_async_wait<2>();
+                for (int x = 0; x < D / 64; ++x)
+                  ptx::tma_load_4d(dst + x * kAtom + (32 * wl + lane) * 128, map, bar, 64 * x, in_page_now, hh, page_now);
+              }
+            } else {
+              const char* pool = kv == 0 ? a.pool.K[rr] : a.pool.V[rr];
+#pragma unroll 4
+              for (int i = 0; i < kN; ++i) {
+                const int tok = i * kAtOnce + lane / kLanes;
+                const int64_t src = __shfl_sync(0xffffffffu, row, tok);
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (src >= 0) x = *reinterpret_cast<const uint4*>(pool + src * kRow + chunk * 16);
+                *reinterpret_cast<uint4*>(dst + tile_at(32 * wl + tok, chunk)) = x;
+              }
               ptx::fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) ptx::mbar_arrive(&r_full[(u - 2) % kSlots]);
+              if (lane == 0) ptx::mbar_arrive(bar);
             }
           }
+          if (!ok) break;
         }
-      }
-      if constexpr (!E4M3) {
-        cp_async_wait<0>();
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0)
-          for (uint32_t v = u >= 2 ? u - 2 : 0; v < u; ++v) ptx::mbar_arrive(&r_full[v % kSlots]);
+        if (*abort_flag && a.boxes)            // copies in flight land before the block ends
+          for (uint32_t v = u >= kSlots ? u - kSlots : 0; v < u; ++v)
+            W.drain(&r_full[v % kSlots], (v / kSlots) & 1u, kDrainNs);
       }
     }
   } else {
     // ------------------------------------------------- softmax and output
-    regs_inc<kRegsSoftmax>();
+    regs_inc<Regs<E4M3>::kSoftmax>();
     const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;       // of the tile
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -702,61 +783,64 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const uint32_t o_addr = lane_addr + kColO + t * 128;
     uint32_t ns = 0, items = 0, blk0 = 0;      // this tile's blocks and items, the CTA's blocks before this item
     bool ok = true;
-    Walk w;
-    bool more = busy && w.begin(a, start, u1 - u0);
+    WarpWalk& ww = walks[warp];
+    Walk& w = ww.now;
+    ww.begin(a, run->start, run->left, lane);
     float c = 0.f;                             // what a score is multiplied by
-    long long at = u0;
     // This thread's row of a new item's Q_t; its place among the token rows.
     int64_t token = 0;
     int head = 0, qpos = -1;
     bool live = false;
     auto load_q = [&]() {
-      const long long rho = static_cast<long long>(w.pair) * kPairRows + t * kTileRows + row;
-      live = rho < static_cast<long long>(w.q.n) * a.G;
-      const int i = static_cast<int>(rho / a.G);
+      const int rho = w.pair * kPairRows + t * kTileRows + row;
+      live = rho < w.q.n * a.G;
+      const int i = a.by_g(rho);
       token = static_cast<int64_t>(w.q.s) + i;
-      head = w.head(a) * a.G + static_cast<int>(rho % a.G);
+      head = w.head(a) * a.G + (rho - i * a.G);
       qpos = live && w.q.ok ? w.q.L - w.q.n + i : -1;
       if (!w.active(t)) return;
-      const char* src = a.Q[w.rank(a)] + (token * a.ldq + static_cast<int64_t>(head) * D) * 2;
+      // A row's 16-byte pieces lie on kQ neighbouring lanes, for whole lines of memory.
+      constexpr int kQ = D / 8, kRows = 32 / kQ;
+      const char* mine = live ? a.Q[w.rank(a)] + (token * a.ldq + static_cast<int64_t>(head) * D) * 2 : nullptr;
       uint8_t* dst = sQ + t * kTile;
       c = a.scale_log2;
-      float f = 1.f;
-      if constexpr (E4M3) {
-        unsigned top = 0;
 #pragma unroll 4
-        for (int k = 0; k < D / 8; ++k) {
-          const uint4 v = live ? *reinterpret_cast<const uint4*>(src + k * 16) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < kQ; ++i) {
+        const int from = i * kRows + lane / kQ;
+        const char* src = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (src != nullptr) v = *reinterpret_cast<const uint4*>(src + (lane % kQ) * 16);
+        if constexpr (E4M3) {
+          unsigned top = 0;
           for (uint32_t y : {v.x, v.y, v.z, v.w}) {
             const unsigned m0 = y & 0x7fffu, m1 = (y >> 16) & 0x7fffu;
             top = max(top, max(m0 < 0x7f80u ? m0 : 0u, m1 < 0x7f80u ? m1 : 0u));
           }
-        }
-        const int e = max(static_cast<int>(top >> 7) - 127, -100) - 14;
-        f = power_of_two(-e);
-        c *= power_of_two(e);
-      }
-#pragma unroll 4
-      for (int k = 0; k < D / 8; ++k) {
-        uint4 v = live ? *reinterpret_cast<const uint4*>(src + k * 16) : make_uint4(0, 0, 0, 0);
-        if constexpr (E4M3) {
-          auto f16 = [&](uint32_t y) {
-            return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f);
-          };
+#pragma unroll
+          for (int k = 1; k < kQ; k *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+          const int e = max(static_cast<int>(top >> 7) - 127, -100) - 14;
+          const float f = power_of_two(-e);
+          auto f16 = [&](uint32_t y) { return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f); };
           v = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));
+          const int own = __shfl_sync(0xffffffffu, e, lane % kRows * kQ);   // of row i kRows + lane % kRows
+          if (lane / kRows == i) c = a.scale_log2 * power_of_two(own);
         }
-        *reinterpret_cast<uint4*>(dst + tile_at(row, k)) = v;
+        *reinterpret_cast<uint4*>(dst + tile_at(32 * quarter + from, lane % kQ)) = v;
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&q_full[t]);
     };
+    bool more = w.more;
     if (more) load_q();
-    while (more && ok) {
+    while (more) {
       float ref = -INFINITY, l = 0.f;
+      uint32_t wide = 0;
+      float late = -INFINITY;                  // the last block's largest t - ref
       int n = 0;
-      for (int j = w.lo[t]; j < w.hi[t]; ++j) {
-        const uint32_t blk = blk0 + (j - w.ja);
+      const int j_end = w.hi[t];
+      uint32_t blk = blk0 + (w.lo[t] - w.ja);
+      for (int j = w.lo[t]; j < j_end; ++j, ++blk) {
         if (!wait_warp(&s_full[t], ns & 1u) || !wait_warp(&c_full[blk % kCols], (blk / kCols) & 1u)) {
           ok = false;
           break;
@@ -769,96 +853,115 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         const long long first = static_cast<long long>(qpos) - a.window + 1 - base;
         const int cmax = qpos - base, cmin = first > 0 ? static_cast<int>(min(first, 128ll)) : 0;
         const uint4 there = *reinterpret_cast<const uint4*>(cc.there);
-        const bool whole = cmin == 0 && cmax >= kBlock - 1 && (there.x & there.y & there.z & there.w) == 0xffffffffu;
+        const bool whole = cmin <= 0 && cmax >= kBlock - 1 && (there.x & there.y & there.z & there.w) == 0xffffffffu;
         auto seen = [&](int k) -> uint32_t {   // columns 32 k .. 32 k + 31
           const int hi = cmax - 32 * k, lo = cmin - 32 * k;
           uint32_t m = k == 0 ? there.x : k == 1 ? there.y : k == 2 ? there.z : there.w;
           m &= hi < 0 ? 0u : hi >= 31 ? 0xffffffffu : (2u << hi) - 1;
           return m & (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1));
         };
-        uint32_t vb[2][32];
-        bool done = false;
-        if (n > 0 && __all_sync(0xffffffffu, (whole && ref != -INFINITY) || !live)) {
-          // A whole block is exponentiated against the reference as it stands while the
-          // next 32 columns come from TMEM; only a maximum that calls for a raise starts over.
-          uint64_t l2[4] = {0, 0, 0, 0};
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t pk[64];
-          const float sub = live ? ref : 0.f;
-          ptx::tmem_ld_32x32b_x32(s_addr, vb[0]);
-          tmem_ld_wait_regs(vb[0]);
+        const bool mask = !__all_sync(0xffffffffu, whole || !live);
+        auto hide = [&](uint32_t (&x)[32], int k) {  // what the row does not see
+          if (!mask) return;
+          const uint32_t m = seen(k);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (k < 3) ptx::tmem_ld_32x32b_x32(s_addr + 32 * (k + 1), vb[(k + 1) & 1]);
-            exponentials<E4M3, false>(vb[k & 1], c, sub, cc, 32 * k, 0, pk + 16 * k, l2, mx);
-            if (k < 3) tmem_ld_wait_regs(vb[(k + 1) & 1]);
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          if (!__any_sync(0xffffffffu, live && top > kOff + kRaise)) {
-            ptx::tmem_st_32x32b_x32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(pk));
-            ptx::tmem_st_32x32b_x32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(pk + 32));
-            l += sum4(l2);
-            done = true;
-          }
-        }
-        if (!done) {
-          // The maximum first, then the exponentials, in two passes over S.
+          for (int i = 0; i < 32; ++i)
+            if (!(m >> i & 1)) x[i] = 0xff800000u;
+        };
+        bool raise;                            // the row asks for a new reference
+        float to;
+        if (!E4M3 && !mask && __all_sync(0xffffffffu, ref != -INFINITY || !live)) {
+          // bf16, and every row of the warp has a reference: the exponentials follow the
+          // scores as they come, and a block's maximum counts for the next one.
+          raise = late > kRaise<E4M3>;
+          to = ref + late;
+        } else {
           float top = -INFINITY;
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
-            ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, vb[0]);
-            tmem_ld_wait_regs(vb[0]);
-            const uint32_t m = seen(k);
+            uint32_t x[32];
+            ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, x);
+            tmem_ld_wait_regs(x);
+            hide(x, k);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float y = __uint_as_float(vb[0][i]) * c;
-              if constexpr (E4M3) y = fmaf(y, cc.ka[32 * k + i], cc.vb[32 * k + i]);
-              if (m >> i & 1) top = fmaxf(top, y);
-            }
+            for (int i = 0; i < 32; i += 2) mx[i / 2 & 3] = ptx::max3(mx[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            const float m32 = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
+            top = fmaxf(top, E4M3 ? fmaf(m32, c * cc.ka[k], cc.vb[k]) : m32 * c);
           }
-          const bool raise = top > ref + (kOff + kRaise);
-          const float ref_new = raise ? top - kOff : ref;
-          const float f = raise ? ex2_from(ref, ref_new) : 1.f;
-          ref = ref_new;
+          raise = top > ref + (kOff + kRaise<E4M3>);
+          to = top - kOff;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise ? ex2_from(ref, to) : 1.f;
+          if (raise) ref = to;
           l *= f;
-          const float sub = ref == -INFINITY ? 0.f : ref;
-          uint64_t l2[4] = {0, 0, 0, 0};
-          float mx[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t pk[16];
-            ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, vb[0]);
-            tmem_ld_wait_regs(vb[0]);
-            exponentials<E4M3, true>(vb[0], c, sub, cc, 32 * k, seen(k), pk, l2, mx);
-            // (P's columns 16 k .. 16 k + 15 lie over scores already read)
-            ptx::tmem_st_32x32b_x16(s_addr + 16 * k, pk);
-          }
-          l += sum4(l2);
           // S_t was issued after the last P_t V: O_t has no product in flight
-          if (n > 0 && __any_sync(0xffffffffu, raise)) {
 #pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-              ptx::tmem_ld_32x32b_x32(o_addr + k, vb[0]);
-              tmem_ld_wait_regs(vb[0]);
+          for (int k = 0; k < D && n > 0; k += 16) {
+            uint32_t o[16];
+            ptx::tmem_ld_32x32b_x16(o_addr + k, o);
+            ptx::tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) vb[0][i] = __float_as_uint(__uint_as_float(vb[0][i]) * f);
-              ptx::tmem_st_32x32b_x32(o_addr + k, vb[0]);
-            }
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            ptx::tmem_st_32x32b_x16(o_addr + k, o);
           }
         }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_full[t]);
+        late = -INFINITY;
+        // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
+        const float sub = ref == -INFINITY ? 0.f : ref;
+        auto exponentials = [&](uint32_t (&x)[32], int k) {
+          hide(x, k);
+          const float ck = E4M3 ? c * cc.ka[k] : c, rk = E4M3 ? cc.vb[k] - sub : -sub;
+          const uint64_t c2 = ptx::f32x2_pack(ck, ck), r2 = ptx::f32x2_pack(rk, rk);
+          uint64_t l2[2] = {0, 0};
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float y0, y1;
+            ptx::f32x2_unpack(ptx::f32x2_fma(ptx::f32x2_pack(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), c2, r2), y0, y1);
+            if constexpr (!E4M3) late = ptx::max3(late, y0, y1);
+            const float p0 = ptx::ex2_approx(y0), p1 = ptx::ex2_approx(y1);
+            l2[i / 2 & 1] = ptx::f32x2_add(l2[i / 2 & 1], ptx::f32x2_pack(p0, p1));
+            pk[i / 2] = pack16<E4M3>(p0, p1);
+          }
+          const float l32 = sum2(l2);
+          l = E4M3 ? fmaf(l32, cc.vi[k], l) : l + l32;
+          // (P's columns 16 k .. 16 k + 15 lie over scores already read)
+          ptx::tmem_st_32x32b_x16(s_addr + 16 * k, pk);
+        };
+        // (rolled loops: thirteen warps in five roles share the instruction caches, and
+        // what they do not hold costs more than the branches)
+        uint32_t x[2][32];
+        ptx::tmem_ld_32x32b_x32(s_addr, x[0]);
+        tmem_ld_wait_regs(x[0]);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ptx::tmem_ld_32x32b_x32(s_addr + 64 * half + 32, x[1]);
+          exponentials(x[0], 2 * half);
+          tmem_ld_wait_regs(x[1]);
+          if (half == 0) ptx::tmem_ld_32x32b_x32(s_addr + 64, x[0]);
+          exponentials(x[1], 2 * half + 1);
+          ptx::tmem_st_wait();                 // half of P is in place
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&p_full[2 * t + half]);
+          tmem_ld_wait_regs(x[0]);
+        }
+        if constexpr (E4M3) {
+          const uint4 w4 = *reinterpret_cast<const uint4*>(cc.wide);
+          wide |= w4.x | w4.y | w4.z | w4.w;
+        }
         ++n;
       }
       if (!ok) break;
       // The next item's queries: this tile's S are all complete.
-      const Walk cur = w;
+      const Walk& cur = ww.old;
       const int64_t o_token = token;
       const int o_head = head, o_qpos = qpos;
       const bool o_live = live;
-      more = w.next_item(a);
+      ww.next(a, lane);
+      more = w.more;
       if (more) load_q();
       blk0 += cur.jb - cur.ja;
       if (n > 0) {
@@ -871,27 +974,33 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       }
       const int r = cur.rank(a);
       const bool complete = cur.ja == cur.j0 && cur.jb == cur.j1;
-      char* part = a.ws + lay.parts + static_cast<size_t>(2 * blockIdx.x + (cur.ja == cur.j0 ? 1 : 0)) * lay.part_bytes;
+      char* part = run->parts + static_cast<size_t>(2 * blockIdx.x + (cur.ja == cur.j0 ? 1 : 0)) * kPartBytes<D>;
       const int prow = t * kTileRows + row;
       const bool none = l == 0.f;
-      const float inv = complete ? (none ? 0.f : 1.f / l) : 1.f;
-      char* dst = a.O[r] + (o_token * a.ldo + static_cast<int64_t>(o_head) * D) * 2;
-      bool odd = !(fabsf(l) < INFINITY);
+      const float inv = complete ? 1.f / l : 1.f;
+      const char* const dst = o_live ? a.O[r] + (o_token * a.ldo + static_cast<int64_t>(o_head) * D) * 2 : nullptr;
+      bool odd = !(fabsf(l) < INFINITY) || wide != 0;
+      uint8_t* const stage = stages + warp * (32 * kStageRow);
 #pragma unroll 1
       for (int k = 0; k < D; k += 32) {
         uint32_t v[32];
-        if (n > 0) {                           // (the same for the whole tile)
-          ptx::tmem_ld_32x32b_x32(o_addr + k, v);
-          tmem_ld_wait_regs(v);
-        }
+        ptx::tmem_ld_32x32b_x32(o_addr + k, v);
+        tmem_ld_wait_regs(v);
+        uint32_t top = 0;                      // the largest magnitude, as bits
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          const float y = n > 0 && !none ? __uint_as_float(v[i]) * inv : 0.f;
-          odd |= n > 0 && !(fabsf(__uint_as_float(v[i])) < INFINITY);
-          v[i] = __float_as_uint(y);
+          top = max(top, v[i] & 0x7fffffffu);
+          v[i] = __float_as_uint(__uint_as_float(v[i]) * inv);
         }
-        if (!o_live) continue;
+        odd |= n > 0 && top >= 0x7f800000u;
+        if (n == 0 || none) {                  // (O_t holds nothing of this row)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0;
+        }
         if (complete) {
+          // 32 columns of the warp's rows pass through shared memory: four lanes store
+          // 64 bytes of a row
+          uint8_t* const st = stage + lane * kStageRow;
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             uint4 y;
@@ -899,9 +1008,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
             y.y = ptx::pack_bf16x2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
             y.z = ptx::pack_bf16x2(__uint_as_float(v[i + 4]), __uint_as_float(v[i + 5]));
             y.w = ptx::pack_bf16x2(__uint_as_float(v[i + 6]), __uint_as_float(v[i + 7]));
-            *reinterpret_cast<uint4*>(dst + (k + i) * 2) = y;
+            *reinterpret_cast<uint4*>(st + i * 2) = y;
           }
-        } else {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int from = 8 * i + lane / 4;
+            char* to = reinterpret_cast<char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), from));
+            const uint4 y = *reinterpret_cast<const uint4*>(stage + from * kStageRow + (lane & 3) * 16);
+            if (to != nullptr) *reinterpret_cast<uint4*>(to + k * 2 + (lane & 3) * 16) = y;
+          }
+          __syncwarp();
+        } else if (o_live) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
             *part_at(part, (k + i) / 4, prow) = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
@@ -941,12 +1059,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           st[kPairRows + prow] = l;
         }
         if (cur.ja == cur.j0 && threadIdx.x == 0) {
-          const long long last = at + (cur.j1 - cur.j0);
-          headers[blockIdx.x] = Header{static_cast<int>((last * tot.ctas - 1) / tot.units) - static_cast<int>(blockIdx.x) + 1,
-                                       cur.b, cur.rh, cur.pair};
+          // (the CTA's last item: what is behind the item's last block)
+          const long long last = run->from + blk0 - (cur.jb - cur.ja) + (cur.j1 - cur.j0);
+          *run->header = Header{static_cast<int>((last * run->ctas - 1) / run->units) - static_cast<int>(blockIdx.x) + 1,
+                                cur.b, cur.rh, cur.pair};
         }
       }
-      at += cur.jb - cur.ja;
     }
   }
 
@@ -970,8 +1088,8 @@ __global__ void __launch_bounds__(kPairRows) join_kernel(const __grid_constant__
   if (hd.parts == 0) return;
   const Seq q = load_seq(a.step, hd.b);
   const int row = threadIdx.x;
-  const long long rho = static_cast<long long>(hd.pair) * kPairRows + row;
-  if (rho >= static_cast<long long>(q.n) * a.G) return;
+  const int rho = hd.pair * kPairRows + row;
+  if (rho >= q.n * a.G) return;
   auto part = [&](int i) {
     return a.ws + lay.parts + static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * lay.part_bytes;
   };
@@ -990,7 +1108,7 @@ __global__ void __launch_bounds__(kPairRows) join_kernel(const __grid_constant__
       o[4 * i + 3] = fmaf(x.w, f, o[4 * i + 3]);
     }
   }
-  const int r = hd.rh / a.pool.H, head = hd.rh % a.pool.H * a.G + static_cast<int>(rho % a.G);
+  const int r = hd.rh / a.pool.H, head = hd.rh % a.pool.H * a.G + rho % a.G;
   const int64_t token = q.s + rho / a.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t w[8];
@@ -1003,13 +1121,21 @@ __global__ void __launch_bounds__(kPairRows) join_kernel(const __grid_constant__
 }
 
 template <int D, bool E4M3>
-cudaError_t launch(const PagedArgs& a, int ctas, unsigned long long timeout_ns, cudaStream_t st) {
+cudaError_t launch(PagedArgs a, int ctas, unsigned long long timeout_ns, cudaStream_t st) {
+  PoolMaps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  const int P = 1 << a.pool.log2P;
+  a.boxes = !E4M3 && P >= 16 ? 1 : 0;
+  for (int r = 0; r < a.R && a.boxes; ++r)
+    if (internal_pool_map(&maps.K[r], a.pool.K[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)) != FCC_OK ||
+        internal_pool_map(&maps.V[r], a.pool.V[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)) != FCC_OK)
+      return cudaErrorUnknown;
   static bool attr_set[64] = {};
   cudaError_t e = smem_attr_once(attr_set, tiles_kernel<D, E4M3>, kSmem<D>);
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1u, a, ctas)) != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if ((e = launch_pdl(tiles_kernel<D, E4M3>, dim3(grid), dim3(kThreads), kSmem<D>, st, 1u, a, timeout_ns)) != cudaSuccess) return e;
+  if ((e = launch_pdl(tiles_kernel<D, E4M3>, dim3(grid), dim3(kThreads), kSmem<D>, st, 1u, a, maps, timeout_ns)) != cudaSuccess) return e;
   return launch_pdl(join_kernel<D>, dim3(grid, D / 16), dim3(kPairRows), 0, st, 1u, a);
 }
 
