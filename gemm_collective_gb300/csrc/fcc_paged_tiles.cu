@@ -67,8 +67,9 @@ struct Regs {
 };
 constexpr int kMaxCtas = 512;
 
-struct Start {                                 // where a CTA's run begins
+struct Start {                                 // where a CTA's run begins (and the one before it ends)
   int b, rh, pair, j;
+  __device__ __forceinline__ bool same_item(const Start& o) const { return b == o.b && rh == o.rh && pair == o.pair; }
 };
 struct Header {                                // of the item that a CTA begins last and does not finish
   int parts, b, rh, pair;
@@ -85,7 +86,7 @@ constexpr size_t kPartBytes = kPairRows * static_cast<size_t>(D + 2) * 4;
 __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   Layout l;
   l.starts = 256;
-  l.headers = l.starts + static_cast<size_t>(ctas) * sizeof(Start);
+  l.headers = l.starts + (static_cast<size_t>(ctas) + 1) * sizeof(Start);
   l.units = l.headers + static_cast<size_t>(ctas) * sizeof(Header);
   l.parts = (l.units + static_cast<size_t>(B) * 8 + 255) & ~size_t{255};
   l.part_bytes = kPairRows * static_cast<size_t>(d + 2) * 4;
@@ -93,13 +94,16 @@ __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   return l;
 }
 struct Totals {                                // at the workspace's start
-  long long units;
-  int ctas;
+  int ctas;                                    // with work
 };
 
 __device__ __forceinline__ int pairs_of(const PagedArgs& a, const Seq& q) {
   return (q.n * a.G + (kPairRows - 1)) / kPairRows;   // (T * G stays below 2^31 - 256)
 }
+
+// What an item costs beside its blocks, in blocks: its queries' loads, the first S and
+// the last P V that nothing runs beside, its output.
+constexpr int kItemBlocks = 4;
 
 // Blocks [j0, j1) that rows [first, last] of a sequence see.
 struct Range {
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       if (np <= kFewPairs)
         for (int p = 0; p < np; ++p) {
           const Range g = pair_blocks(a, q, p);
-          n += g.j1 - g.j0;
+          n += g.j1 - g.j0 + kItemBlocks;
         }
     }
     for (unsigned m = __ballot_sync(0xffffffffu, np > kFewPairs); m != 0; m &= m - 1) {
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       long long sum = 0;
       for (int p = lane; p < onp; p += 32) {
         const Range g = pair_blocks(a, o, p);
-        sum += g.j1 - g.j0;
+        sum += g.j1 - g.j0 + kItemBlocks;
       }
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -206,7 +210,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       int n = 0;
       if (p < np) {
         const Range g = pair_blocks(a, q, p);
-        n = g.j1 - g.j0;
+        n = g.j1 - g.j0 + kItemBlocks;
       }
       int incl = n;
 #pragma unroll
@@ -217,14 +221,26 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
       const unsigned m = __ballot_sync(0xffffffffu, rest < incl);
       if (m != 0) {
         if (lane == __ffs(m) - 1)
-          starts[c] = Start{b, at_rh, p, static_cast<int>(rest - (incl - n))};
+          // (an item's own cost comes before its first block: no cut falls into it)
+          starts[c] = Start{b, at_rh, p, max(0, static_cast<int>(rest - (incl - n)) - kItemBlocks)};
         break;
       }
       rest -= __shfl_sync(0xffffffffu, incl, 31);
     }
   }
-  if (threadIdx.x == 0) *reinterpret_cast<Totals*>(a.ws) = Totals{total, static_cast<int>(ctas)};
+  if (threadIdx.x == 0) {
+    starts[ctas] = Start{a.step.B, 0, 0, 0};
+    *reinterpret_cast<Totals*>(a.ws) = Totals{static_cast<int>(ctas)};
+  }
 }
+
+// This CTA's run of blocks.
+struct alignas(16) Run {
+  char* parts;
+  Header* header;
+  Start start, stop;
+  bool busy;
+};
 
 // A walk over a CTA's run: item after item, each from block ja to block jb.
 struct Walk {
@@ -232,19 +248,18 @@ struct Walk {
   Seq q;
   int j0, j1;                                  // the item's blocks
   int ja, jb;                                  // the CTA's part of them
-  long long left;                              // blocks of the CTA behind this item's
+  Start stop;                                  // where the run ends
   int lo[2], hi[2];                            // tile t's blocks of [ja, jb): none if lo >= hi
   bool more;                                   // there is such an item
 
-  __device__ __forceinline__ void take(const PagedArgs& a, int skip) {
+  __device__ __forceinline__ bool take(const PagedArgs& a, int skip) {
     const int rows = q.n * a.G, first = pair * kPairRows;
     const Range g = pair_blocks(a, q, pair);
     j0 = g.j0;
     j1 = g.j1;
     ja = j0 + skip;
-    const int n = static_cast<int>(min(static_cast<long long>(j1 - ja), left));
-    jb = ja + n;
-    left -= n;
+    jb = stop.same_item(Start{b, rh, pair, 0}) ? j0 + stop.j : j1;
+    if (ja >= jb) return false;                // (the run ends where the item begins)
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const int r0 = first + t * kTileRows;
@@ -254,20 +269,20 @@ struct Walk {
       lo[t] = max(ja, s.j0);
       hi[t] = min(jb, s.j1);
     }
-  }
-  __device__ __forceinline__ bool begin(const PagedArgs& a, const Start& s, long long units) {
-    left = units;
-    if (left <= 0) return false;               // (s says nothing then)
-    b = s.b;
-    rh = s.rh;
-    pair = s.pair;
-    q = load_seq(a.step, b);
-    pairs = pairs_of(a, q);
-    take(a, s.j);
     return true;
   }
+  __device__ __forceinline__ bool begin(const PagedArgs& a, const Run& r) {
+    if (!r.busy) return false;                 // (its start says nothing then)
+    stop = r.stop;
+    b = r.start.b;
+    rh = r.start.rh;
+    pair = r.start.pair;
+    q = load_seq(a.step, b);
+    pairs = pairs_of(a, q);
+    return take(a, r.start.j);
+  }
   __device__ __forceinline__ bool next_item(const PagedArgs& a) {
-    if (left <= 0) return false;
+    if (stop.same_item(Start{b, rh, pair, 0})) return false;
     if (++pair == pairs) {
       pair = 0;
       if (++rh == a.R * a.pool.H) {
@@ -279,8 +294,7 @@ struct Walk {
         pairs = pairs_of(a, q);
       }
     }
-    take(a, 0);
-    return true;
+    return take(a, 0);
   }
   __device__ __forceinline__ bool sees(int j, int t) const { return j >= lo[t] && j < hi[t]; }
   // Tile t has a block here.  Where it has none, its softmax warps and the issuing
@@ -294,8 +308,8 @@ struct Walk {
 // spare): lane 0 takes the steps.  The softmax warps also keep the item before.
 struct alignas(16) WarpWalk {
   Walk now, old;
-  __device__ __forceinline__ void begin(const PagedArgs& a, const Start& s, long long units, int lane) {
-    if (lane == 0) now.more = now.begin(a, s, units);
+  __device__ __forceinline__ void begin(const PagedArgs& a, const Run& r, int lane) {
+    if (lane == 0) now.more = now.begin(a, r);
     __syncwarp();
   }
   __device__ __forceinline__ void next(const PagedArgs& a, int lane) {
@@ -334,18 +348,8 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// This CTA's run of blocks.
-struct alignas(16) Run {
-  long long units;                             // of all CTAs
-  long long from, left;                        // the first of this one, and how many
-  char* parts;
-  Header* header;
-  Start start;
-  int ctas;
-};
-
 constexpr int kStageRow = 80;                  // 64 bytes of output and 16 that keep lanes apart
-constexpr int kBars = 2 * kSlots + kCols + 2 + 2 + 4 + 2 + 1;
+constexpr int kBars = 2 * kSlots + kCols + 2 + 2 + 2 + 2 + 1;
 
 template <int D>
 constexpr uint32_t kTileBytes = (D / 64) * kAtom;
@@ -476,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   uint64_t* c_full = r_empty + kSlots;         // [kCols], four loading warps
   uint64_t* q_full = c_full + kCols;           // [2]: Q_t written, the tile's four softmax warps
   uint64_t* s_full = q_full + 2;               // [2]: S_t complete
-  uint64_t* p_full = s_full + 2;               // [2][2]: half of P_t written (and O_t rescaled)
-  uint64_t* o_full = p_full + 4;               // [2]: an item's products of tile t complete
+  uint64_t* p_full = s_full + 2;               // [2]: P_t written (and O_t rescaled)
+  uint64_t* o_full = p_full + 2;               // [2]: an item's products of tile t complete
   uint64_t* mma_done = o_full + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -492,8 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&q_full[t], 4);
       ptx::mbar_init(&s_full[t], 1);
-      ptx::mbar_init(&p_full[2 * t], 4);
-      ptx::mbar_init(&p_full[2 * t + 1], 4);
+      ptx::mbar_init(&p_full[t], 4);
       ptx::mbar_init(&o_full[t], 1);
     }
     ptx::mbar_init(mma_done, 1);
@@ -513,14 +516,14 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   ptx::griddep_launch_dependents();
   if (threadIdx.x == 0) {
     const Layout lay = layout_of(D, a.step.B, gridDim.x);
-    const Totals tot = *reinterpret_cast<const Totals*>(a.ws);
-    reinterpret_cast<Header*>(a.ws + lay.headers)[blockIdx.x] = Header{0, 0, 0, 0};
+    const Start* starts = reinterpret_cast<const Start*>(a.ws + lay.starts);
     const int c = blockIdx.x;
-    run->units = tot.units;
-    run->ctas = tot.ctas;
-    run->from = c < tot.ctas ? c * tot.units / tot.ctas : 0;
-    run->left = c < tot.ctas ? (c + 1) * tot.units / tot.ctas - run->from : 0;
-    if (c < tot.ctas) run->start = reinterpret_cast<const Start*>(a.ws + lay.starts)[c];
+    run->busy = c < reinterpret_cast<const Totals*>(a.ws)->ctas;
+    if (run->busy) {
+      run->start = starts[c];
+      run->stop = starts[c + 1];
+    }
+    reinterpret_cast<Header*>(a.ws + lay.headers)[c] = Header{0, 0, 0, 0};
     run->parts = a.ws + lay.parts;
     run->header = reinterpret_cast<Header*>(a.ws + lay.headers) + c;
   }
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       // stand between one product and the next)
       Walk& w = walks[12].now;
       bool any = false, ok = true;
-      bool more = w.begin(a, run->start, run->left);
+      bool more = w.begin(a, *run);
       uint32_t q_phase = 0, p_phase = 0;       // bit t: the parity that Q_t / P_t will complete
       uint32_t u = 0;                          // ring position of the block's K, V is at u + 1
       const uint64_t qd0 = desc_of(sQ, 16), kd0 = desc_of(sR, 16), vd0 = desc_of(sR, kAtom);
@@ -546,16 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       auto issue_pv = [&](int t, uint32_t pos, bool first) -> bool {
         const uint64_t vd = vd0 + (pos % kSlots) * (kTile >> 4);
         const uint32_t pa = tmem_base + t * 128, o = tmem_base + kColO + t * 128;
-        const uint32_t parity = p_phase >> t & 1u;
-        if (!W.wait(&p_full[2 * t], parity)) return false;
+        // (P as a whole: its halves as they come, on a barrier each, were 4 to 13 % slower)
+        if (!W.wait(&p_full[t], p_phase >> t & 1u)) return false;
         ptx::tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
+        for (int kk = 0; kk < kBlock / 16; ++kk)
           ptx::mma_f16_tmem_a(o, pa + kk * 8, vd + step_mnmajor(kk), kIdescO, (!first || kk > 0) ? 1u : 0u);
-        if (!W.wait(&p_full[2 * t + 1], parity)) return false;
-        ptx::tc_fence_after();
-#pragma unroll
-        for (int kk = 4; kk < 8; ++kk) ptx::mma_f16_tmem_a(o, pa + kk * 8, vd + step_mnmajor(kk), kIdescO, 1u);
         p_phase ^= 1u << t;
         return true;
       };
@@ -603,10 +602,10 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     const int wl = warp - 8;
     constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kN = 32 / kAtOnce;
     const int chunk = lane % kLanes;
-    if (run->left > 0) {
+    if (run->busy) {
       WarpWalk& ww = walks[warp];
       Walk& w = ww.now;
-      ww.begin(a, run->start, run->left, lane);
+      ww.begin(a, *run, lane);
       int j = w.ja;                            // the block that is looked up next
       int page = -1, in_page = 0, r = 0, h = 0;  // this lane's position in the block looked up last
       bool have = false;
@@ -785,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     bool ok = true;
     WarpWalk& ww = walks[warp];
     Walk& w = ww.now;
-    ww.begin(a, run->start, run->left, lane);
+    ww.begin(a, *run, lane);
     float c = 0.f;                             // what a score is multiplied by
     // This thread's row of a new item's Q_t; its place among the token rows.
     int64_t token = 0;
@@ -804,12 +803,18 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       const char* mine = live ? a.Q[w.rank(a)] + (token * a.ldq + static_cast<int64_t>(head) * D) * 2 : nullptr;
       uint8_t* dst = sQ + t * kTile;
       c = a.scale_log2;
-#pragma unroll 4
+      uint4 in[kQ];                            // (all loads in flight)
+#pragma unroll
       for (int i = 0; i < kQ; ++i) {
         const int from = i * kRows + lane / kQ;
         const char* src = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), from));
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (src != nullptr) v = *reinterpret_cast<const uint4*>(src + (lane % kQ) * 16);
+        in[i] = make_uint4(0, 0, 0, 0);
+        if (src != nullptr) in[i] = *reinterpret_cast<const uint4*>(src + (lane % kQ) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < kQ; ++i) {
+        const int from = i * kRows + lane / kQ;
+        uint4 v = in[i];
         if constexpr (E4M3) {
           unsigned top = 0;
           for (uint32_t y : {v.x, v.y, v.z, v.w}) {
@@ -942,12 +947,12 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           tmem_ld_wait_regs(x[1]);
           if (half == 0) ptx::tmem_ld_32x32b_x32(s_addr + 64, x[0]);
           exponentials(x[1], 2 * half + 1);
-          ptx::tmem_st_wait();                 // half of P is in place
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&p_full[2 * t + half]);
           tmem_ld_wait_regs(x[0]);
         }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&p_full[t]);
         if constexpr (E4M3) {
           const uint4 w4 = *reinterpret_cast<const uint4*>(cc.wide);
           wide |= w4.x | w4.y | w4.z | w4.w;
@@ -1059,10 +1064,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
           st[kPairRows + prow] = l;
         }
         if (cur.ja == cur.j0 && threadIdx.x == 0) {
-          // (the CTA's last item: what is behind the item's last block)
-          const long long last = run->from + blk0 - (cur.jb - cur.ja) + (cur.j1 - cur.j0);
-          *run->header = Header{static_cast<int>((last * run->ctas - 1) / run->units) - static_cast<int>(blockIdx.x) + 1,
-                                cur.b, cur.rh, cur.pair};
+          // (the CTAs whose runs begin within the item have its other parts)
+          const Start* next = reinterpret_cast<const Start*>(a.ws + layout_of(D, a.step.B, gridDim.x).starts) + blockIdx.x + 1;
+          int parts = 1;
+          while (next[parts - 1].same_item(Start{cur.b, cur.rh, cur.pair, 0})) ++parts;
+          *run->header = Header{parts, cur.b, cur.rh, cur.pair};
         }
       }
     }
