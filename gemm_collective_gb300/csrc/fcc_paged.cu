@@ -4,20 +4,23 @@
 // With few rows every byte of the cache is used once or twice, so DRAM bounds the
 // kernel: it is built to keep loads in flight and every SM busy.
 //
-//  * The work is the list of all (sequence, rank, head, 16 rows) items, each a
-//    run of units of 8 kTok positions.  The list is cut into as many equal runs of
-//    units as there are CTAs (one to an SM), wherever the cuts fall: sequences of all
-//    lengths, or a single long one, load all SMs alike.  An item that a cut goes
+//  * The work is the list of all (sequence, rank, head, tile of 8 NQ rows) items, each
+//    a run of units of kWarps kTok positions.  The list is cut into as many equal runs
+//    of units as there are CTAs (two to an SM), wherever the cuts fall: sequences of
+//    all lengths, or a single long one, load all SMs alike.  An item that a cut goes
 //    through leaves partial sums (O, its reference exponent and l) in the
 //    workspace, at most two from a CTA, and combine_kernel adds an item's in order.
-//  * A unit is 8 slices of kTok positions, one for each warp.  A warp has a ring of
+//  * A unit is kWarps slices of kTok positions, one for each warp.  A warp has a ring of
 //    kStages slices of its own in shared memory, filled by its own cp.async, and
 //    runs through the positions without ever waiting for another warp; the
-//    loads run ahead over the ends of items.  Any page size works: a
-//    position's place is looked up for itself, one slice before its loads.
-//  * S = Q K^T and O += P V on m16n8k16 products of the warp: 16 query rows (a
-//    group's heads, and a few tokens).  At 23 bytes a clock and SM these run
-//    at a fraction of their rate; tensor memory would only add its round trip.
+//    loads run ahead over the ends of items, and one CTA's sums are added up while
+//    the SM's other one still loads.  Any page size works: a position's place is
+//    looked up for itself, one slice before its loads.
+//  * S^T = K Q^T and O^T += V^T P^T on m16n8k16 products of the warp: positions (and
+//    columns of V) fill the 16 rows, the tile's rows come 8 at a time as n, so 8 heads
+//    of one token leave nothing empty.  At 23 bytes a clock and SM these products run
+//    at a fraction of their rate (8.6 clocks each); tensor memory would only add its
+//    round trip.
 //  * e4m3 codes become f16 exactly.  The powers of two never touch them: with
 //    k_j = 2^a_j K_j and v_j = 2^b_j V_j in codes K, V, the exponent of
 //    position j is t_j = 2^a_j (q . K_j) c + b_j in one multiply-add, the sum over V
@@ -38,31 +41,44 @@
 namespace fcc {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kStages = 3;
-constexpr int kHalf = 4096;                    // bytes of a slice's keys (and of its values)
 constexpr float kRaise = 8.f;                  // the reference is raised past this (log2 units)
-constexpr int kRowTile = 16;
-
-// Partial sums of an item: 16 references, 16 sums, 16 x D values as the threads hold them.
-template <int D>
-constexpr int kPartFloats = 2 * kRowTile + kRowTile * D;
 
 struct Header {                                // of the item whose first part CTA c holds last
   int parts;                                   // CTAs from c on (0: none)
   int b, item;
 };
 
-__host__ __device__ inline size_t header_bytes(int ctas) { return (static_cast<size_t>(ctas) * sizeof(Header) + 255) & ~size_t{255}; }
+__host__ __device__ inline size_t header_bytes(int ctas) {
+  return (static_cast<size_t>(ctas) * sizeof(Header) + 255) & ~size_t{255};
+}
 
-template <int D, bool E4M3>
+// Partial sums of an item: its rows' references and sums, then the values as the
+// threads hold them.
+__host__ __device__ constexpr size_t part_floats(int d, int nq) { return 8 * static_cast<size_t>(nq) * (d + 2); }
+
+template <int D, bool E4M3, int NQ>
 struct Few {
   static constexpr int kRow = D * (E4M3 ? 1 : 2);        // bytes of a position's key
+  // Bytes of a slice's keys (and of its values): long slices, because a slice's look-ups
+  // and addresses are as many instructions as 16 positions' products.
+  static constexpr int kHalf = 4096;
   static constexpr int kTok = kHalf / kRow;              // positions of a slice: 16, 32 or 64
+  // 96 KB of rings, two CTAs to an SM: more warps where the registers allow it (8 rows to
+  // an item: 6 warps of 2 slices read 201 x 8000 e4m3 in 330 us, 4 of 3 in 334, 64 x 8192
+  // bf16 in 205 and 210; 16 rows: 4 of 3 take 106 us for 40 x 1-5 rows, 6 of 2 143).
+  static constexpr int kWarps = NQ == 1 ? 6 : 4;
+  static constexpr int kStages = NQ == 1 ? 2 : 3;
   static constexpr int kUnit = kWarps * kTok;
+  static constexpr int kRows = 8 * NQ;                   // of a tile
   static constexpr int kLanes = kRow / 16;               // lanes that load a row
   static constexpr int kRowsAtOnce = 32 / kLanes;
   static constexpr int kPer = (kTok + 31) / 32;          // positions that a lane looks up
+  // a slice in the ring: keys, values, e4m3: the bytes of their powers
+  static constexpr int kStage = 2 * kHalf + (E4M3 ? 2 * kTok : 0);
+  static constexpr int kSmem = kWarps * kStages * kStage;
+  // a warp's values pass through the place of its last slice, a part of the rows at a time
+  static constexpr int kRounds = NQ * 8 * D * 4 > 2 * kHalf ? NQ * 8 * D * 4 / (2 * kHalf) : 1;
+  static constexpr int kQTiles = NQ / kRounds;           // tiles of 8 rows in a round
   // 16-byte chunks are permuted so that eight rows' chunks of one number lie in
   // eight different groups of banks
   static __device__ __forceinline__ uint32_t at(int row, int chunk) {
@@ -96,119 +112,127 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (F16)
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The transpose of the warp's 8 x 8 16-bit values.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 // A walk over a CTA's run of units: item after item, each from unit k to unit end.
+template <int kRows, int kUnit>
 struct Walk {
   int b, item, k, end;
   Seq q;
-  int first;         // the first position of unit 0
+  int seen;          // the first position that a row sees
+  int first;         // the first position of unit 0: 16 positions from a multiple of 16 on lie together
   int nk;            // units of each of the sequence's items
-  int tiles;         // tiles of 16 rows
+  int tiles;         // tiles of kRows rows
   int items;         // R * H * tiles
   long long left;    // units of the CTA behind this item's
+  int r, h, row0;    // the item's rank, head and first row
+  int hi;            // the position of its last row (-1: nothing is seen)
+  int whole_from, whole_to;   // positions in (from, to] are seen by every row
 
   // What sequence `seq` has to do (units of all its items).
-  template <int kUnit>
   __device__ __forceinline__ long long measure(const PagedArgs& a, int seq) {
     b = seq;
     q = load_seq(a.step, seq);
-    tiles = static_cast<int>((static_cast<long long>(q.n) * a.G + kRowTile - 1) / kRowTile);
+    tiles = (q.n * a.G + kRows - 1) / kRows;
     items = a.R * a.pool.H * tiles;
-    first = max(0, q.L - q.n - a.window + 1);
+    seen = max(0, q.L - q.n - a.window + 1);
+    first = seen & ~15;
     nk = q.ok ? static_cast<int>((static_cast<long long>(q.L) - first + kUnit - 1) / kUnit) : 1;
     return static_cast<long long>(items) * nk;
   }
-  __device__ __forceinline__ void take() {
+  __device__ __forceinline__ void take(const PagedArgs& a) {
     const int n = static_cast<int>(min(static_cast<long long>(nk - k), left));
     end = k + n;
     left -= n;
+    const int rh = item / tiles;
+    row0 = (item - rh * tiles) * kRows;
+    r = rh / a.pool.H;
+    h = rh - r * a.pool.H;
+    hi = q.ok ? q.L - q.n + a.by_g(min(q.n * a.G - row0, kRows) + row0 - 1) : -1;
+    whole_from = hi - a.window;
+    whole_to = q.ok ? q.L - q.n + a.by_g(row0) : -1;
   }
-  template <int kUnit>
   __device__ __forceinline__ bool next_item(const PagedArgs& a) {
     if (left <= 0) return false;
     if (++item == items) {
       item = 0;
       do {
         if (b + 1 >= a.step.B) return false;
-      } while (measure<kUnit>(a, b + 1) == 0);
+      } while (measure(a, b + 1) == 0);
     }
     k = 0;
-    take();
+    take(a);
     return true;
   }
-  __device__ __forceinline__ int rank(const PagedArgs& a) const { return item / (a.pool.H * tiles); }
-  __device__ __forceinline__ int head(const PagedArgs& a) const { return item / tiles % a.pool.H; }
-  __device__ __forceinline__ int tile() const { return item % tiles; }
-  // The position of row rho of the sequence's rows (tokens times a group's heads).
-  __device__ __forceinline__ int position(const PagedArgs& a, long long rho) const {
-    return q.L - q.n + static_cast<int>(rho / a.G);
-  }
-  __device__ __forceinline__ long long last_row(const PagedArgs& a) const {
-    return min(static_cast<long long>(q.n) * a.G, (tile() + 1ll) * kRowTile) - 1;
-  }
 };
 
-// An item's sums for the 16 columns that a warp handles: thread `lane` holds rows
-// lane / 4 and + 8 of n-tiles 2 j and 2 j + 1.
+// An item's sums for one product's 16 columns and 8 rows: thread `lane` holds columns
+// lane / 4 and + 8 (in V's order) of rows 2 (lane % 4) and + 1.
 struct Sums {
-  float o[8] = {};
+  float o[4] = {};
   float ref[2] = {-INFINITY, -INFINITY}, l[2] = {};
-  __device__ __forceinline__ void add(const float4& x, const float4& y, const float (&f)[2]) {
-    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(v[i], f[(i >> 1) & 1], o[i]);
+  __device__ __forceinline__ void add(const float4& x, const float (&f)[2]) {
+    o[0] = fmaf(x.x, f[0], o[0]);
+    o[1] = fmaf(x.y, f[1], o[1]);
+    o[2] = fmaf(x.z, f[0], o[2]);
+    o[3] = fmaf(x.w, f[1], o[3]);
   }
 };
 
+// Stores columns 16 j .. 16 j + 15 of rows row0 .. row0 + 7 of a sequence.
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int item, int tiles, int j, int lane,
+__device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int r, int h, int row0, int j, int lane,
                                            const Sums& m) {
-  const int r = item / (a.pool.H * tiles), h = item / tiles % a.pool.H, c = lane & 3;
+  const int g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const long long rho = static_cast<long long>(item % tiles) * kRowTile + (lane >> 2) + 8 * i;
-    if (rho >= static_cast<long long>(q.n) * a.G) continue;
-    const int64_t t = q.s + rho / a.G;
-    const int head = h * a.G + static_cast<int>(rho % a.G);
     const bool none = m.l[i] == 0.f;
-    const float inv = none ? 0.f : 1.f / m.l[i];
-    float v[4];                                // (x0, x1) of n-tile 2 j, (y0, y1) of 2 j + 1
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = none ? 0.f : m.o[(k >> 1) * 4 + 2 * i + (k & 1)] * inv;
-    char* dst = a.O[r] + (t * a.ldo + static_cast<int64_t>(head) * D + 16 * j) * 2;
-    if constexpr (E4M3) {                      // even columns in 2 j, odd ones in 2 j + 1
-      *reinterpret_cast<uint2*>(dst + 8 * c) = make_uint2(ptx::pack_bf16x2(v[0], v[2]), ptx::pack_bf16x2(v[1], v[3]));
-    } else {
-      *reinterpret_cast<uint32_t*>(dst + 4 * c) = ptx::pack_bf16x2(v[0], v[1]);
-      *reinterpret_cast<uint32_t*>(dst + 16 + 4 * c) = ptx::pack_bf16x2(v[2], v[3]);
+    const float inv = 1.f / m.l[i];
+    float x = none ? 0.f : m.o[i] * inv, y = none ? 0.f : m.o[2 + i] * inv;
+    int col = 2 * g;                           // e4m3: columns 2 g and 2 g + 1
+    if constexpr (!E4M3) {                     // columns g and g + 8: neighbours are brought together
+      const float other = __shfl_xor_sync(0xffffffffu, g & 1 ? x : y, 4);
+      col = g & 1 ? g + 7 : g;
+      x = g & 1 ? other : x;
+      y = g & 1 ? y : other;
     }
-    if (j == 0 && c == 0 && a.lse[r] != nullptr)
-      a.lse[r][t * a.Hq + head] = none ? -INFINITY : (m.ref[i] + log2f(m.l[i])) * kLn2;
+    const int rho = row0 + 2 * c + i;
+    if (rho >= q.n * a.G) continue;
+    const int t = a.by_g(rho), head = h * a.G + (rho - t * a.G);
+    const int64_t token = static_cast<int64_t>(q.s) + t;
+    *reinterpret_cast<uint32_t*>(a.O[r] + (token * a.ldo + static_cast<int64_t>(head) * D + 16 * j + col) * 2) = ptx::pack_bf16x2(x, y);
+    if (j == 0 && g == 0 && a.lse[r] != nullptr)
+      a.lse[r][token * a.Hq + head] = none ? -INFINITY : (m.ref[i] + log2f(m.l[i])) * kLn2;
   }
 }
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_constant__ PagedArgs a) {
-  using F = Few<D, E4M3>;
-  constexpr int kTok = F::kTok, kUnit = F::kUnit, kPer = F::kPer;
-  constexpr int kNT = kTok / 8;                // n-tiles of 8 positions
+template <int D, bool E4M3, int NQ>
+__global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_kernel(const __grid_constant__ PagedArgs a) {
+  using F = Few<D, E4M3, NQ>;
+  constexpr int kTok = F::kTok, kUnit = F::kUnit, kPer = F::kPer, kWarps = F::kWarps, kHalf = F::kHalf, kStages = F::kStages;
+  constexpr int kM = kTok / 16;                // products' rows of 16 positions
+  constexpr int kD = D / 16;
   constexpr float kOff = E4M3 ? 6.f : 0.f;     // p up to 2^(kOff + kRaise): f16 holds 2^14, and 2^-38 of it
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[kWarps], s_off;
   __shared__ int s_b;
-  __shared__ float s_ref[kWarps][kRowTile], s_l[kWarps][kRowTile];
+  __shared__ float s_ref[kWarps][F::kRows], s_l[kWarps][F::kRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
@@ -216,12 +240,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
   ptx::griddep_launch_dependents();
 
   // ---------------------------------------------- this CTA's run of units
-  Walk w;
+  Walk<F::kRows, kUnit> w;
   const int per = (a.step.B + kWarps * 32 - 1) / (kWarps * 32);
   const int b_first = min(a.step.B, static_cast<int>(threadIdx.x) * per), b_last = min(a.step.B, b_first + per);
   long long mine = 0;
   for (int b = b_first; b < b_last; ++b) {
-    mine += w.measure<kUnit>(a, b);
+    mine += w.measure(a, b);
     if (blockIdx.x == 0 && !w.q.ok) record_invalid(a.status);
   }
   long long upto = mine;
@@ -246,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
   if (u0 >= from && u0 < from + mine) {
     long long off = u0 - from;
     for (int b = b_first; b < b_last; ++b) {
-      const long long n = w.measure<kUnit>(a, b);
+      const long long n = w.measure(a, b);
       if (off < n) {
         s_b = b;
         s_off = off;
@@ -256,72 +280,112 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
     }
   }
   __syncthreads();
-  w.measure<kUnit>(a, s_b);
+  w.measure(a, s_b);
   w.item = static_cast<int>(s_off / w.nk);
   w.k = static_cast<int>(s_off % w.nk);
   w.left = u1 - u0;
-  w.take();
+  w.take(a);
 
   // ------------------------------------------------------------- loading
   // The loads' own walk runs kStages - 1 slices ahead of the products, and the
   // look-up of the pages one slice more.
-  uint8_t* const ring = smem + warp * (kStages * 2 * kHalf);
+  uint8_t* const ring = smem + warp * (kStages * F::kStage);
   const uint32_t ring_addr = ptx::smem_addr(ring);
   struct Slice {
     uint32_t there[kPer];                      // which positions the pages hold
-    uint32_t exps[kPer];                       // e4m3: this lane's positions' two bytes
   };
-  Walk lw = w;
+  Walk<F::kRows, kUnit> lw = w;
   bool more = true;
-  int page[kPer], in_page[kPer], pool_r = 0, pool_h = 0;
+  int page[kPer], in_page[kPer] = {}, pool_r = 0, pool_h = 0;
+  const int* table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;   // of lw's sequence
+  uint32_t pos = lw.first + lw.k * kUnit + warp * kTok + lane;   // of the next slice's
   auto look_up = [&]() {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) page[i] = -1;
     if (!more) return;
-    const int hi = lw.q.ok ? lw.position(a, lw.last_row(a)) : -1;
-    pool_r = lw.rank(a);
-    pool_h = lw.head(a);
+    pool_r = lw.r;
+    pool_h = lw.h;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int tok = lane + 32 * i;
-      const long long pos = static_cast<long long>(lw.first) + static_cast<long long>(lw.k) * kUnit + warp * kTok + tok;
-      if (tok < kTok && pos <= hi) {
-        page[i] = page_of(a.step, a.pool.pages, lw.b, static_cast<int>(pos >> a.pool.log2P));
-        in_page[i] = static_cast<int>(pos) & ((1 << a.pool.log2P) - 1);
-        if (page[i] < 0) record_invalid(a.status);
+      const uint32_t p = pos + 32 * i;
+      if ((kTok >= 32 || lane < kTok) && p < static_cast<uint32_t>(lw.hi + 1) && p >= static_cast<uint32_t>(lw.seen)) {
+        const uint32_t idx = p >> a.pool.log2P;
+        if (idx < static_cast<uint32_t>(a.step.max_pages)) page[i] = __ldg(table + idx);
+        in_page[i] = p & ((1u << a.pool.log2P) - 1);
+        if (static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.pool.pages)) {
+          page[i] = -1;
+          record_invalid(a.status);
+        }
       }
     }
-    if (++lw.k == lw.end) more = lw.next_item<kUnit>(a);
+    pos += kUnit;
+    if (++lw.k == lw.end) {
+      more = lw.next_item(a);
+      table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;
+      pos = lw.first + lw.k * kUnit + warp * kTok + lane;
+    }
   };
   auto issue = [&](int slot) -> Slice {
     Slice s;
-    int64_t row[kPer];
+    uint32_t any = 0, run = 0xffffffffu;       // run: each 16 positions lie one after another in a page
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       s.there[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
-      s.exps[i] = 0;
-      row[i] = page[i] < 0 ? 0 : ((static_cast<int64_t>(page[i]) * a.pool.H + pool_h) << a.pool.log2P) + in_page[i];
+      any |= s.there[i];
+      const int page0 = __shfl_sync(0xffffffffu, page[i], lane & 16), in_page0 = __shfl_sync(0xffffffffu, in_page[i], lane & 16);
+      const bool next = page[i] >= 0 && page[i] == page0 && in_page[i] == in_page0 + (lane & 15);
+      run &= __ballot_sync(0xffffffffu, next || (kTok < 32 && lane >= kTok));
     }
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) any |= s.there[i];
     if (any != 0) {
-      const char* K = a.pool.K[pool_r];
-      const char* V = a.pool.V[pool_r];
-      if constexpr (E4M3) {
+      int64_t row[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (page[i] >= 0) s.exps[i] = a.pool.Ke[pool_r][row[i]] | (a.pool.Ve[pool_r][row[i]] << 8);
-      }
-      const uint32_t dst = ring_addr + slot * (2 * kHalf);
+      for (int i = 0; i < kPer; ++i)
+        row[i] = page[i] < 0 ? 0 : ((static_cast<int64_t>(page[i]) * a.pool.H + pool_h) << a.pool.log2P) + in_page[i];
+      const int chunk = lane % F::kLanes, sub = lane / F::kLanes;
+      const uint32_t dst = ring_addr + slot * F::kStage;
+      if (run == 0xffffffffu) {                // 16 positions are one piece of memory, 512 bytes to a step
+        constexpr int kSteps = 16 / F::kRowsAtOnce;
+        const char* K = a.pool.K[pool_r] + lane * 16;
+        const char* V = a.pool.V[pool_r] + lane * 16;
 #pragma unroll
-      for (int i = 0; i < kTok / F::kRowsAtOnce; ++i) {
-        const int tok = i * F::kRowsAtOnce + lane / F::kLanes;
-        const int chunk = lane % F::kLanes;
-        const int64_t off = __shfl_sync(0xffffffffu, row[(i * F::kRowsAtOnce) / 32], tok & 31) * F::kRow + chunk * 16;
-        const bool there = s.there[(i * F::kRowsAtOnce) / 32] >> (tok & 31) & 1;
-        cp_async16(dst + F::at(tok, chunk), K + off, there);
-        cp_async16(dst + kHalf + F::at(tok, chunk), V + off, there);
+        for (int n = 0; n < kTok / 16; ++n) {
+          const int64_t off = __shfl_sync(0xffffffffu, row[n / 2], 16 * (n & 1)) * F::kRow;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const uint32_t to = dst + F::at(n * 16 + i * F::kRowsAtOnce + sub, chunk);
+            cp_async16(to, K + off + i * 512, true);
+            cp_async16(to + kHalf, V + off + i * 512, true);
+          }
+        }
+        if constexpr (E4M3) {                  // (through memory like the rest: a register waits for its load)
+          const int64_t at = __shfl_sync(0xffffffffu, row[kPer - 1], lane * 16 & 31);
+          const int64_t at0 = __shfl_sync(0xffffffffu, row[0], lane * 16 & 31);
+          if (lane < 2 * (kTok / 16)) {
+            const int n = lane % (kTok / 16);  // 16 bytes of keys or values
+            const uint8_t* e = lane < kTok / 16 ? a.pool.Ke[pool_r] : a.pool.Ve[pool_r];
+            cp_async16(dst + 2 * kHalf + lane * 16, e + (n < 2 ? at0 : at), true);
+          }
+        }
+      } else {
+        const char* K = a.pool.K[pool_r] + chunk * 16;
+        const char* V = a.pool.V[pool_r] + chunk * 16;
+#pragma unroll
+        for (int i = 0; i < kTok / F::kRowsAtOnce; ++i) {
+          const int tok = i * F::kRowsAtOnce + sub;
+          const int64_t off = __shfl_sync(0xffffffffu, row[(i * F::kRowsAtOnce) / 32], tok & 31) * F::kRow;
+          const bool there = s.there[(i * F::kRowsAtOnce) / 32] >> (tok & 31) & 1;
+          cp_async16(dst + F::at(tok, chunk), K + off, there);
+          cp_async16(dst + kHalf + F::at(tok, chunk), V + off, there);
+        }
+        if constexpr (E4M3) {
+          uint8_t* const e = ring + slot * F::kStage + 2 * kHalf;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const bool there = page[i] >= 0;
+            e[lane + 32 * i] = there ? a.pool.Ke[pool_r][row[i]] : 127;
+            e[kTok + lane + 32 * i] = there ? a.pool.Ve[pool_r][row[i]] : 127;
+          }
+        }
       }
     }
     cp_async_commit();
@@ -340,55 +404,59 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
   int slot = 0;
   long long at = u0;                           // unit that the walk stands at
   do {
-    const int r = w.rank(a), h = w.head(a);
-    const long long row0 = static_cast<long long>(w.tile()) * kRowTile;
-    const int k0 = w.k;
-    const int lo = w.position(a, row0), hi = w.position(a, w.last_row(a));  // the rows' positions
-    int qpos[2];
-    uint32_t qa[D / 16][4];
-    float scale[2];
+    const int k0 = w.k, rows = w.q.n * a.G;
+    // Queries: the thread's row (of n) is g; the scales of its columns' rows 2 c, 2 c + 1.
+    uint32_t qb[NQ][kD][2];
+    float scale[NQ][2], ref[NQ][2], l[NQ][2];
+    int qpos[NQ][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const long long rho = min(row0 + g + 8 * i, w.last_row(a));  // (a row past the last repeats it)
-      qpos[i] = w.position(a, rho);
-      const char* src = a.Q[r] + ((w.q.s + rho / a.G) * a.ldq + (static_cast<int64_t>(h) * a.G + rho % a.G) * D) * 2;
-      scale[i] = a.scale_log2;
+    for (int nq = 0; nq < NQ; ++nq) {
+      const int rho = min(w.row0 + 8 * nq + g, rows - 1), t = a.by_g(rho);   // (a row past the last repeats it)
+      const char* src = a.Q[w.r] + ((static_cast<int64_t>(w.q.s) + t) * a.ldq + static_cast<int64_t>(w.h * a.G + rho - t * a.G) * D) * 2;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
+      for (int kk = 0; kk < kD; ++kk) {
         if constexpr (E4M3) {
           const uint2 x = *reinterpret_cast<const uint2*>(src + kk * 32 + 8 * c);
-          qa[kk][i] = x.x;
-          qa[kk][i + 2] = x.y;
+          qb[nq][kk][0] = x.x;
+          qb[nq][kk][1] = x.y;
         } else {
-          qa[kk][i] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + 4 * c);
-          qa[kk][i + 2] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + 16 + 4 * c);
+          qb[nq][kk][0] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + 4 * c);
+          qb[nq][kk][1] = *reinterpret_cast<const uint32_t*>(src + kk * 32 + 16 + 4 * c);
         }
       }
+      float mine = a.scale_log2;
       if constexpr (E4M3) {
         // the row's largest finite magnitude, as bf16 bits
         unsigned top = 0;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+        for (int kk = 0; kk < kD; ++kk)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const unsigned m = (qa[kk][i + 2 * (j >> 1)] >> (16 * (j & 1))) & 0x7fffu;
+            const unsigned m = (qb[nq][kk][j >> 1] >> (16 * (j & 1))) & 0x7fffu;
             top = max(top, m < 0x7f80u ? m : 0u);
           }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = max(static_cast<int>(top >> 7) - 127, -100) - 14;
         const float f = power_of_two(-e);
-        scale[i] *= power_of_two(e);
+        mine *= power_of_two(e);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
+        for (int kk = 0; kk < kD; ++kk)
 #pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            const uint32_t x = qa[kk][i + j];
-            qa[kk][i + j] = pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t x = qb[nq][kk][j];
+            qb[nq][kk][j] = pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f);
           }
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        scale[nq][i] = __shfl_sync(0xffffffffu, mine, (2 * c + i) * 4);
+        qpos[nq][i] = w.q.ok ? w.q.L - w.q.n + a.by_g(min(w.row0 + 8 * nq + 2 * c + i, rows - 1)) : -1;
+        ref[nq][i] = -INFINITY;
+        l[nq][i] = 0.f;
+      }
     }
-    float o[D / 8][4] = {}, ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[kD][NQ][4] = {};
 
     for (; w.k < w.end; ++w.k) {
       cp_async_wait<kStages - 2>();
@@ -398,8 +466,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
       for (int s = 0; s + 1 < kStages - 1; ++s) queue[s] = queue[s + 1];
       queue[kStages - 2] = issue(slot == 0 ? kStages - 1 : slot - 1);
       look_up();
-      const uint32_t ks = ring_addr + slot * (2 * kHalf), vs = ks + kHalf;
-      uint8_t* const scratch = ring + slot * (2 * kHalf);
+      const uint32_t ks = ring_addr + slot * F::kStage, vs = ks + kHalf;
+      uint8_t* const scratch = ring + slot * F::kStage;
       slot = slot + 1 == kStages ? 0 : slot + 1;
 
       uint32_t any = 0, all = 0xffffffffu;
@@ -409,92 +477,96 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
         all &= kTok < 32 ? cur.there[i] | ~((1u << (kTok & 31)) - 1) : cur.there[i];
       }
       if (any == 0) continue;
-      const int pos0 = static_cast<int>(w.first + static_cast<long long>(w.k) * kUnit + warp * kTok);
+      const int pos0 = w.first + w.k * kUnit + warp * kTok;   // (some position of it is there)
       // every row sees every position (a window reaches back from the last row)
-      const bool whole = all == 0xffffffffu && pos0 <= lo - (kTok - 1) && static_cast<long long>(pos0) > static_cast<long long>(hi) - a.window;
+      const bool whole = all == 0xffffffffu && pos0 <= w.whole_to - (kTok - 1) && pos0 > w.whole_from;
+      auto sees = [&](int mt, int nq, int i) -> bool {
+        const int tok = mt * 16 + g + 8 * (i >> 1), q = qpos[nq][i & 1];
+        const long long pos = static_cast<long long>(pos0) + tok;
+        return (cur.there[mt / 2] >> (tok & 31) & 1) && pos <= q && pos > static_cast<long long>(q) - a.window;
+      };
 
-      float s[kNT][4];
+      // S^T: element i of a product is position g + 8 (i / 2), row 2 c + i % 2
+      float s[kM][NQ][4];
 #pragma unroll
-      for (int np = 0; np < kNT / 2; ++np) {
+      for (int mt = 0; mt < kM; ++mt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[2 * np][i] = s[2 * np + 1][i] = 0.f;
-        const int row = np * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-        uint32_t x[4];
+        for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][nq][i] = 0.f;
+        const int row = mt * 16 + (lane & 15);
+        uint32_t x[4], y[4];
         if constexpr (E4M3) {
 #pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            ldsm4(x, ks + F::at(row, 2 * j + half));
+          for (int j = 0; j < D / 32; ++j) {   // two steps of 16: chunks 2 j and 2 j + 1
+            ldsm4(x, ks + F::at(row, 2 * j + (lane >> 4)));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              mma<true>(s[2 * np], qa[2 * j + i], f16x2_of_e4m3(x[i]), f16x2_of_e4m3(x[i] >> 16));
-              mma<true>(s[2 * np + 1], qa[2 * j + i], f16x2_of_e4m3(x[2 + i]), f16x2_of_e4m3(x[2 + i] >> 16));
+              f16x4_of_e4m3(x[2 * i], y[0], y[2]);
+              f16x4_of_e4m3(x[2 * i + 1], y[1], y[3]);
+#pragma unroll
+              for (int nq = 0; nq < NQ; ++nq) mma<true>(s[mt][nq], y, qb[nq][2 * j + i][0], qb[nq][2 * j + i][1]);
             }
           }
         } else {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            ldsm4(x, ks + F::at(row, 2 * kk + half));
-            mma<false>(s[2 * np], qa[kk], x[0], x[1]);
-            mma<false>(s[2 * np + 1], qa[kk], x[2], x[3]);
+          for (int kk = 0; kk < kD; ++kk) {
+            ldsm4(x, ks + F::at(row, 2 * kk + (lane >> 4)));
+#pragma unroll
+            for (int nq = 0; nq < NQ; ++nq) mma<false>(s[mt][nq], x, qb[nq][kk][0], qb[nq][kk][1]);
           }
         }
       }
-      // exponents (log2 units), and the rows' largest
-      float inv[kNT][2];                       // e4m3: what brings p back to the sum's units
-      float top[2] = {-INFINITY, -INFINITY};
+      // exponents (log2 units), and whether a row asks for a new reference
+      float inv[kM][2];                        // e4m3: what brings p back to the sum's units
+      bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < kNT; ++nt) {
-        float kx[2] = {1.f, 1.f}, vx[2] = {0.f, 0.f};
+      for (int mt = 0; mt < kM; ++mt) {
+        float kx[2], vx[2];
         if constexpr (E4M3) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t e = __shfl_sync(0xffffffffu, cur.exps[nt / 4], (nt * 8 + 2 * c + j) & 31);
-            const int ev = min(static_cast<int>(e >> 8), 254);
-            kx[j] = __int_as_float(static_cast<int>(e & 0xff) << 23);
+            const uint8_t* e = scratch + 2 * kHalf + mt * 16 + g + 8 * j;
+            const int ev = min(static_cast<int>(e[kTok]), 254);
+            kx[j] = __int_as_float(static_cast<int>(e[0]) << 23);
             vx[j] = static_cast<float>(ev - 127);
-            inv[nt][j] = __int_as_float((254 - ev) << 23);
+            inv[mt][j] = __int_as_float((254 - ev) << 23);
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s[nt][i] = E4M3 ? fmaf(s[nt][i] * scale[i >> 1], kx[i & 1], vx[i & 1]) : s[nt][i] * scale[i >> 1];
-        if (!whole) {
+        for (int nq = 0; nq < NQ; ++nq)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int tok = nt * 8 + 2 * c + (i & 1), q = qpos[i >> 1];
-            const long long pos = static_cast<long long>(pos0) + tok;
-            if (!(cur.there[nt / 4] >> (tok & 31) & 1) || pos > q || pos <= static_cast<long long>(q) - a.window)
-              s[nt][i] = -INFINITY;
+            float& t = s[mt][nq][i];
+            t = E4M3 ? fmaf(t * scale[nq][i & 1], kx[i >> 1], vx[i >> 1]) : t * scale[nq][i & 1];
+            if (!whole && !sees(mt, nq, i)) t = -INFINITY;
+            raise |= t > ref[nq][i & 1] + (kOff + kRaise);
           }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top[i >> 1] = fmaxf(top[i >> 1], s[nt][i]);
-      }
-      bool raise = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-        top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-        raise |= top[i] > ref[i] + (kOff + kRaise);
       }
       if (__any_sync(0xffffffffu, raise)) {
-        float f[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f[i] = 1.f;
-          if (top[i] > ref[i] + (kOff + kRaise)) {
-            f[i] = ex2_from(ref[i], top[i] - kOff);
-            ref[i] = top[i] - kOff;
-            l[i] *= f[i];
+        for (int nq = 0; nq < NQ; ++nq) {
+          float f[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float top = -INFINITY;             // the row's largest
+#pragma unroll
+            for (int mt = 0; mt < kM; ++mt) top = ptx::max3(top, s[mt][nq][i], s[mt][nq][2 + i]);
+#pragma unroll
+            for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            f[i] = 1.f;
+            if (top > ref[nq][i] + (kOff + kRaise)) {
+              f[i] = ex2_from(ref[nq][i], top - kOff);
+              ref[nq][i] = top - kOff;
+              l[nq][i] *= f[i];
+            }
           }
+#pragma unroll
+          for (int j = 0; j < kD; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[j][nq][i] *= f[i & 1];
         }
-#pragma unroll
-        for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[j][i] *= f[i >> 1];
       }
-      // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
-      const float sub[2] = {ref[0] == -INFINITY ? 0.f : ref[0], ref[1] == -INFINITY ? 0.f : ref[1]};
       bool plain = true;
       if (!whole) {
         // A value that is not finite must not reach rows that do not see it through
@@ -512,79 +584,82 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
       }
       if (plain) {
 #pragma unroll
-        for (int tg = 0; tg < kNT / 2; ++tg) {
-          uint32_t pa[4];
+        for (int mt = 0; mt < kM; ++mt) {
+          uint32_t pb[NQ][2];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
+          for (int nq = 0; nq < NQ; ++nq) {
             float p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              p[i] = ptx::ex2_approx(s[2 * tg + j][i] - sub[i >> 1]);
-              l[i >> 1] = E4M3 ? fmaf(p[i], inv[2 * tg + j][i & 1], l[i >> 1]) : l[i >> 1] + p[i];
+              // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
+              p[i] = ptx::ex2_approx(s[mt][nq][i] - (ref[nq][i & 1] == -INFINITY ? 0.f : ref[nq][i & 1]));
+              l[nq][i & 1] = E4M3 ? fmaf(p[i], inv[mt][i >> 1], l[nq][i & 1]) : l[nq][i & 1] + p[i];
             }
-            pa[2 * j] = pack16<E4M3>(p[0], p[1]);
-            pa[2 * j + 1] = pack16<E4M3>(p[2], p[3]);
+            pb[nq][0] = transpose8(pack16<E4M3>(p[0], p[1]));
+            pb[nq][1] = transpose8(pack16<E4M3>(p[2], p[3]));
           }
-          const int row = tg * 16 + (lane & 15);
-          uint32_t x[4];
+          uint32_t x[4], y[4];
           if constexpr (E4M3) {
+            const int row = mt * 16 + (lane & 15);
 #pragma unroll
             for (int j = 0; j < D / 32; ++j) {
               ldsm4_t(x, vs + F::at(row, 2 * j + (lane >> 4)));
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = __byte_perm(x[i], 0, 0x3120);
+              for (int i = 0; i < 2; ++i) {    // columns 2 g in the products' rows g, 2 g + 1 in g + 8
+                f16x4_of_e4m3(__byte_perm(x[2 * i], 0, 0x3120), y[0], y[1]);
+                f16x4_of_e4m3(__byte_perm(x[2 * i + 1], 0, 0x3120), y[2], y[3]);
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                mma<true>(o[4 * j + 2 * i], pa, f16x2_of_e4m3(x[2 * i]), f16x2_of_e4m3(x[2 * i + 1]));
-                mma<true>(o[4 * j + 2 * i + 1], pa, f16x2_of_e4m3(x[2 * i] >> 16), f16x2_of_e4m3(x[2 * i + 1] >> 16));
+                for (int nq = 0; nq < NQ; ++nq) mma<true>(o[2 * j + i][nq], y, pb[nq][0], pb[nq][1]);
               }
             }
           } else {
+            const int row = mt * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              ldsm4_t(x, vs + F::at(row, 2 * j + (lane >> 4)));
-              mma<false>(o[2 * j], pa, x[0], x[1]);
-              mma<false>(o[2 * j + 1], pa, x[2], x[3]);
+            for (int j = 0; j < kD; ++j) {
+              ldsm4_t(x, vs + F::at(row, 2 * j + half));
+#pragma unroll
+              for (int nq = 0; nq < NQ; ++nq) mma<false>(o[j][nq], x, pb[nq][0], pb[nq][1]);
             }
           }
         }
       } else {
-        // One position after another, in f32; the probabilities pass through the
-        // keys' place, -1 for a position that the row does not see.
-        float* const ps = reinterpret_cast<float*>(scratch);   // [16][kTok]
-        __syncwarp();
+        // One position after another, in f32; the probabilities of 8 rows at a time pass
+        // through the keys' place, -1 for a position that the row does not see.
+        float* const ps = reinterpret_cast<float*>(scratch);   // [8][kTok]
 #pragma unroll
-        for (int nt = 0; nt < kNT; ++nt)
+        for (int nq = 0; nq < NQ; ++nq) {
+          __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = nt * 8 + 2 * c + (i & 1), q = qpos[i >> 1];
-            const long long pos = static_cast<long long>(pos0) + tok;
-            const bool sees = (cur.there[nt / 4] >> (tok & 31) & 1) && pos <= q && pos > static_cast<long long>(q) - a.window;
-            const float p = ptx::ex2_approx(s[nt][i] - sub[i >> 1]);
-            if (sees) l[i >> 1] = E4M3 ? fmaf(p, inv[nt][i & 1], l[i >> 1]) : l[i >> 1] + p;
-            ps[(g + 8 * (i >> 1)) * kTok + tok] = sees ? p : -1.f;
-          }
-        __syncwarp();
-#pragma unroll 1
-        for (int tok = 0; tok < kTok; ++tok) {
-          const float p[2] = {ps[g * kTok + tok], ps[(g + 8) * kTok + tok]};
+          for (int mt = 0; mt < kM; ++mt)
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            float v[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int col = E4M3 ? 16 * (j >> 1) + 4 * c + 2 * i + (j & 1) : 8 * j + 2 * c + i;
-              if constexpr (E4M3) {
-                const uint32_t code = scratch[kHalf + F::at(tok, col >> 4) + (col & 15)];
-                v[i] = __low2float(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(code), __NV_E4M3)));
-              } else {
-                v[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
-                    scratch + kHalf + F::at(tok, col >> 3) + (col & 7) * 2));
-              }
+            for (int i = 0; i < 4; ++i) {
+              const bool there = sees(mt, nq, i);
+              const float p = ptx::ex2_approx(s[mt][nq][i] - (ref[nq][i & 1] == -INFINITY ? 0.f : ref[nq][i & 1]));
+              if (there) l[nq][i & 1] = E4M3 ? fmaf(p, inv[mt][i >> 1], l[nq][i & 1]) : l[nq][i & 1] + p;
+              ps[(2 * c + (i & 1)) * kTok + mt * 16 + g + 8 * (i >> 1)] = there ? p : -1.f;
             }
+          __syncwarp();
+#pragma unroll 1
+          for (int tok = 0; tok < kTok; ++tok) {
+            const float p[2] = {ps[2 * c * kTok + tok], ps[(2 * c + 1) * kTok + tok]};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!(p[i >> 1] < 0.f)) o[j][i] = fmaf(p[i >> 1], v[i & 1], o[j][i]);
+            for (int j = 0; j < kD; ++j) {
+              float v[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int col = 16 * j + (E4M3 ? 2 * g + i : g + 8 * i);
+                if constexpr (E4M3) {
+                  const uint32_t code = scratch[kHalf + F::at(tok, col >> 4) + (col & 15)];
+                  v[i] = __low2float(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(code), __NV_E4M3)));
+                } else {
+                  v[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(
+                      scratch + kHalf + F::at(tok, col >> 3) + (col & 7) * 2));
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (!(p[i & 1] < 0.f)) o[j][nq][i] = fmaf(p[i & 1], v[i >> 1], o[j][nq][i]);
+            }
           }
         }
         __syncwarp();
@@ -593,122 +668,131 @@ __global__ void __launch_bounds__(kWarps * 32, 1) few_rows_kernel(const __grid_c
 
     // ------------------------------------- the warps' sums, added in order
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      if (c == 0) {
-        s_ref[warp][g + 8 * i] = ref[i];
-        s_l[warp][g + 8 * i] = l[i];
+    for (int nq = 0; nq < NQ; ++nq)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int x = 4; x < 32; x *= 2) l[nq][i] += __shfl_xor_sync(0xffffffffu, l[nq][i], x);
+        if (g == 0) {
+          s_ref[warp][8 * nq + 2 * c + i] = ref[nq][i];
+          s_l[warp][8 * nq + 2 * c + i] = l[nq][i];
+        }
       }
-    }
+    const bool complete = k0 == 0 && w.end == w.nk;
     // (the slice just used: its place is loaded again by the next item's first step)
     const int used = slot == 0 ? kStages - 1 : slot - 1;
-    __syncwarp();
-    float4* const mine_o = reinterpret_cast<float4*>(ring + used * (2 * kHalf));
+    float4* const mine_o = reinterpret_cast<float4*>(ring + used * F::kStage);
+    // an item that begins here and does not end goes to the second place of this CTA
+    float* const part = reinterpret_cast<float*>(a.ws + header_bytes(gridDim.x)) +
+                        (2 * static_cast<size_t>(blockIdx.x) + (k0 == 0 ? 1 : 0)) * part_floats(D, NQ);
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) mine_o[j * 32 + lane] = make_float4(o[j][0], o[j][1], o[j][2], o[j][3]);
-    __syncthreads();
-    const bool complete = k0 == 0 && w.end == w.nk;
-    if (warp < D / 16) {
-      Sums m;
+    for (int round = 0; round < F::kRounds; ++round) {
+      __syncwarp();
 #pragma unroll
-      for (int v = 0; v < kWarps; ++v)
+      for (int n = 0; n < F::kQTiles; ++n)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) m.ref[i] = fmaxf(m.ref[i], s_ref[v][g + 8 * i]);
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) {
-        float f[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f[i] = ex2_from(s_ref[v][g + 8 * i], m.ref[i]);
-          m.l[i] = fmaf(s_l[v][g + 8 * i], f[i], m.l[i]);
+        for (int j = 0; j < kD; ++j) {
+          const float (&x)[4] = o[j][round * F::kQTiles + n];
+          mine_o[(n * kD + j) * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
         }
-        const float4* src = reinterpret_cast<const float4*>(smem + (v * kStages + used) * (2 * kHalf));
-        m.add(src[2 * warp * 32 + lane], src[(2 * warp + 1) * 32 + lane], f);
-      }
-      if (complete) {
-        store_rows<D, E4M3>(a, w.q, w.item, w.tiles, warp, lane, m);
-      } else {
-        // an item that begins here goes to the second place of this CTA
-        float* part = reinterpret_cast<float*>(a.ws + header_bytes(gridDim.x)) +
-                      static_cast<size_t>(2 * blockIdx.x + (k0 == 0 ? 1 : 0)) * kPartFloats<D>;
-        if (warp == 0 && c == 0) {
+      __syncthreads();
+#pragma unroll 1
+      for (int f4 = warp; f4 < F::kQTiles * kD; f4 += kWarps) {
+        const int n = f4 / kD, j = f4 % kD, row = 8 * (round * F::kQTiles + n) + 2 * c;
+        Sums m;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) m.ref[i] = fmaxf(m.ref[i], s_ref[v][row + i]);
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) {
+          float f[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            part[g + 8 * i] = m.ref[i];
-            part[kRowTile + g + 8 * i] = m.l[i];
+            f[i] = ex2_from(s_ref[v][row + i], m.ref[i]);
+            m.l[i] = fmaf(s_l[v][row + i], f[i], m.l[i]);
           }
+          m.add(reinterpret_cast<const float4*>(smem + (v * kStages + used) * F::kStage)[f4 * 32 + lane], f);
         }
-        float4* dst = reinterpret_cast<float4*>(part + 2 * kRowTile);
-        dst[2 * warp * 32 + lane] = make_float4(m.o[0], m.o[1], m.o[2], m.o[3]);
-        dst[(2 * warp + 1) * 32 + lane] = make_float4(m.o[4], m.o[5], m.o[6], m.o[7]);
-        if (k0 == 0 && threadIdx.x == 0) {
-          const long long last = at + w.nk;    // behind the item's last unit
-          headers[blockIdx.x] = Header{static_cast<int>((last * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1, w.b, w.item};
+        if (complete) {
+          store_rows<D, E4M3>(a, w.q, w.r, w.h, w.row0 + row - 2 * c, j, lane, m);
+        } else {
+          if (j == 0 && g == 0) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              part[row + i] = m.ref[i];
+              part[F::kRows + row + i] = m.l[i];
+            }
+          }
+          reinterpret_cast<float4*>(part + 2 * F::kRows)[(round * F::kQTiles * kD + f4) * 32 + lane] =
+              make_float4(m.o[0], m.o[1], m.o[2], m.o[3]);
         }
       }
+      __syncthreads();
+    }
+    if (!complete && k0 == 0 && threadIdx.x == 0) {
+      const long long last = at + w.nk;        // behind the item's last unit
+      headers[blockIdx.x] = Header{static_cast<int>((last * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1, w.b, w.item};
     }
     at += w.end - k0;
-    __syncthreads();
-  } while (w.next_item<kUnit>(a));
+  } while (w.next_item(a));
   cp_async_wait<0>();
 }
 
 // Adds the parts of the item that CTA blockIdx.x of few_rows_kernel began last
-// and did not finish, in the CTAs' order.
-template <int D, bool E4M3>
+// and did not finish, in the CTAs' order; blockIdx.y counts tiles of 8 rows.
+template <int D, bool E4M3, int NQ>
 __global__ void __launch_bounds__(D * 2) combine_kernel(const __grid_constant__ PagedArgs a) {
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
   const Header hd = reinterpret_cast<const Header*>(a.ws)[blockIdx.x];
   if (hd.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 8 * blockIdx.y + 2 * (lane & 3);
   const float* parts = reinterpret_cast<const float*>(a.ws + header_bytes(gridDim.x));
-  auto part = [&](int i) {
-    return parts + static_cast<size_t>(2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * kPartFloats<D>;
-  };
+  auto part = [&](int i) { return parts + (2 * static_cast<size_t>(blockIdx.x + i) + (i == 0 ? 1 : 0)) * part_floats(D, NQ); };
   Sums m;
   for (int v = 0; v < hd.parts; ++v)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) m.ref[i] = fmaxf(m.ref[i], part(v)[g + 8 * i]);
+    for (int i = 0; i < 2; ++i) m.ref[i] = fmaxf(m.ref[i], part(v)[row + i]);
+#pragma unroll 4
   for (int v = 0; v < hd.parts; ++v) {
     float f[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f[i] = ex2_from(part(v)[g + 8 * i], m.ref[i]);
-      m.l[i] = fmaf(part(v)[kRowTile + g + 8 * i], f[i], m.l[i]);
+      f[i] = ex2_from(part(v)[row + i], m.ref[i]);
+      m.l[i] = fmaf(part(v)[8 * NQ + row + i], f[i], m.l[i]);
     }
-    const float4* src = reinterpret_cast<const float4*>(part(v) + 2 * kRowTile);
-    m.add(src[2 * warp * 32 + lane], src[(2 * warp + 1) * 32 + lane], f);
+    m.add(reinterpret_cast<const float4*>(part(v) + 16 * NQ)[(blockIdx.y * (D / 16) + warp) * 32 + lane], f);
   }
   const Seq q = load_seq(a.step, hd.b);
-  const int tiles = static_cast<int>((static_cast<long long>(q.n) * a.G + kRowTile - 1) / kRowTile);
-  store_rows<D, E4M3>(a, q, hd.item, tiles, warp, lane, m);
+  const int tiles = (q.n * a.G + 8 * NQ - 1) / (8 * NQ), rh = hd.item / tiles;
+  store_rows<D, E4M3>(a, q, rh / a.pool.H, rh % a.pool.H, (hd.item - rh * tiles) * 8 * NQ + 8 * blockIdx.y, warp, lane, m);
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, int NQ>
 cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t st) {
-  constexpr int kSmem = kWarps * kStages * 2 * kHalf;
+  using F = Few<D, E4M3, NQ>;
   static bool attr_set[64] = {};
-  cudaError_t e = smem_attr_once(attr_set, few_rows_kernel<D, E4M3>, kSmem);
+  cudaError_t e = smem_attr_once(attr_set, few_rows_kernel<D, E4M3, NQ>, F::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(ctas));
-  if ((e = launch_pdl(few_rows_kernel<D, E4M3>, grid, dim3(kWarps * 32), kSmem, st, 1u, a)) != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D, E4M3>, grid, dim3(D * 2), 0, st, 1u, a);
+  const unsigned grid = static_cast<unsigned>(ctas);
+  if ((e = launch_pdl(few_rows_kernel<D, E4M3, NQ>, dim3(grid), dim3(F::kWarps * 32), F::kSmem, st, 1u, a)) != cudaSuccess)
+    return e;
+  return launch_pdl(combine_kernel<D, E4M3, NQ>, dim3(grid, NQ), dim3(D * 2), 0, st, 1u, a);
 }
 
-size_t few_rows_ws_bytes(int64_t d, int ctas) {
-  const size_t part = (2 * kRowTile + kRowTile * static_cast<size_t>(d)) * sizeof(float);
-  return header_bytes(ctas) + 2 * static_cast<size_t>(ctas) * part;
+template <int NQ>
+cudaError_t launch_few(const PagedArgs& a, bool e4m3, int ctas, cudaStream_t st) {
+  return a.pool.d == 128 ? (e4m3 ? launch_few<128, true, NQ>(a, ctas, st) : launch_few<128, false, NQ>(a, ctas, st))
+                         : (e4m3 ? launch_few<64, true, NQ>(a, ctas, st) : launch_few<64, false, NQ>(a, ctas, st));
 }
 
-// Up to 16 rows to a sequence and key/value head on average: the tensor cores'
-// tiles of 128 rows would be mostly empty, and their latency is what a short
-// item waits for.
-bool few_rows(int64_t T, int B, int G) { return T * G <= static_cast<int64_t>(kRowTile) * B; }
-
-size_t paged_ws_bytes(int64_t T, int B, int G, int64_t d, int ctas) {
-  return few_rows(T, B, G) ? few_rows_ws_bytes(d, ctas) : tiles_ws_bytes(d, B, ctas);
+// The form for a step: NQ tiles of 8 rows to an item, or 0 for tiles of 128 rows on
+// the tensor cores' own memory.  By the rows to a sequence and key/value head on
+// average, which is all that the host knows; every form takes every step.
+int form_of(int64_t T, int B, int G) {
+  const int64_t rows = T * G;
+  return rows <= 8 * static_cast<int64_t>(B) ? 1 : rows <= 16 * static_cast<int64_t>(B) ? 2 : 0;
 }
 
 int usable_sms(const fcc_opts* o) {
@@ -719,6 +803,14 @@ int usable_sms(const fcc_opts* o) {
     sms = 256;  // (no device: sizes for the largest grid)
   }
   return o != nullptr && o->max_ctas > 0 ? std::min(sms, o->max_ctas) : sms;
+}
+
+// CTAs of a form's kernel: two to an SM, or one of tiles_kernel's.
+int ctas_of(int form, const fcc_opts* o) { return usable_sms(o) * (form != 0 ? 2 : 1); }
+
+size_t paged_ws_bytes(int form, int B, int64_t d, int ctas) {
+  return form != 0 ? header_bytes(ctas) + 2 * static_cast<size_t>(ctas) * part_floats(static_cast<int>(d), form) * sizeof(float)
+                   : tiles_ws_bytes(d, B, ctas);
 }
 
 }  // namespace
@@ -733,7 +825,8 @@ size_t fcc_paged_attention_workspace_size(int R, int64_t T, int B, int Hq, int H
   if (R < 1 || R > FCC_MAX_RANKS || T < 1 || B < 1 || H < 1 || Hq < H || Hq % H != 0 ||
       (d != 64 && d != 128))
     return 0;
-  return paged_ws_bytes(T, B, Hq / H, d, usable_sms(opts));
+  const int form = form_of(T, B, Hq / H);
+  return paged_ws_bytes(form, B, d, ctas_of(form, opts));
 }
 
 fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const fcc_cache* cache,
@@ -764,10 +857,10 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   if (in != FCC_BF16 || out != FCC_BF16) return FCC_ERR_UNSUPPORTED;
   if (opts != nullptr && opts->algo != FCC_ALGO_AUTO && opts->algo != FCC_ALGO_FUSED)
     return FCC_ERR_UNSUPPORTED;
-  // rows (tokens times a group's heads) and tiles of 16 of them are counted in 32 bits
+  // rows (tokens times a group's heads) and tiles of 8 of them are counted in 32 bits
   const int64_t rows = batch->T * (Hq / cache->H);
   if (rows > INT_MAX - 256 ||
-      static_cast<int64_t>(R) * cache->H * (rows / kRowTile + batch->B) > INT_MAX)
+      static_cast<int64_t>(R) * cache->H * (rows / 8 + batch->B) > INT_MAX)
     return FCC_ERR_INVALID;
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (opts == nullptr || opts->workspace == nullptr) {
@@ -775,12 +868,12 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
     if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return FCC_ERR_CUDA;
     if (capture != cudaStreamCaptureStatusNone) return FCC_ERR_WORKSPACE;
   }
-  const int ctas = usable_sms(opts);
   a.G = Hq / cache->H;
+  const int form = form_of(batch->T, batch->B, a.G), ctas = ctas_of(form, opts);
   void* ws = nullptr;
   int sms = 0;
   unsigned long long timeout_ns = 0;
-  const fcc_status s = internal_prepare(opts, paged_ws_bytes(batch->T, batch->B, a.G, cache->d, ctas), &ws,
+  const fcc_status s = internal_prepare(opts, paged_ws_bytes(form, batch->B, cache->d, ctas), &ws,
                                         &a.status, &sms, &timeout_ns);
   if (s != FCC_OK) return s;
   for (int r = 0; r < R; ++r) {
@@ -799,13 +892,11 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
                                     1.4426950408889634);
   a.ws = static_cast<char*>(ws);
   const bool e4m3 = cache->dtype == FCC_E4M3;
-  const bool few = few_rows(batch->T, batch->B, a.G);
-  const cudaError_t e =
-      !few ? launch_tiles(a, e4m3, ctas, timeout_ns, st)
-      : cache->d == 128 ? (e4m3 ? launch_few<128, true>(a, ctas, st) : launch_few<128, false>(a, ctas, st))
-                        : (e4m3 ? launch_few<64, true>(a, ctas, st) : launch_few<64, false>(a, ctas, st));
+  const cudaError_t e = form == 1   ? launch_few<1>(a, e4m3, ctas, st)
+                        : form == 2 ? launch_few<2>(a, e4m3, ctas, st)
+                                    : launch_tiles(a, e4m3, ctas, timeout_ns, st);
   if (e != cudaSuccess) return FCC_ERR_CUDA;
-  bump_launch_count(few ? 2 : 3);
+  bump_launch_count(form != 0 ? 2 : 3);
   return FCC_OK;
 }
 
