@@ -750,19 +750,42 @@ __global__ void __launch_bounds__(D * 2) combine_kernel(const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 8 * blockIdx.y + 2 * (lane & 3);
   const float* parts = reinterpret_cast<const float*>(a.ws + header_bytes(gridDim.x));
   auto part = [&](int i) { return parts + (2 * static_cast<size_t>(blockIdx.x + i) + (i == 0 ? 1 : 0)) * part_floats(D, NQ); };
+  // (four parts' loads at a time: a long item's parts are a chain of them otherwise)
+  constexpr int kAtOnce = 4;
   Sums m;
-  for (int v = 0; v < hd.parts; ++v)
+  for (int v0 = 0; v0 < hd.parts; v0 += kAtOnce) {
+    float2 ref[kAtOnce], l[kAtOnce];
+    float4 x[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) m.ref[i] = fmaxf(m.ref[i], part(v)[row + i]);
-#pragma unroll 4
-  for (int v = 0; v < hd.parts; ++v) {
-    float f[2];
+    for (int v = 0; v < kAtOnce; ++v) {
+      const float* p = part(min(v0 + v, hd.parts - 1));
+      ref[v] = *reinterpret_cast<const float2*>(p + row);
+      l[v] = *reinterpret_cast<const float2*>(p + 8 * NQ + row);
+      x[v] = reinterpret_cast<const float4*>(p + 16 * NQ)[(blockIdx.y * (D / 16) + warp) * 32 + lane];
+    }
+    float top[2] = {m.ref[0], m.ref[1]}, f[2];
+#pragma unroll
+    for (int v = 0; v < kAtOnce; ++v) {
+      top[0] = fmaxf(top[0], ref[v].x);
+      top[1] = fmaxf(top[1], ref[v].y);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f[i] = ex2_from(part(v)[row + i], m.ref[i]);
-      m.l[i] = fmaf(part(v)[8 * NQ + row + i], f[i], m.l[i]);
+      f[i] = ex2_from(m.ref[i], top[i]);
+      m.ref[i] = top[i];
+      m.l[i] *= f[i];
+      m.o[i] *= f[i];
+      m.o[2 + i] *= f[i];
     }
-    m.add(reinterpret_cast<const float4*>(part(v) + 16 * NQ)[(blockIdx.y * (D / 16) + warp) * 32 + lane], f);
+#pragma unroll
+    for (int v = 0; v < kAtOnce; ++v) {
+      if (v0 + v >= hd.parts) break;
+      f[0] = ex2_from(ref[v].x, top[0]);
+      f[1] = ex2_from(ref[v].y, top[1]);
+      m.l[0] = fmaf(l[v].x, f[0], m.l[0]);
+      m.l[1] = fmaf(l[v].y, f[1], m.l[1]);
+      m.add(x[v], f);
+    }
   }
   const Seq q = load_seq(a.step, hd.b);
   const int tiles = (q.n * a.G + 8 * NQ - 1) / (8 * NQ), rh = hd.item / tiles;
