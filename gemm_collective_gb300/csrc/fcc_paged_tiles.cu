@@ -19,7 +19,8 @@
 // loaded, and its first S computed, before the old one's O has been stored.
 //
 // Warps: 0-3 and 4-7 softmax and output of tiles A and B (a thread owns a row and
-// its 128 columns), 8-11 load keys and values, 12 issues the products.  The
+// its 128 columns), then those that load keys and values and the one that issues the
+// products.  The
 // loaders look up every position's page for itself (any page size), bf16 rows go
 // by TMA into the swizzled tile, 32 positions to a warp.  e4m3 rows pass through registers and become
 // f16 there, times their powers of two relative to the largest, 2^A of the keys and
@@ -55,15 +56,18 @@ constexpr float kRaise = E4M3 ? 8.f : 32.f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;                // S_t at 128 t, O_t at 256 + 128 t
 constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;
-constexpr int kThreads = 512;                  // 16 warps: 8 softmax, 4 loading, 1 issuing, 3 idle
-// Registers: the launch's 512 x 128 are dealt out anew, to 256 softmax threads, 128
-// loading ones (which hold an e4m3 block's pieces in flight) and the issuing warp's
-// 128.  Next to nothing may spill: what shared memory leaves of the L1 is too small to
-// hold it (200 bytes a thread made a 2048-row prompt three times as slow).
+// Warps: 8 softmax, 4 loading (e4m3: 4 for the keys and 4 for the values), 1 issuing and
+// its 3 idle neighbours.  Registers: the launch's are dealt out anew.  Next to nothing
+// may spill: what shared memory leaves of the L1 is too small to hold it (200 bytes a
+// thread made a 2048-row prompt three times as slow).
 template <bool E4M3>
-struct Regs {
-  static constexpr int kSoftmax = E4M3 ? 144 : 176, kLoad = E4M3 ? 128 : 80, kIssue = E4M3 ? 96 : 80;
-  static_assert(256 * kSoftmax + 128 * kLoad + 128 * kIssue <= kThreads * 128);
+struct Roles {
+  static constexpr int kLoadWarps = E4M3 ? 8 : 4;
+  static constexpr int kIssuer = 8 + kLoadWarps;         // the issuing warp
+  static constexpr int kThreads = (kIssuer + 4) * 32;
+  static constexpr int kLaunch = E4M3 ? 96 : 128;
+  static constexpr int kSoftmax = E4M3 ? 112 : 176, kLoad = E4M3 ? 96 : 80, kIssue = E4M3 ? 64 : 80;
+  static_assert(kThreads * kLaunch <= 65536 && 256 * kSoftmax + 32 * kLoadWarps * kLoad + 128 * kIssue <= kThreads * kLaunch);
 };
 constexpr int kMaxCtas = 512;
 
@@ -321,14 +325,14 @@ struct alignas(16) WarpWalk {
     __syncwarp();
   }
 };
-constexpr int kWalks = 13;
+constexpr int kWalks = 17;
 
 // What the softmax warps need to know of a block's columns, for each 32 of them: e4m3
 // the largest powers of two of their keys and values; which positions the pages hold.
 struct alignas(16) Columns {
   float ka[4], vb[4], vi[4];                   // 2^A, B and 2^-B
   uint32_t there[4];
-  uint32_t wide[4];                            // powers too far apart for f16, see f16_power()
+  uint32_t wide[2][4];                         // keys', values' powers too far apart for f16, see f16_power()
 };
 
 // 2^(byte - top) in f16 (both halves), 0 below what f16 holds.  An e4m3 code times it
@@ -359,13 +363,13 @@ constexpr int kSmem = 1024 + (2 + kSlots) * static_cast<int>(kTileBytes<D>) + kC
                       static_cast<int>(sizeof(Run)) + kBars * 8 + 16;
 static_assert(kSmem<128> <= 232448, "shared memory per CTA");
 
-// A descriptor's address field counts 16 bytes: the K steps of 16 are added to the
-// operand's own descriptor.
-__device__ __forceinline__ uint64_t desc_of(const uint8_t* tile, uint32_t lbo) {
-  uint64_t d = ptx::smem_desc_sw128(ptx::smem_addr(tile), lbo, 1024);
-  asm volatile("" : "+l"(d));                  // (the steps are added where they are used, not kept)
-  return d;
+// The low words of the operands' descriptors (address and leading offset, in 16 bytes;
+// the K steps of 16 are added there) and the high word that all share: 1024 bytes
+// between groups of 8 rows, 128-byte swizzle.
+__device__ __forceinline__ uint32_t desc_low(const uint8_t* tile, uint32_t lbo) {
+  return static_cast<uint32_t>(ptx::smem_desc_sw128(ptx::smem_addr(tile), lbo, 1024));
 }
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 __host__ __device__ constexpr uint32_t step_kmajor(int kk) { return ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4; }
 __host__ __device__ constexpr uint32_t step_mnmajor(int kk) { return (kk * 2048) >> 4; }
 // The byte of 16-byte chunk `chunk` (8 values) of a tile's row.
@@ -459,8 +463,9 @@ struct PoolMaps {                              // bf16 pools with pages of 16 ro
 };
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PoolMaps maps, unsigned long long timeout_ns) {
+__global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const __grid_constant__ PagedArgs a, const __grid_constant__ PoolMaps maps, unsigned long long timeout_ns) {
   constexpr uint32_t kTile = kTileBytes<D>;
+  constexpr int kIssuer = Roles<E4M3>::kIssuer;
   constexpr uint32_t kFormat = E4M3 ? 0u : (1u << 7) | (1u << 10);   // f16 or bf16 operands
   constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
   constexpr uint32_t kIdescS = (ptx::idesc_bf16_f32(kTileRows, kBlock, false, false) & ~kBf16) | kFormat;
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   Run* run = reinterpret_cast<Run*>(stages + 8 * 32 * kStageRow);
   uint64_t* r_full = reinterpret_cast<uint64_t*>(run + 1);  // [kSlots], four loading warps
   uint64_t* r_empty = r_full + kSlots;         // [kSlots]
-  uint64_t* c_full = r_empty + kSlots;         // [kCols], four loading warps
+  uint64_t* c_full = r_empty + kSlots;         // [kCols], the loading warps
   uint64_t* q_full = c_full + kCols;           // [2]: Q_t written, the tile's four softmax warps
   uint64_t* s_full = q_full + 2;               // [2]: S_t complete
   uint64_t* p_full = s_full + 2;               // [2]: P_t written (and O_t rescaled)
@@ -492,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       ptx::mbar_init(&r_full[i], 4);
       ptx::mbar_init(&r_empty[i], 1);
     }
-    for (int i = 0; i < kCols; ++i) ptx::mbar_init(&c_full[i], 4);
+    for (int i = 0; i < kCols; ++i) ptx::mbar_init(&c_full[i], Roles<E4M3>::kLoadWarps);
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(&q_full[t], 4);
       ptx::mbar_init(&s_full[t], 1);
@@ -503,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 12) {
+  if (warp == kIssuer) {
     ptx::tmem_alloc(tmem_slot, kTmemCols);
     ptx::tmem_relinquish();
   }
@@ -533,36 +538,36 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     return __all_sync(0xffffffffu, W.wait(bar, parity) ? 1 : 0) != 0;
   };
 
-  if (warp >= 12) {
+  if (warp >= kIssuer) {
     // ----------------------------------------------------------- MMA issue
-    regs_dec<Regs<E4M3>::kIssue>();
-    if (warp == 12 && lane == 0) {
+    regs_dec<Roles<E4M3>::kIssue>();
+    if (warp == kIssuer && lane == 0) {
       // (what the loop over blocks needs is in registers: this thread's own instructions
       // stand between one product and the next)
-      Walk& w = walks[12].now;
+      Walk& w = walks[kIssuer].now;
       bool any = false, ok = true;
       bool more = w.begin(a, *run);
       uint32_t q_phase = 0, p_phase = 0;       // bit t: the parity that Q_t / P_t will complete
       uint32_t u = 0;                          // ring position of the block's K, V is at u + 1
-      const uint64_t qd0 = desc_of(sQ, 16), kd0 = desc_of(sR, 16), vd0 = desc_of(sR, kAtom);
+      const uint32_t qd0 = desc_low(sQ, 16), kd0 = desc_low(sR, 16), vd0 = desc_low(sR, kAtom);
       // O_t += P_t V, the V at ring position `pos`.
       auto issue_pv = [&](int t, uint32_t pos, bool first) -> bool {
-        const uint64_t vd = vd0 + (pos % kSlots) * (kTile >> 4);
+        const uint32_t vd = vd0 + (pos % kSlots) * (kTile >> 4);
         const uint32_t pa = tmem_base + t * 128, o = tmem_base + kColO + t * 128;
         // (P as a whole: its halves as they come, on a barrier each, were 4 to 13 % slower)
         if (!W.wait(&p_full[t], p_phase >> t & 1u)) return false;
         ptx::tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kBlock / 16; ++kk)
-          ptx::mma_f16_tmem_a(o, pa + kk * 8, vd + step_mnmajor(kk), kIdescO, (!first || kk > 0) ? 1u : 0u);
+          ptx::mma_f16_tmem_a_words(o, pa + kk * 8, vd + step_mnmajor(kk), kDescHigh, kIdescO, (!first || kk > 0) ? 1u : 0u);
         p_phase ^= 1u << t;
         return true;
       };
       auto issue_s = [&](int t) {
-        const uint64_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (u % kSlots) * (kTile >> 4);
+        const uint32_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (u % kSlots) * (kTile >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_f16(tmem_base + t * 128, qd + step_kmajor(kk), kd + step_kmajor(kk), kIdescS, kk > 0 ? 1u : 0u);
+          ptx::mma_f16_words(tmem_base + t * 128, qd + step_kmajor(kk), kd + step_kmajor(kk), kDescHigh, kIdescS, kk > 0 ? 1u : 0u);
         ptx::mma_commit(&s_full[t]);
       };
       while (more && ok) {
@@ -596,12 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------- loading
-    // Warp 8 + i brings positions 32 i .. 32 i + 31 of each block.  A lane looks up
-    // one of them, a block ahead.
-    regs_dec<Regs<E4M3>::kLoad>();
-    const int wl = warp - 8;
+    // Warp 8 + i brings positions 32 i .. 32 i + 31 of each block (e4m3: their keys,
+    // warp 12 + i their values).  A lane looks up one of them, a block ahead.
+    regs_dec<Roles<E4M3>::kLoad>();
+    const int wl = (warp - 8) & 3, kind = (warp - 8) >> 2;   // kind 1: e4m3 values
     constexpr int kRow = D * (E4M3 ? 1 : 2), kLanes = kRow / 16, kAtOnce = 32 / kLanes, kN = 32 / kAtOnce;
-    const int chunk = lane % kLanes;
     if (run->busy) {
       WarpWalk& ww = walks[warp];
       Walk& w = ww.now;
@@ -641,89 +645,84 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
       auto wait_slot = [&]() -> bool { return wait_warp(&r_empty[u % kSlots], ((u / kSlots) & 1u) ^ 1u); };
       // (called once the block's key slot is free: the products of the block that had
       // these constants four blocks ago were issued before the slot was handed back)
-      uint32_t fk = 0, fv = 0;                 // e4m3: this lane's position's factors
-      auto constants = [&](int64_t row, int ke, int ve) {
+      // What the softmax warps are told of the block (called once the block's slot is
+      // free: the products of the block that had these constants four blocks ago were
+      // issued before the slot was handed back).  e4m3: returns this position's factor.
+      auto constants = [&](int64_t row, int byte) -> uint32_t {
         Columns& cc = cols[blk % kCols];
-        const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
+        uint32_t factor = 0;
         if constexpr (E4M3) {
-          ke = min(ke, 254);
-          ve = min(ve, 254);
-          const int A = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? ke : 1));
-          const int B = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? ve : 1));
-          const bool wide = __any_sync(0xffffffffu, row >= 0 && (too_wide(ke, A) || too_wide(ve, B)));
-          fk = f16_power(ke, A);
-          fv = f16_power(ve, B);
+          byte = min(byte, 254);
+          const int top = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 1));
+          const bool wide = __any_sync(0xffffffffu, row >= 0 && too_wide(byte, top));
+          factor = f16_power(byte, top);
           if (lane == 0) {
-            cc.ka[wl] = __int_as_float(A << 23);
-            cc.vb[wl] = static_cast<float>(B - 127);
-            cc.vi[wl] = __int_as_float((254 - B) << 23);
-            cc.wide[wl] = wide;
+            cc.wide[kind][wl] = wide;
+            if (kind == 0) {
+              cc.ka[wl] = __int_as_float(top << 23);
+            } else {
+              cc.vb[wl] = static_cast<float>(top - 127);
+              cc.vi[wl] = __int_as_float((254 - top) << 23);
+            }
           }
         }
+        const uint32_t there = __ballot_sync(0xffffffffu, row >= 0);
         if (lane == 0) {
-          cc.there[wl] = there;
+          if (kind == 0) cc.there[wl] = there;
           ptx::mbar_arrive(&c_full[blk % kCols]);
         }
         ++blk;
+        return factor;
       };
       look_up();
       if constexpr (E4M3) {
-        // A block's keys are fetched into registers while the block before's values
-        // are converted, and the other way round.
-        uint4 xk[kN], xv[kN];
-        auto fetch = [&](uint4 (&x)[kN], const char* pool, int64_t row) {
+        // Eight lanes hold four 16-byte pieces of one 64-column atom of two rows next to
+        // each other: their f16 stores fall into different banks.
+        constexpr int kAtoms = D / 64;
+        const int piece = (lane >> 3) % kAtoms * 4 + (lane & 3);
+        const int sub = (lane >> 3) / kAtoms * 2 + (lane >> 2 & 1);  // row of the kAtOnce
+        uint4 x[kN];
+        int byte = 1;
+        u = kind;
+        auto fetch = [&](int64_t row) {
+          const char* pool = (kind == 0 ? a.pool.K[r] : a.pool.V[r]) + piece * 16;
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
-            const int64_t src = __shfl_sync(0xffffffffu, row, i * kAtOnce + lane / kLanes);
+            const int64_t src = __shfl_sync(0xffffffffu, row, i * kAtOnce + sub);
             x[i] = make_uint4(0, 0, 0, 0);
-            if (src >= 0) x[i] = *reinterpret_cast<const uint4*>(pool + src * kRow + chunk * 16);
+            if (src >= 0) x[i] = *reinterpret_cast<const uint4*>(pool + src * kRow);
           }
+          if (row >= 0) byte = (kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r])[row];
         };
-        auto convert = [&](const uint4 (&x)[kN], uint32_t power) {
+        int64_t row = row_of();
+        bool full = have;
+        if (full) fetch(row);
+        while (full) {
+          look_up();                           // the next block
+          if (!(ok = wait_slot())) break;
+          const uint32_t power = constants(row, byte);
           uint8_t* dst = sR + (u % kSlots) * kTile;
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
-            const int tok = 32 * wl + i * kAtOnce + lane / kLanes;
-            const uint32_t f = __shfl_sync(0xffffffffu, power, tok & 31);
-            auto f16 = [&](uint32_t codes) { return mul_f16x2(f16x2_of_e4m3(codes), f); };
-            *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk)) =
-                make_uint4(f16(x[i].x), f16(x[i].x >> 16), f16(x[i].y), f16(x[i].y >> 16));
-            *reinterpret_cast<uint4*>(dst + tile_at(tok, 2 * chunk + 1)) =
-                make_uint4(f16(x[i].z), f16(x[i].z >> 16), f16(x[i].w), f16(x[i].w >> 16));
+            const int tok = i * kAtOnce + sub;
+            const uint32_t f = __shfl_sync(0xffffffffu, power, tok);
+            uint32_t y[8];
+            f16x4_of_e4m3(x[i].x, y[0], y[1]);
+            f16x4_of_e4m3(x[i].y, y[2], y[3]);
+            f16x4_of_e4m3(x[i].z, y[4], y[5]);
+            f16x4_of_e4m3(x[i].w, y[6], y[7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = mul_f16x2(y[e], f);
+            *reinterpret_cast<uint4*>(dst + tile_at(32 * wl + tok, 2 * piece)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + tile_at(32 * wl + tok, 2 * piece + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
           }
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&r_full[u % kSlots]);
-          ++u;
-        };
-        int64_t row = row_of();
-        int ke = 1, ve = 1;
-        auto fetch_exps = [&]() {
-          if (row >= 0) {
-            ke = a.pool.Ke[r][row];
-            ve = a.pool.Ve[r][row];
-          }
-        };
-        bool full = have;
-        if (full) {
-          fetch(xk, a.pool.K[r], row);
-          fetch(xv, a.pool.V[r], row);
-          fetch_exps();
-        }
-        while (full) {
-          look_up();                           // the next block
-          if (!(ok = wait_slot())) break;
-          constants(row, ke, ve);
-          convert(xk, fk);
+          u += 2;
           row = row_of();
-          if (have) {
-            fetch(xk, a.pool.K[r], row);
-            fetch_exps();
-          }
-          if (!(ok = wait_slot())) break;
-          convert(xv, fv);
-          if (have) fetch(xv, a.pool.V[r], row);
           full = have;
+          if (full) fetch(row);
         }
       } else {
         // A warp's 32 positions come by TMA, a box of a page's rows and 64 columns at a
@@ -738,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++u) {
             if (!(ok = wait_slot())) break;
-            if (kv == 0) constants(row, 0, 0);
+            if (kv == 0) constants(row, 0);
             uint8_t* dst = sR + (u % kSlots) * kTile;
             uint64_t* bar = &r_full[u % kSlots];
             if (boxes) {
@@ -752,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
               }
             } else {
               const char* pool = kv == 0 ? a.pool.K[rr] : a.pool.V[rr];
+              const int chunk = lane % kLanes;
 #pragma unroll 4
               for (int i = 0; i < kN; ++i) {
                 const int tok = i * kAtOnce + lane / kLanes;
@@ -774,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------- softmax and output
-    regs_inc<Regs<E4M3>::kSoftmax>();
+    regs_inc<Roles<E4M3>::kSoftmax>();
     const int t = warp >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;       // of the tile
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -937,25 +937,35 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
         };
         // (rolled loops: thirteen warps in five roles share the instruction caches, and
         // what they do not hold costs more than the branches)
-        uint32_t x[2][32];
-        ptx::tmem_ld_32x32b_x32(s_addr, x[0]);
-        tmem_ld_wait_regs(x[0]);
+        if constexpr (E4M3) {                  // (its softmax threads have fewer registers)
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          ptx::tmem_ld_32x32b_x32(s_addr + 64 * half + 32, x[1]);
-          exponentials(x[0], 2 * half);
-          tmem_ld_wait_regs(x[1]);
-          if (half == 0) ptx::tmem_ld_32x32b_x32(s_addr + 64, x[0]);
-          exponentials(x[1], 2 * half + 1);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t x[32];
+            ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, x);
+            tmem_ld_wait_regs(x);
+            exponentials(x, k);
+          }
+        } else {
+          uint32_t x[2][32];
+          ptx::tmem_ld_32x32b_x32(s_addr, x[0]);
           tmem_ld_wait_regs(x[0]);
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            ptx::tmem_ld_32x32b_x32(s_addr + 64 * half + 32, x[1]);
+            exponentials(x[0], 2 * half);
+            tmem_ld_wait_regs(x[1]);
+            if (half == 0) ptx::tmem_ld_32x32b_x32(s_addr + 64, x[0]);
+            exponentials(x[1], 2 * half + 1);
+            tmem_ld_wait_regs(x[0]);
+          }
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&p_full[t]);
         if constexpr (E4M3) {
-          const uint4 w4 = *reinterpret_cast<const uint4*>(cc.wide);
-          wide |= w4.x | w4.y | w4.z | w4.w;
+          const uint4 wk = *reinterpret_cast<const uint4*>(cc.wide[0]), wv = *reinterpret_cast<const uint4*>(cc.wide[1]);
+          wide |= wk.x | wk.y | wk.z | wk.w | wv.x | wv.y | wv.z | wv.w;
         }
         ++n;
       }
@@ -1077,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1) tiles_kernel(const __grid_constan
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kIssuer) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, kTmemCols);
   }
@@ -1141,7 +1151,7 @@ cudaError_t launch(PagedArgs a, int ctas, unsigned long long timeout_ns, cudaStr
   if (e != cudaSuccess) return e;
   if ((e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, 1u, a, ctas)) != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if ((e = launch_pdl(tiles_kernel<D, E4M3>, dim3(grid), dim3(kThreads), kSmem<D>, st, 1u, a, maps, timeout_ns)) != cudaSuccess) return e;
+  if ((e = launch_pdl(tiles_kernel<D, E4M3>, dim3(grid), dim3(Roles<E4M3>::kThreads), kSmem<D>, st, 1u, a, maps, timeout_ns)) != cudaSuccess) return e;
   return launch_pdl(join_kernel<D>, dim3(grid, D / 16), dim3(kPairRows), 0, st, 1u, a);
 }
 
