@@ -79,6 +79,7 @@ struct Few {
   // a warp's values pass through the place of its last slice, a part of the rows at a time
   static constexpr int kRounds = NQ * 8 * D * 4 > 2 * kHalf ? NQ * 8 * D * 4 / (2 * kHalf) : 1;
   static constexpr int kQTiles = NQ / kRounds;           // tiles of 8 rows in a round
+  static_assert(kQTiles * kRounds == NQ && kQTiles * 8 * D * 4 <= 2 * kHalf, "a round's values fit a slice's place");
   // 16-byte chunks are permuted so that eight rows' chunks of one number lie in
   // eight different groups of banks
   static __device__ __forceinline__ uint32_t at(int row, int chunk) {

@@ -79,18 +79,17 @@ struct Header {                                // of the item that a CTA begins 
   int parts, b, rh, pair;
 };
 
-// Workspace: the plan's totals, the runs' starts, the headers, the sequences'
-// blocks, then two partial results for each CTA.
+// Workspace: the plan's totals, the headers, the cost of what is before each sequence,
+// then two partial results for each CTA.
 struct Layout {
-  size_t starts, headers, units, parts, part_bytes, total;
+  size_t headers, units, parts, part_bytes, total;
 };
 // References, sums, then [D / 4][256] float4.
 template <int D>
 constexpr size_t kPartBytes = kPairRows * static_cast<size_t>(D + 2) * 4;
 __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   Layout l;
-  l.starts = 256;
-  l.headers = l.starts + (static_cast<size_t>(ctas) + 1) * sizeof(Start);
+  l.headers = 256;
   l.units = l.headers + static_cast<size_t>(ctas) * sizeof(Header);
   l.parts = (l.units + static_cast<size_t>(B) * 8 + 255) & ~size_t{255};
   l.part_bytes = kPairRows * static_cast<size_t>(d + 2) * 4;
@@ -98,6 +97,7 @@ __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   return l;
 }
 struct Totals {                                // at the workspace's start
+  long long cost;                              // of all items
   int ctas;                                    // with work
 };
 
@@ -126,7 +126,12 @@ __device__ __forceinline__ Range pair_blocks(const PagedArgs& a, const Seq& q, i
 constexpr int kPlanThreads = 1024;
 constexpr int kFewPairs = 8;                   // up to here a thread counts a sequence's blocks alone
 
-// Counts the blocks of all items and finds where each CTA's run begins.
+// Division by 32-bit means where they will do: 64-bit ones are long.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+
+// Adds up what all items cost, in blocks.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PagedArgs a, int grid) {
   __shared__ long long s_scan[32];
   ptx::griddep_wait();
@@ -184,65 +189,65 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     total += s_scan[i];
   }
   const long long ctas = min(static_cast<long long>(grid), total);
-  // (from here on units[b] is the sum of the blocks before sequence b)
+  // (from here on units[b] is the cost of what is before sequence b)
   for (int b = b_first; b < b_last; ++b) {
     const long long n = units[b];
     units[b] = from;
     from += n;
   }
-  __syncthreads();
-  Start* starts = reinterpret_cast<Start*>(a.ws + lay.starts);
-  for (int c = warp; c < ctas; c += 32) {
-    const long long u = c * total / ctas;
-    // the last sequence whose blocks begin at or before u
-    int b = 0;
-    for (int count = a.step.B; count > 1;) {
-      const int step = (count + 31) >> 5, i = lane * step;
-      const unsigned m = __ballot_sync(0xffffffffu, i < count && units[b + i] <= u);
-      const int k = 31 - __clz(m);
-      b += k * step;
-      count = min(step, count - k * step);
+  if (threadIdx.x == 0) *reinterpret_cast<Totals*>(a.ws) = Totals{total, static_cast<int>(ctas)};
+}
+
+// Where the run that begins `u` blocks into the list begins; cost0: what is before its
+// item.  A whole warp calls it; every lane gets the answer.
+__device__ __forceinline__ Start find_start(const PagedArgs& a, const long long* units, long long total, long long u, long long& cost0) {
+  const int lane = threadIdx.x & 31;
+  // the last sequence whose items begin at or before u
+  int b = 0;
+  for (int count = a.step.B; count > 1;) {
+    const int step = (count + 31) >> 5, i = lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i < count && units[b + i] <= u);
+    const int k = 31 - __clz(m);
+    b += k * step;
+    count = min(step, count - k * step);
+  }
+  const Seq q = load_seq(a.step, b);
+  const long long off = u - units[b];
+  const long long each = divide((b + 1 < a.step.B ? units[b + 1] : total) - units[b], static_cast<long long>(a.R) * a.pool.H);
+  const int rh = static_cast<int>(divide(off, each));
+  long long rest = off - rh * each;
+  const int np = pairs_of(a, q);
+  for (int p0 = 0; p0 < np; p0 += 32) {
+    const int p = p0 + lane;
+    int n = 0;
+    if (p < np) {
+      const Range g = pair_blocks(a, q, p);
+      n = g.j1 - g.j0 + kItemBlocks;
     }
-    const long long off = u - units[b];
-    const long long each = ((b + 1 < a.step.B ? units[b + 1] : total) - units[b]) / rh;
-    const int at_rh = static_cast<int>(off / each);
-    long long rest = off - at_rh * each;
-    const Seq q = load_seq(a.step, b);
-    const int np = pairs_of(a, q);
-    for (int p0 = 0; p0 < np; p0 += 32) {
-      const int p = p0 + lane;
-      int n = 0;
-      if (p < np) {
-        const Range g = pair_blocks(a, q, p);
-        n = g.j1 - g.j0 + kItemBlocks;
-      }
-      int incl = n;
+    int incl = n;
 #pragma unroll
-      for (int s = 1; s < 32; s *= 2) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, s);
-        if (lane >= s) incl += v;
-      }
-      const unsigned m = __ballot_sync(0xffffffffu, rest < incl);
-      if (m != 0) {
-        if (lane == __ffs(m) - 1)
-          // (an item's own cost comes before its first block: no cut falls into it)
-          starts[c] = Start{b, at_rh, p, max(0, static_cast<int>(rest - (incl - n)) - kItemBlocks)};
-        break;
-      }
-      rest -= __shfl_sync(0xffffffffu, incl, 31);
+    for (int s = 1; s < 32; s *= 2) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, s);
+      if (lane >= s) incl += v;
     }
+    const unsigned m = __ballot_sync(0xffffffffu, rest < incl);
+    if (m != 0) {
+      const int src = __ffs(m) - 1;
+      const int within = static_cast<int>(rest) - __shfl_sync(0xffffffffu, incl - n, src);
+      cost0 = u - within;
+      // (an item's own cost comes before its first block: no cut falls into it)
+      return Start{b, rh, p0 + src, max(0, within - kItemBlocks)};
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
   }
-  if (threadIdx.x == 0) {
-    starts[ctas] = Start{a.step.B, 0, 0, 0};
-    *reinterpret_cast<Totals*>(a.ws) = Totals{static_cast<int>(ctas)};
-  }
+  return Start{a.step.B, 0, 0, 0};             // (not reached: u lies before the list's end)
 }
 
 // This CTA's run of blocks.
 struct alignas(16) Run {
-  char* parts;
-  Header* header;
   Start start, stop;
+  long long cost, cost0;                       // of all items; of what is before the first one here
+  int ctas;                                    // with work
   bool busy;
 };
 
@@ -252,6 +257,7 @@ struct Walk {
   Seq q;
   int j0, j1;                                  // the item's blocks
   int ja, jb;                                  // the CTA's part of them
+  long long cost0;                             // of what is before the item
   Start stop;                                  // where the run ends
   int lo[2], hi[2];                            // tile t's blocks of [ja, jb): none if lo >= hi
   bool more;                                   // there is such an item
@@ -278,6 +284,7 @@ struct Walk {
   __device__ __forceinline__ bool begin(const PagedArgs& a, const Run& r) {
     if (!r.busy) return false;                 // (its start says nothing then)
     stop = r.stop;
+    cost0 = r.cost0;
     b = r.start.b;
     rh = r.start.rh;
     pair = r.start.pair;
@@ -287,6 +294,7 @@ struct Walk {
   }
   __device__ __forceinline__ bool next_item(const PagedArgs& a) {
     if (stop.same_item(Start{b, rh, pair, 0})) return false;
+    cost0 += j1 - j0 + kItemBlocks;
     if (++pair == pairs) {
       pair = 0;
       if (++rh == a.R * a.pool.H) {
@@ -519,18 +527,24 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
   const ptx::Waiter W{abort_flag, a.status, timeout_ns};
   ptx::griddep_wait();
   ptx::griddep_launch_dependents();
-  if (threadIdx.x == 0) {
+  if (warp < 2) {                              // where this run begins, and where the next one does
     const Layout lay = layout_of(D, a.step.B, gridDim.x);
-    const Start* starts = reinterpret_cast<const Start*>(a.ws + lay.starts);
-    const int c = blockIdx.x;
-    run->busy = c < reinterpret_cast<const Totals*>(a.ws)->ctas;
-    if (run->busy) {
-      run->start = starts[c];
-      run->stop = starts[c + 1];
+    const Totals tot = *reinterpret_cast<const Totals*>(a.ws);
+    const int c = static_cast<int>(blockIdx.x) + warp;
+    Start s{a.step.B, 0, 0, 0};                // (behind all items)
+    long long cost0 = 0;
+    if (c < tot.ctas)
+      s = find_start(a, reinterpret_cast<const long long*>(a.ws + lay.units), tot.cost, divide(c * tot.cost, tot.ctas), cost0);
+    if (lane == 0) {
+      (warp == 0 ? run->start : run->stop) = s;
+      if (warp == 0) {
+        run->cost = tot.cost;
+        run->cost0 = cost0;
+        run->ctas = tot.ctas;
+        run->busy = c < tot.ctas;
+        reinterpret_cast<Header*>(a.ws + lay.headers)[blockIdx.x] = Header{0, 0, 0, 0};
+      }
     }
-    reinterpret_cast<Header*>(a.ws + lay.headers)[c] = Header{0, 0, 0, 0};
-    run->parts = a.ws + lay.parts;
-    run->header = reinterpret_cast<Header*>(a.ws + lay.headers) + c;
   }
   __syncthreads();
 
@@ -989,7 +1003,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
       }
       const int r = cur.rank(a);
       const bool complete = cur.ja == cur.j0 && cur.jb == cur.j1;
-      char* part = run->parts + static_cast<size_t>(2 * blockIdx.x + (cur.ja == cur.j0 ? 1 : 0)) * kPartBytes<D>;
+      char* part = a.ws + layout_of(D, a.step.B, gridDim.x).parts + static_cast<size_t>(2 * blockIdx.x + (cur.ja == cur.j0 ? 1 : 0)) * kPartBytes<D>;
       const int prow = t * kTileRows + row;
       const bool none = l == 0.f;
       const float inv = complete ? 1.f / l : 1.f;
@@ -1074,11 +1088,10 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           st[kPairRows + prow] = l;
         }
         if (cur.ja == cur.j0 && threadIdx.x == 0) {
-          // (the CTAs whose runs begin within the item have its other parts)
-          const Start* next = reinterpret_cast<const Start*>(a.ws + layout_of(D, a.step.B, gridDim.x).starts) + blockIdx.x + 1;
-          int parts = 1;
-          while (next[parts - 1].same_item(Start{cur.b, cur.rh, cur.pair, 0})) ++parts;
-          *run->header = Header{parts, cur.b, cur.rh, cur.pair};
+          // the CTA that has the item's last block
+          const long long last = divide((cur.cost0 + (cur.j1 - cur.j0) + kItemBlocks) * run->ctas - 1, run->cost);
+          reinterpret_cast<Header*>(a.ws + layout_of(D, a.step.B, gridDim.x).headers)[blockIdx.x] =
+              Header{static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1, cur.b, cur.rh, cur.pair};
         }
       }
     }
