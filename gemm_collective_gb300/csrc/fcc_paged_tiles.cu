@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         uint4 x[kN];
         int byte = 1;
         u = kind;
-        auto fetch = [&](int64_t row) {
+        auto fetch = [&](int64_t row, int r) {
           const char* pool = (kind == 0 ? a.pool.K[r] : a.pool.V[r]) + piece * 16;
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
@@ -708,11 +708,16 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           }
           if (row >= 0) byte = (kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r])[row];
         };
+        // A block is looked up two blocks ahead and brought into the L2 one block ahead of
+        // its loads: they would wait for DRAM between one block's conversion and the next.
         int64_t row = row_of();
         bool full = have;
-        if (full) fetch(row);
+        if (full) fetch(row, r);
+        look_up();
         while (full) {
-          look_up();                           // the next block
+          const bool next = have;
+          const int next_r = r, next_h = h, next_page = page, next_in = in_page;
+          look_up();
           if (!(ok = wait_slot())) break;
           const uint32_t power = constants(row, byte);
           uint8_t* dst = sR + (u % kSlots) * kTile;
@@ -734,9 +739,14 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&r_full[u % kSlots]);
           u += 2;
-          row = row_of();
-          full = have;
-          if (full) fetch(row);
+          full = next;
+          row = next_page < 0 ? -1 : ((static_cast<int64_t>(next_page) * a.pool.H + next_h) << a.pool.log2P) + next_in;
+          if (full) fetch(row, next_r);
+          if (page >= 0) {
+            const int64_t far = row_of();
+            ptx::prefetch_l2((kind == 0 ? a.pool.K[r] : a.pool.V[r]) + far * kRow);
+            ptx::prefetch_l2((kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r]) + far);
+          }
         }
       } else {
         // A warp's 32 positions come by TMA, a box of a page's rows and 64 columns at a
