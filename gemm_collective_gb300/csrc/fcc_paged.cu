@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   bool more = true;
   int page[kPer], in_page[kPer] = {}, pool_r = 0, pool_h = 0;
   const int* table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;   // of lw's sequence
-  uint32_t pos = lw.first + lw.k * kUnit + warp * kTok + lane;   // of the next slice's
+  uint32_t pos = static_cast<uint32_t>(lw.first) + static_cast<uint32_t>(lw.k) * kUnit + warp * kTok + lane;   // of the next slice's
   auto look_up = [&]() {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) page[i] = -1;
@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
     if (++lw.k == lw.end) {
       more = lw.next_item(a);
       table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;
-      pos = lw.first + lw.k * kUnit + warp * kTok + lane;
+      pos = static_cast<uint32_t>(lw.first) + static_cast<uint32_t>(lw.k) * kUnit + warp * kTok + lane;
     }
   };
   auto issue = [&](int slot) -> Slice {
@@ -825,18 +825,17 @@ int form_of(int64_t T, int B, int G, bool e4m3) {
   return rows <= (e4m3 ? kFewRowsE4m3 : kFewRowsBf16) * each ? 2 : 0;
 }
 
-int usable_sms(const fcc_opts* o) {
+// CTAs of a form's kernel: two to an SM, or one of tiles_kernel's.
+int ctas_of(int form, const fcc_opts* o) {
   int sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
     sms = 256;  // (no device: sizes for the largest grid)
   }
-  return o != nullptr && o->max_ctas > 0 ? std::min(sms, o->max_ctas) : sms;
+  const int ctas = sms * (form != 0 ? 2 : 1);
+  return o != nullptr && o->max_ctas > 0 ? std::min(ctas, o->max_ctas) : ctas;
 }
-
-// CTAs of a form's kernel: two to an SM, or one of tiles_kernel's.
-int ctas_of(int form, const fcc_opts* o) { return usable_sms(o) * (form != 0 ? 2 : 1); }
 
 size_t form_ws_bytes(int form, int B, int64_t d, int ctas) {
   return form != 0 ? header_bytes(ctas) + 2 * static_cast<size_t>(ctas) * part_floats(static_cast<int>(d), form) * sizeof(float)

@@ -4,11 +4,13 @@
 // A row is a token and one of the G query heads that share a key/value head, so a
 // tile's rows read the same keys whatever G is, and few tokens fill it.  An item is
 // a pair of tiles (256 rows of one sequence, rank and head) and its blocks of 128
-// positions, from the first that any row sees to the last.  plan_kernel counts all
-// items' blocks and cuts their list into as many equal runs as there are CTAs, one
-// to an SM: causal, windowed and ragged steps load all SMs alike, and a few rows
-// over a long context are spread over all of them.  What a cut leaves of an item
-// are partial sums, at most two from a CTA, added in order by join_kernel.
+// positions, from the first that any row sees to the last.  plan_kernel adds up what
+// all items cost (their blocks, and four more each), and the list is cut into as many
+// equal runs as there are CTAs, one to an SM: causal, windowed and ragged steps load all
+// SMs alike, and a few rows over a long context are spread over all of them.  (Without
+// the four, the CTAs with a causal prompt's many short items came last: 1.60 against
+// 1.05 ms for 8192 rows of 64 heads.)  What a cut leaves of an item are partial sums, at
+// most two from a CTA, added in order by join_kernel.
 //
 // Within an item, for tile t and block j (all f32 in TMEM):
 //   S_t = Q_t K_j^T;  P_t = 2^(S_t c - ref), in 16 bits over S_t's first columns;
@@ -18,14 +20,20 @@
 // tile's exponentials run under the other's products.  A new item's queries are
 // loaded, and its first S computed, before the old one's O has been stored.
 //
-// Warps: 0-3 and 4-7 softmax and output of tiles A and B (a thread owns a row and
-// its 128 columns), then those that load keys and values and the one that issues the
-// products.  The
-// loaders look up every position's page for itself (any page size), bf16 rows go
-// by TMA into the swizzled tile, 32 positions to a warp.  e4m3 rows pass through registers and become
-// f16 there, times their powers of two relative to the largest, 2^A of the keys and
-// 2^B of the values, of each 32 positions; those enter at the exponent (see
-// fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
+// Warps: 0-3 and 4-7 softmax and output of tiles A and B (a thread owns a row and its
+// 128 columns), then those that load keys and values and the one that issues the
+// products.  The loaders look up every position's page for itself (any page size).
+// bf16 rows go by TMA into the swizzled tile, 32 positions to a warp.  e4m3 rows pass
+// through registers and become f16 there, times their powers of two relative to the
+// largest, 2^A of the keys and 2^B of the values, of each 32 positions; those enter at
+// the exponent (see fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
+//
+// What bounds it: 2048 rows of 32 heads over 32768 positions take 823 us in bf16
+// (1294 TFLOP/s, 0.66 of the measured burst peak), 1.9 us a block and pair.  A
+// 128 x 128 x 16 product alone takes 64 clocks, 2048 for a block; here each takes about
+// 100, because the operands of S fill shared memory's 128 bytes a clock by themselves
+// and the next blocks' TMA writes come on top.  e4m3 (1067 us) waits for its loaders'
+// conversions and the maximum that f16 needs before the exponentials.
 // Shared memory (128-byte swizzle): Q_t and four slots of [128 rows][D] 16-bit
 // values in atoms of 64 columns, K_0, V_0, K_1, V_1, ... in the slots; K is the
 // K-major and V the MN-major B operand of the same layout.
@@ -308,7 +316,6 @@ struct Walk {
     }
     return take(a, 0);
   }
-  __device__ __forceinline__ bool sees(int j, int t) const { return j >= lo[t] && j < hi[t]; }
   // Tile t has a block here.  Where it has none, its softmax warps and the issuing
   // warp pass the item without a word: a barrier's phases stay one to an exchange.
   __device__ __forceinline__ bool active(int t) const { return lo[t] < hi[t]; }
@@ -343,17 +350,16 @@ struct alignas(16) Columns {
   uint32_t wide[2][4];                         // keys', values' powers too far apart for f16, see f16_power()
 };
 
-// 2^(byte - top) in f16 (both halves), 0 below what f16 holds.  An e4m3 code times it
-// stays within f16 and is off by 2^-25 at most, so a row whose power is up to 2^20
-// below its group's largest keeps its own digits to 2^-12 of its maximum (224 and
-// more in codes).  Rows further below are `wide`: their tile is computed again row by
-// row.  (Byte 63 holds what is nearly zero on its own.)
+// 2^(byte - top) in f16 (both halves).  An e4m3 code (a multiple of 2^-9) times it is
+// exact in f16 down to 2^-15.  A group with powers further apart is `wide`: the rows
+// that met it are computed again one by one.  (Byte 63 holds what is nearly zero on its
+// own, a row of zeros above all: that may vanish.)
 __device__ __forceinline__ uint32_t f16_power(int byte, int top) {
   const int k = byte - top;
-  const uint32_t h = k >= -14 ? static_cast<uint32_t>(15 + k) << 10 : k >= -24 ? 1u << (24 + k) : 0u;
+  const uint32_t h = k >= -14 ? static_cast<uint32_t>(15 + k) << 10 : k == -15 ? 1u << 9 : 0u;
   return h | (h << 16);
 }
-__device__ __forceinline__ bool too_wide(int byte, int top) { return byte < top - 20 && byte > 63; }
+__device__ __forceinline__ bool too_wide(int byte, int top) { return byte < top - 15 && byte > 63; }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -791,7 +797,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           }
           if (!ok) break;
         }
-        if (*abort_flag && a.boxes)            // copies in flight land before the block ends
+        if (a.boxes)                           // copies in flight land before the block ends
           for (uint32_t v = u >= kSlots ? u - kSlots : 0; v < u; ++v)
             W.drain(&r_full[v % kSlots], (v / kSlots) & 1u, kDrainNs);
       }

@@ -166,6 +166,62 @@ def test_attention(dtype, d, P, seqs):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8])
+def test_ragged_steps_in_every_form(dtype, G):
+    """6.25 rows to a sequence for each head of a group: by items of 8 and of 16 rows, and by tiles of 128, each
+    with a sequence of many rows among ones of few."""
+    s = Step([(1, 300), (21, 400), (1, 1), (2, 130)], H=2, dtype=dtype, seed=G, lead=1)
+    Q = queries(s, G)
+    for window in (0, 77):
+        O, lse = attend(s, G, Q, window=window)
+        assert fcc.fcc_stream_status() == fcc.FCC_OK
+        check(s, G, Q, O, lse, 1 / np.sqrt(128), window)
+        again, z = attend(s, G, Q, window=window)
+        assert torch.equal(O[0], again[0]) and torch.equal(lse[0], z[0])  # a fixed order of summation
+
+
+@pytest.mark.parametrize("B,n,G", [(700, 1, 2), (1100, 3, 12)])
+def test_many_sequences(B, n, G):
+    """More sequences than a block of threads counts one by one, some without rows."""
+    seqs = [(0 if b % 7 == 3 else n, n + b % 23) for b in range(B)]
+    s = Step(seqs, H=1, d=64, P=8, dtype="bf16", seed=1)
+    Q = queries(s, G)
+    O, lse = attend(s, G, Q)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(s, G, Q, O, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("case,G", [([(1, 200), (1, 70)], 4), ([(9, 200)], 3), ([(150, 300), (40, 40)], 2)])
+@pytest.mark.parametrize("step", [10, 16, 40])
+def test_powers_of_neighbours_far_apart(case, G, step):
+    """e4m3 rows whose powers of two differ by 2^step from one position to the next: the small ones keep their digits."""
+    s = Step(case, H=2, dtype="e4m3", seed=step)
+    for which in (0, 1):
+        e = s.exps[which].astype(int)
+        e[:, :, :, 1::3] -= step
+        e[:, :, :, 2::3] = 63  # 2^-64, the least that append writes
+        s.exps[which] = np.clip(e, 63, 247).astype(np.uint8)
+        s.vals[which] = oc.values(s.codes[which], s.exps[which])
+    s.upload()
+    Q = queries(s, G, amp=3.0)
+    O, lse = attend(s, G, Q, window=2)  # (few positions to a row: some rows see only small ones)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(s, G, Q, O, lse, 1 / np.sqrt(128), 2)
+    O, lse = attend(s, G, Q)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(s, G, Q, O, lse, 1 / np.sqrt(128))
+
+
+def test_eight_ranks():
+    s = Step([(1, 150), (3, 40)], H=1, d=64, P=4, dtype="e4m3", R=8)
+    for G in (2, 30):
+        Q = queries(s, G)
+        O, lse = attend(s, G, Q)
+        assert fcc.fcc_stream_status() == fcc.FCC_OK
+        check(s, G, Q, O, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 100, 128, 129, 1000000])
 def test_window(dtype, window):
     for case, G in [([(1, 300), (1, 17), (1, 1)], 4), ([(40, 300), (1, 290), (140, 140)], 3)]:
@@ -374,6 +430,23 @@ def test_append_and_gather(dtype, d, P, H):
             assert same[~touched].all()
     for which in range(2):
         assert all(bool((x[torch.from_numpy(~owner).cuda()] == 7).all()) for x in back[which])
+
+
+def test_rows_of_sequences_far_apart_in_the_list():
+    """Neighbouring rows with many sequences without rows between them, and rows that begin in the middle of a group."""
+    seqs = [(2, 5)] + [(0, 7)] * 70 + [(3, 9)] + [(0, 0)] * 40 + [(1, 1)] * 33 + [(25, 31)]
+    s = Step(seqs, H=3, d=64, P=4, dtype="bf16", lead=3, behind=9)
+    x = torch.randn(2, s.T, 3, 64, device="cuda").bfloat16()
+    fcc.fcc_cache_append(1, [x[0]], [x[1]], s.cache(), s.batch())
+    out = torch.full_like(x, 7.0)
+    fcc.fcc_cache_gather(1, s.cache(), s.batch(), [out[0]], [out[1]])
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    assert torch.equal(out[:, 3:-9], x[:, 3:-9]) and bool((out[:, :3] == 7).all()) and bool((out[:, -9:] == 7).all())
+    for b in (0, 71, 112, 144, 145):
+        n, L = seqs[b]
+        for which, pool in ((0, s.K[0]), (1, s.V[0])):
+            got = oc.rows_of(to_f64(pool), s.table_np[b], L - n, L)
+            assert np.array_equal(got, to_f64(x[which, int(s.start_np[b]):int(s.start_np[b]) + n])), b
 
 
 def test_append_of_numbers_that_are_not_finite():
