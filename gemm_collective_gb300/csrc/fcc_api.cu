@@ -1157,52 +1157,6 @@ fcc_status internal_encode_map(CUtensorMap* m, const void* ptr, int64_t rows, in
              : FCC_ERR_CUDA;
 }
 
-// The same direct-mapped reuse as make_map's, for the pools' maps.
-fcc_status internal_pool_map(CUtensorMap* m, const void* ptr, int64_t pages, int H, int P, int d,
-                             uint32_t box_rows) {
-  struct Key {
-    const void* ptr;
-    int64_t pages;
-    int H, P, d;
-    uint32_t box_rows;
-  };
-  struct Entry {
-    bool used = false;
-    Key key{};
-    CUtensorMap map{};
-  };
-  constexpr size_t kEntries = 256;
-  static Entry entries[kEntries];
-  static std::mutex mu;
-  uint64_t h = reinterpret_cast<uintptr_t>(ptr) * 0x9E3779B97F4A7C15ull;
-  h ^= static_cast<uint64_t>(pages) * 0xC2B2AE3D27D4EB4Full;
-  Entry& e = entries[(h >> 32) % kEntries];
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    const Key& k = e.key;
-    if (e.used && k.ptr == ptr && k.pages == pages && k.H == H && k.P == P && k.d == d &&
-        k.box_rows == box_rows) {
-      *m = e.map;
-      return FCC_OK;
-    }
-  }
-  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(P),
-                        static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(pages)};
-  cuuint64_t strides[3] = {row, row * P, row * P * H};
-  cuuint32_t box[4] = {64, box_rows, 1, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  if (g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box,
-               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return FCC_ERR_CUDA;
-  std::lock_guard<std::mutex> lk(mu);
-  e.used = true;
-  e.key = Key{ptr, pages, H, P, d, box_rows};
-  e.map = *m;
-  return FCC_OK;
-}
-
 fcc_status internal_streams_events(cudaStream_t* side, int nside, cudaEvent_t* ev, int nev) {
   DeviceState* d = nullptr;
   fcc_status s = device_state(&d);

@@ -258,10 +258,6 @@ fcc_status internal_make_map(CUtensorMap* m, const void* ptr, int64_t rows, int6
 // columns has the 128-byte swizzle, one of 32 the 64-byte swizzle.
 fcc_status internal_encode_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols,
                                int64_t ld, uint32_t box_rows, uint32_t box_cols = 64);
-// 4-D bf16 tensor map of a pool [pages, H, P, d], box [1, 1, box_rows, 64], 128-byte
-// swizzle (after internal_prepare).
-fcc_status internal_pool_map(CUtensorMap* m, const void* ptr, int64_t pages, int H, int P, int d,
-                             uint32_t box_rows);
 // A side stream and n <= 8 events of the current device (after internal_prepare).
 fcc_status internal_side_stream(cudaStream_t* side, cudaEvent_t* ev, int n);
 // The device's side streams 0..nside-1 (nside <= 4) and events 0..nev-1

@@ -44,8 +44,55 @@
 #include <algorithm>
 #include <climits>
 #include <cstring>
+#include <mutex>
 
 namespace fcc {
+namespace ptx {
+
+// 4-D tiled load global -> shared, completion counted on `bar` in bytes.
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Stores 16 consecutive 32-bit columns of each thread's TMEM lane.
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// mma_f16 and mma_f16_tmem_a (fcc_ptx.cuh) with the descriptors as words: their low ones,
+// and a high one that both share.
+__device__ __forceinline__ void mma_f16_words(uint32_t d_tmem, uint32_t a_low, uint32_t b_low,
+                                              uint32_t high, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(high), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_tmem_a_words(uint32_t d_tmem, uint32_t a_tmem,
+                                                     uint32_t b_low, uint32_t high, uint32_t idesc,
+                                                     uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(high), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+}  // namespace ptx
+
 namespace {
 
 constexpr int kTileRows = 128;
@@ -1165,6 +1212,60 @@ __global__ void __launch_bounds__(kPairRows) join_kernel(const __grid_constant__
   if (blockIdx.y == 0 && a.lse[r] != nullptr) a.lse[r][token * a.Hq + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
 }
 
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// 4-D bf16 tensor map of a pool [pages, H, P, d], box [1, 1, box_rows, 64], 128-byte
+// swizzle.  An encoding is a pure function of what it is given: calls on the same pools
+// reuse it (direct-mapped).
+bool pool_map(CUtensorMap* m, const void* ptr, int64_t pages, int H, int P, int d, uint32_t box_rows) {
+  struct Entry {
+    const void* ptr = nullptr;
+    int64_t pages = 0;
+    int H = 0, P = 0, d = 0;
+    uint32_t box_rows = 0;
+    CUtensorMap map{};
+  };
+  constexpr size_t kEntries = 256;
+  static Entry entries[kEntries];
+  static EncodeTiledFn encode = nullptr;
+  static std::mutex mu;
+  uint64_t hash = reinterpret_cast<uintptr_t>(ptr) * 0x9E3779B97F4A7C15ull;
+  hash ^= static_cast<uint64_t>(pages) * 0xC2B2AE3D27D4EB4Full;
+  std::lock_guard<std::mutex> lk(mu);
+  Entry& e = entries[(hash >> 32) % kEntries];
+  if (e.ptr == ptr && e.pages == pages && e.H == H && e.P == P && e.d == d && e.box_rows == box_rows) {
+    *m = e.map;
+    return true;
+  }
+  if (encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess || fn == nullptr)
+      return false;
+    encode = reinterpret_cast<EncodeTiledFn>(fn);
+  }
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(P), static_cast<cuuint64_t>(H),
+                              static_cast<cuuint64_t>(pages)};
+  const cuuint64_t strides[3] = {row, row * P, row * P * H};
+  const cuuint32_t box[4] = {64, box_rows, 1, 1}, steps[4] = {1, 1, 1, 1};
+  if (encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  e.ptr = ptr;
+  e.pages = pages;
+  e.H = H;
+  e.P = P;
+  e.d = d;
+  e.box_rows = box_rows;
+  e.map = *m;
+  return true;
+}
+
 template <int D, bool E4M3>
 cudaError_t launch(PagedArgs a, int ctas, unsigned long long timeout_ns, cudaStream_t st) {
   PoolMaps maps;
@@ -1172,8 +1273,8 @@ cudaError_t launch(PagedArgs a, int ctas, unsigned long long timeout_ns, cudaStr
   const int P = 1 << a.pool.log2P;
   a.boxes = !E4M3 && P >= 16 ? 1 : 0;
   for (int r = 0; r < a.R && a.boxes; ++r)
-    if (internal_pool_map(&maps.K[r], a.pool.K[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)) != FCC_OK ||
-        internal_pool_map(&maps.V[r], a.pool.V[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)) != FCC_OK)
+    if (!pool_map(&maps.K[r], a.pool.K[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)) ||
+        !pool_map(&maps.V[r], a.pool.V[r], a.pool.pages, a.pool.H, P, D, std::min(P, 32)))
       return cudaErrorUnknown;
   static bool attr_set[64] = {};
   cudaError_t e = smem_attr_once(attr_set, tiles_kernel<D, E4M3>, kSmem<D>);
