@@ -5,10 +5,10 @@
 // tile's rows read the same keys whatever G is, and few tokens fill it.  An item is
 // a pair of tiles (256 rows of one sequence, rank and head) and its blocks of 128
 // positions, from the first that any row sees to the last.  plan_kernel adds up what
-// all items cost (their blocks, and four more each), and the list is cut into as many
+// all items cost (their blocks, and three more each), and the list is cut into as many
 // equal runs as there are CTAs, one to an SM: causal, windowed and ragged steps load all
 // SMs alike, and a few rows over a long context are spread over all of them.  (Without
-// the four, the CTAs with a causal prompt's many short items came last: 1.60 against
+// the three, the CTAs with a causal prompt's many short items came last: 1.60 against
 // 1.05 ms for 8192 rows of 64 heads.)  What a cut leaves of an item are partial sums, at
 // most two from a CTA, added in order by join_kernel.
 //
@@ -162,7 +162,7 @@ __device__ __forceinline__ int pairs_of(const PagedArgs& a, const Seq& q) {
 
 // What an item costs beside its blocks, in blocks: its queries' loads, the first S and
 // the last P V that nothing runs beside, its output.
-constexpr int kItemBlocks = 4;
+constexpr int kItemBlocks = 3;
 
 // Blocks [j0, j1) that rows [first, last] of a sequence see.
 struct Range {

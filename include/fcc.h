@@ -39,8 +39,8 @@
  *  - Environment defaults, read once when the library first needs one:
  *    FCC_ALGO=fused|unfused|interdecom|ce replaces FCC_ALGO_AUTO (also in
  *    fcc_choose_algo) for the operators with several forms (a form an
- *    operator lacks gives FCC_ERR_UNSUPPORTED; the attention, the MoE
- *    combine and the losses have one form and ignore it); FCC_DETERMINISTIC=0|1 is the
+ *    operator lacks gives FCC_ERR_UNSUPPORTED; the attentions, the cache,
+ *    the MoE combine and the losses have one form and ignore it); FCC_DETERMINISTIC=0|1 is the
  *    summation mode of calls with opts == NULL; FCC_CHUNKS=n (1..64) the
  *    InterDecom chunk count where opts->chunks is 0; FCC_TIMEOUT_MS=n the
  *    device wait limit where opts->timeout_ns is 0.  Unset or unparsable
@@ -512,15 +512,18 @@ fcc_status fcc_cache_gather(int R, const fcc_cache *cache, const fcc_batch *batc
  * Hq * d; multiples of 8): O[r] is the A of fcc_gemv_ar or fcc_gemm_ar for
  * the output projection.  lse: NULL, or R arrays [T, Hq] f32.  scale: 0 means
  * 1 / sqrt(d), otherwise finite and positive.  Hq % H == 0, Hq <= 1024.
- * Scores, maxima, sums and O's accumulators are f32; the probabilities enter
- * the product with V in 16 bits (bf16, relative to a running maximum; where the
- * rows are few and the cache is e4m3, f16).  Repeatable (a fixed order of summation).
+ * Scores, maxima, sums and O's accumulators are f32; the probabilities enter the
+ * product with V in 16 bits (bf16; f16 where the cache is e4m3), relative to a running
+ * maximum.  Repeatable (a fixed order of summation).  Powers of an e4m3 cache are read
+ * as append writes them (bytes 63 to 247); rows of byte 63, nearly zero by themselves,
+ * may count as zero.  O[r] must not overlap Q[r].
  * A sequence with len[b] < n has no visible positions; a row with none has
  * O = 0, lse = -inf.  Where a needed page is not valid, or lies past
  * max_pages, its positions are left out.  Both record FCC_ERR_INVALID.
- * One token or many: a step with up to 16 query rows to a sequence and
+ * One token or many: a step with up to 16 query rows (e4m3: 32) to a sequence and
  * key/value head on average (T * Hq / H <= 16 B) is read as few rows over many
- * positions, any other one in tiles of 128 rows; both take every step.
+ * positions, any other one in tiles of 128 rows; both take every step.  T * Hq / H is
+ * below 2^31 - 256.
  * Uses workspace (fcc_paged_attention_workspace_size).  A call made while its
  * stream is being captured must bring its own (FCC_ERR_WORKSPACE): the pool may
  * move before the graph is replayed.  Graphs and streams that run at the same time
