@@ -943,13 +943,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           return m & (lo <= 0 ? 0xffffffffu : lo >= 32 ? 0u : ~((1u << lo) - 1));
         };
         const bool mask = !__all_sync(0xffffffffu, whole || !live);
-        auto hide = [&](uint32_t (&x)[32], int k) {  // what the row does not see
-          if (!mask) return;
-          const uint32_t m = seen(k);
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(m >> i & 1)) x[i] = 0xff800000u;
-        };
         bool raise;                            // the row asks for a new reference
         float to;
         if (!E4M3 && !mask && __all_sync(0xffffffffu, ref != -INFINITY || !live)) {
@@ -964,13 +957,20 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
             uint32_t x[32];
             ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, x);
             tmem_ld_wait_regs(x);
-            hide(x, k);
+            if (mask) {                        // what the row does not see, here and for the exponentials
+              const uint32_t m = seen(k);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(m >> i & 1)) x[i] = 0xff800000u;
+              ptx::tmem_st_32x32b_x32(s_addr + 32 * k, x);
+            }
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int i = 0; i < 32; i += 2) mx[i / 2 & 3] = ptx::max3(mx[i / 2 & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
             const float m32 = fmaxf(ptx::max3(mx[0], mx[1], mx[2]), mx[3]);
             top = fmaxf(top, E4M3 ? fmaf(m32, c * cc.ka[k], cc.vb[k]) : m32 * c);
           }
+          if (mask) ptx::tmem_st_wait();
           raise = top > ref + (kOff + kRaise<E4M3>);
           to = top - kOff;
         }
@@ -993,7 +993,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
         const float sub = ref == -INFINITY ? 0.f : ref;
         auto exponentials = [&](uint32_t (&x)[32], int k) {
-          hide(x, k);
           const float ck = E4M3 ? c * cc.ka[k] : c, rk = E4M3 ? cc.vb[k] - sub : -sub;
           const uint64_t c2 = ptx::f32x2_pack(ck, ck), r2 = ptx::f32x2_pack(rk, rk);
           uint64_t l2[2] = {0, 0};
