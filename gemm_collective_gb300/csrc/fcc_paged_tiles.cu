@@ -475,7 +475,7 @@ __device__ __forceinline__ float4* part_at(char* part, int c4, int row) {
 // in a product with P = 0 a value that is not finite reaches rows that do not see it,
 // and rows that saw powers too far apart.
 template <int D, bool E4M3>
-__device__ __forceinline__ void row_again(const PagedArgs& a, int b, int r, int h, int head, int64_t t, int from, int to, int lane,
+__device__ __noinline__ void row_again(const PagedArgs& a, int b, int r, int h, int head, int64_t t, int from, int to, int lane,
                                        float (&o)[D / 32], float& ref, float& l) {
   constexpr int N = D / 32;
   float x[N];
@@ -1011,29 +1011,15 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           // (P's columns 16 k .. 16 k + 15 lie over scores already read)
           ptx::tmem_st_32x32b_x16(s_addr + 16 * k, pk);
         };
-        // (rolled loops: thirteen warps in five roles share the instruction caches, and
-        // what they do not hold costs more than the branches)
-        if constexpr (E4M3) {                  // (its softmax threads have fewer registers)
+        // (Rolled: the warps of five roles share the instruction caches, and what they do
+        // not hold costs more than a load's latency.  Two chunks a step, one under the
+        // other's load, took 832 instead of 800 us for 2048 rows over 32768 positions.)
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t x[32];
-            ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, x);
-            tmem_ld_wait_regs(x);
-            exponentials(x, k);
-          }
-        } else {
-          uint32_t x[2][32];
-          ptx::tmem_ld_32x32b_x32(s_addr, x[0]);
-          tmem_ld_wait_regs(x[0]);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            ptx::tmem_ld_32x32b_x32(s_addr + 64 * half + 32, x[1]);
-            exponentials(x[0], 2 * half);
-            tmem_ld_wait_regs(x[1]);
-            if (half == 0) ptx::tmem_ld_32x32b_x32(s_addr + 64, x[0]);
-            exponentials(x[1], 2 * half + 1);
-            tmem_ld_wait_regs(x[0]);
-          }
+        for (int k = 0; k < 4; ++k) {
+          uint32_t x[32];
+          ptx::tmem_ld_32x32b_x32(s_addr + 32 * k, x);
+          tmem_ld_wait_regs(x);
+          exponentials(x, k);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
