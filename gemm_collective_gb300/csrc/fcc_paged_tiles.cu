@@ -438,6 +438,13 @@ __device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
   return (chunk >> 3) * kAtom + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
+// One lane of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -608,60 +615,77 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
   if (warp >= kIssuer) {
     // ----------------------------------------------------------- MMA issue
     regs_dec<Roles<E4M3>::kIssue>();
-    if (warp == kIssuer && lane == 0) {
-      // (what the loop over blocks needs is in registers: this thread's own instructions
-      // stand between one product and the next)
-      Walk& w = walks[kIssuer].now;
+    if (warp == kIssuer) {
+      // The whole warp walks and waits, and one lane issues: what a product takes stays
+      // in registers that the warp shares.  What the loop over blocks needs is in
+      // registers too: this warp's own instructions stand between one product and the next.
+      WarpWalk& ww = walks[kIssuer];
+      const bool lead = elect_one();
       bool any = false, ok = true;
-      bool more = w.begin(a, *run);
+      ww.begin(a, *run, lane);
       uint32_t q_phase = 0, p_phase = 0;       // bit t: the parity that Q_t / P_t will complete
       uint32_t u = 0;                          // ring position of the block's K, V is at u + 1
-      const uint32_t qd0 = desc_low(sQ, 16), kd0 = desc_low(sR, 16), vd0 = desc_low(sR, kAtom);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+      const uint32_t qd0 = __shfl_sync(0xffffffffu, desc_low(sQ, 16), 0), kd0 = __shfl_sync(0xffffffffu, desc_low(sR, 16), 0),
+                     vd0 = __shfl_sync(0xffffffffu, desc_low(sR, kAtom), 0);
       // O_t += P_t V, the V at ring position `pos`.
       auto issue_pv = [&](int t, uint32_t pos, bool first) -> bool {
         const uint32_t vd = vd0 + (pos % kSlots) * (kTile >> 4);
-        const uint32_t pa = tmem_base + t * 128, o = tmem_base + kColO + t * 128;
+        const uint32_t pa = tmem + t * 128, o = tmem + kColO + t * 128;
         // (P as a whole: its halves as they come, on a barrier each, were 4 to 13 % slower)
-        if (!W.wait(&p_full[t], p_phase >> t & 1u)) return false;
+        if (!wait_warp(&p_full[t], p_phase >> t & 1u)) return false;
         ptx::tc_fence_after();
+        if (lead) {
 #pragma unroll
-        for (int kk = 0; kk < kBlock / 16; ++kk)
-          ptx::mma_f16_tmem_a_words(o, pa + kk * 8, vd + step_mnmajor(kk), kDescHigh, kIdescO, (!first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBlock / 16; ++kk)
+            ptx::mma_f16_tmem_a_words(o, pa + kk * 8, vd + step_mnmajor(kk), kDescHigh, kIdescO, (!first || kk > 0) ? 1u : 0u);
+        }
+        __syncwarp();
         p_phase ^= 1u << t;
         return true;
       };
       auto issue_s = [&](int t) {
         const uint32_t qd = qd0 + t * (kTile >> 4), kd = kd0 + (u % kSlots) * (kTile >> 4);
+        if (lead) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          ptx::mma_f16_words(tmem_base + t * 128, qd + step_kmajor(kk), kd + step_kmajor(kk), kDescHigh, kIdescS, kk > 0 ? 1u : 0u);
-        ptx::mma_commit(&s_full[t]);
+          for (int kk = 0; kk < D / 16; ++kk)
+            ptx::mma_f16_words(tmem + t * 128, qd + step_kmajor(kk), kd + step_kmajor(kk), kDescHigh, kIdescS, kk > 0 ? 1u : 0u);
+          ptx::mma_commit(&s_full[t]);
+        }
+        __syncwarp();
       };
-      while (more && ok) {
-        const int ja = w.ja, jb = w.jb, lo0 = w.lo[0], hi0 = w.hi[0], lo1 = w.lo[1], hi1 = w.hi[1];
+      while (ok && __shfl_sync(0xffffffffu, ww.now.more ? 1 : 0, 0) != 0) {
+        auto same = [&](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+        const int ja = same(ww.now.ja), jb = same(ww.now.jb), lo0 = same(ww.now.lo[0]), hi0 = same(ww.now.hi[0]),
+                  lo1 = same(ww.now.lo[1]), hi1 = same(ww.now.hi[1]);
         any = true;
-        if (lo0 < hi0) ok = W.wait(&q_full[0], q_phase & 1u), q_phase ^= 1u;
-        if (ok && lo1 < hi1) ok = W.wait(&q_full[1], q_phase >> 1 & 1u), q_phase ^= 2u;
+        if (lo0 < hi0) ok = wait_warp(&q_full[0], q_phase & 1u), q_phase ^= 1u;
+        if (ok && lo1 < hi1) ok = wait_warp(&q_full[1], q_phase >> 1 & 1u), q_phase ^= 2u;
         // one step more than there are blocks: the last one's P V
         for (int j = ja; j <= jb && ok; ++j, u += 2) {
-          if (j < jb && !(ok = W.wait(&r_full[u % kSlots], u / kSlots & 1u))) break;
-          if (j > ja && !(ok = W.wait(&r_full[(u - 1) % kSlots], (u - 1) / kSlots & 1u))) break;
+          if (j < jb && !(ok = wait_warp(&r_full[u % kSlots], u / kSlots & 1u))) break;
+          if (j > ja && !(ok = wait_warp(&r_full[(u - 1) % kSlots], (u - 1) / kSlots & 1u))) break;
           ptx::tc_fence_after();
           if (j > lo0 && j <= hi0 && !(ok = issue_pv(0, u - 1, j == lo0 + 1))) break;
           if (j >= lo0 && j < hi0) issue_s(0);
           if (j > lo1 && j <= hi1 && !(ok = issue_pv(1, u - 1, j == lo1 + 1))) break;
           if (j >= lo1 && j < hi1) issue_s(1);
           // K_j is free once both tiles' S are done, V_{j-1} once both P V are
-          if (j < jb) ptx::mma_commit(&r_empty[u % kSlots]);
-          if (j > ja) ptx::mma_commit(&r_empty[(u - 1) % kSlots]);
+          if (lead) {
+            if (j < jb) ptx::mma_commit(&r_empty[u % kSlots]);
+            if (j > ja) ptx::mma_commit(&r_empty[(u - 1) % kSlots]);
+          }
+          __syncwarp();
         }
         if (!ok) break;
         u -= 2;                                // (the step more had no block)
-        if (lo0 < hi0) ptx::mma_commit(&o_full[0]);
-        if (lo1 < hi1) ptx::mma_commit(&o_full[1]);
-        more = w.next_item(a);
+        if (lead) {
+          if (lo0 < hi0) ptx::mma_commit(&o_full[0]);
+          if (lo1 < hi1) ptx::mma_commit(&o_full[1]);
+        }
+        ww.next(a, lane);
       }
-      if (any) {
+      if (any && lead) {
         ptx::mma_commit(mma_done);
         W.drain(mma_done, 0, kDrainNs);
       }
