@@ -35,13 +35,7 @@ __device__ __forceinline__ float ex2_from(float x, float ref) {
   return x == -INFINITY ? 0.f : ptx::ex2_approx(x - ref);
 }
 
-// Two e4m3 codes (the low 16 bits) as a pair of f16: exact.
-__device__ __forceinline__ uint32_t f16x2_of_e4m3(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 x;\n\tcvt.u16.u32 x, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\t}" : "=r"(r) : "r"(codes));
-  return r;
-}
-// Four of them.
+// Four e4m3 codes as two pairs of f16: exact.
 __device__ __forceinline__ void f16x4_of_e4m3(uint32_t codes, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 x, y;\n\tmov.b32 {x, y}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, x;\n\tcvt.rn.f16x2.e4m3x2 %1, y;\n\t}"
       : "=r"(lo), "=r"(hi)

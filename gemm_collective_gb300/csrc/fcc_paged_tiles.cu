@@ -734,8 +734,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
       uint32_t u = 0, blk = 0;
       bool ok = true;
       auto wait_slot = [&]() -> bool { return wait_warp(&r_empty[u % kSlots], ((u / kSlots) & 1u) ^ 1u); };
-      // (called once the block's key slot is free: the products of the block that had
-      // these constants four blocks ago were issued before the slot was handed back)
       // What the softmax warps are told of the block (called once the block's slot is
       // free: the products of the block that had these constants four blocks ago were
       // issued before the slot was handed back).  e4m3: returns this position's factor.
@@ -1045,14 +1043,16 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           tmem_ld_wait_regs(x);
           exponentials(x, k);
         }
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&p_full[t]);
+        // (before P is handed over: nothing that this tile does later holds back the block
+        // that has these constants next)
         if constexpr (E4M3) {
           const uint4 wk = *reinterpret_cast<const uint4*>(cc.wide[0]), wv = *reinterpret_cast<const uint4*>(cc.wide[1]);
           wide |= wk.x | wk.y | wk.z | wk.w | wv.x | wv.y | wv.z | wv.w;
         }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&p_full[t]);
         ++n;
       }
       if (!ok) break;
