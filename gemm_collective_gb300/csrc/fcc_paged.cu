@@ -159,7 +159,8 @@ struct Walk {
     items = a.R * a.pool.H * tiles;
     seen = max(0, q.L - q.n - a.window + 1);
     first = seen & ~15;
-    nk = q.ok ? static_cast<int>((static_cast<long long>(q.L) - first + kUnit - 1) / kUnit) : 1;
+    const int L = min(q.L, a.held);
+    nk = q.ok && L > first ? static_cast<int>((static_cast<long long>(L) - first + kUnit - 1) / kUnit) : 1;
     return static_cast<long long>(items) * nk;
   }
   __device__ __forceinline__ void take(const PagedArgs& a) {
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   long long mine = 0;
   for (int b = b_first; b < b_last; ++b) {
     mine += w.measure(a, b);
-    if (blockIdx.x == 0 && !w.q.ok) record_invalid(a.status);
+    if (blockIdx.x == 0 && bad_sequence(a, w.q)) record_invalid(a.status);
   }
   long long upto = mine;
 #pragma unroll
@@ -889,6 +890,9 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   for (int64_t ld : {ldq, ldo})
     if (ld < width || ld % 8 != 0 || ld > INT_MAX) return FCC_ERR_INVALID;
   if (!(scale >= 0.f) || std::isinf(scale) || window < 0) return FCC_ERR_INVALID;
+  a.scale_log2 = static_cast<float>((scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->d))) *
+                                    1.4426950408889634);
+  if (std::isinf(a.scale_log2)) return FCC_ERR_INVALID;
   for (fcc_dtype t : {in, out})
     if (t != FCC_BF16 && t != FCC_F16 && t != FCC_F32) return FCC_ERR_INVALID;
   if (described != FCC_OK) return described;
@@ -926,9 +930,8 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   a.Hq = Hq;
   while ((1 << a.g_shift) < a.G) ++a.g_shift;
   a.g_mul = static_cast<uint32_t>(((uint64_t{1} << (31 + a.g_shift)) + a.G - 1) / a.G);
+  a.held = static_cast<int>(std::min<int64_t>(batch->max_pages << a.pool.log2P, INT_MAX));
   a.window = window == 0 ? INT_MAX : static_cast<int>(std::min<int64_t>(window, INT_MAX));
-  a.scale_log2 = static_cast<float>((scale > 0.f ? static_cast<double>(scale) : 1.0 / std::sqrt(static_cast<double>(cache->d))) *
-                                    1.4426950408889634);
   a.ws = static_cast<char*>(ws);
   const cudaError_t e = form == 1   ? launch_few<1>(a, e4m3, ctas, st)
                         : form == 2 ? launch_few<2>(a, e4m3, ctas, st)

@@ -15,6 +15,7 @@ struct PagedArgs {
   int64_t ldq, ldo;
   int R, Hq, G;
   int window;                  // INT_MAX: none
+  int held;                    // positions that max_pages pages hold: no work for others
   float scale_log2;            // scale * log2(e)
   int* status;
   char* ws;
@@ -27,6 +28,11 @@ struct PagedArgs {
     return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(x)) * g_mul) >> (31 + g_shift));
   }
 };
+
+// A sequence that needs a page past its table's end, or that is not valid.
+__device__ __forceinline__ bool bad_sequence(const PagedArgs& a, const Seq& q) {
+  return !q.ok || (q.n > 0 && q.L > a.held);
+}
 
 constexpr float kLn2 = 0.6931471805599453f;
 

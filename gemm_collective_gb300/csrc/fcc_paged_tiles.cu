@@ -171,7 +171,8 @@ struct Range {
 __device__ __forceinline__ Range blocks_of(const PagedArgs& a, const Seq& q, int first, int last) {
   if (!q.ok) return Range{0, 1};               // (one, of which nothing is seen)
   const int p0 = q.L - q.n + a.by_g(first), p1 = q.L - q.n + a.by_g(last);
-  return Range{max(0, p0 - a.window + 1) / kBlock, p1 / kBlock + 1};
+  const int j0 = max(0, p0 - a.window + 1) / kBlock;
+  return Range{j0, max(j0, min(p1, a.held - 1) / kBlock) + 1};
 }
 __device__ __forceinline__ Range pair_blocks(const PagedArgs& a, const Seq& q, int pair) {
   const int first = pair * kPairRows;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     long long n = 0;
     if (b < a.step.B) {
       q = load_seq(a.step, b);
-      if (!q.ok) record_invalid(a.status);
+      if (bad_sequence(a, q)) record_invalid(a.status);
       np = pairs_of(a, q);
       if (np <= kFewPairs)
         for (int p = 0; p < np; ++p) {

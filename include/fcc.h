@@ -511,7 +511,7 @@ fcc_status fcc_cache_gather(int R, const fcc_cache *cache, const fcc_batch *batc
  * values hold.  Q[r], O[r]: [T, Hq, d] bf16, rows ldq / ldo elements apart (0:
  * Hq * d; multiples of 8): O[r] is the A of fcc_gemv_ar or fcc_gemm_ar for
  * the output projection.  lse: NULL, or R arrays [T, Hq] f32.  scale: 0 means
- * 1 / sqrt(d), otherwise finite and positive.  Hq % H == 0, Hq <= 1024.
+ * 1 / sqrt(d), otherwise positive and, times log2(e), finite.  Hq % H == 0, Hq <= 1024.
  * Scores, maxima, sums and O's accumulators are f32; the probabilities enter the
  * product with V in 16 bits (bf16; f16 where the cache is e4m3), relative to a running
  * maximum.  Repeatable (a fixed order of summation).  Powers of an e4m3 cache are read

@@ -160,3 +160,9 @@ def test_refusals(fcc):
     assert fcc.fcc_launch_count() == n0
     with pytest.raises(fcc.FccError):  # a cache described for fewer ranks than the call's
         fcc.fcc_cache_append(3, [16] * 3, [16] * 3, _cache(fcc), _batch(fcc))
+
+
+def test_scales_whose_exponents_overflow_are_refused(fcc):
+    # scale * log2(e) is what a score is multiplied by; FLT_MAX / log2(e) is 2.3587e38
+    for scale in (2.36e38, 3.4e38):
+        assert _calls(fcc, scale=scale, which=("attention",)) == [fcc.FCC_ERR_INVALID]

@@ -340,6 +340,29 @@ def test_sequences_that_are_not_valid(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("more", [0, 3, 60])
+def test_lengths_far_past_the_table(dtype, more):
+    """All that the table's pages hold is seen (no time is spent on the rest), with a window nothing."""
+    for window in (0, 100):
+        s = Step([(1 + more, 80), (2 + more, 160), (1 + more, 70)], dtype=dtype, P=16)
+        s.table, s.max_pages = s.table[:, :10].contiguous(), 10   # the second sequence's 160 positions, exactly
+        s.len = dev([80, 2**31 - 1, 70])
+        Q = queries(s, 4)
+        O, lse = attend(s, 4, Q, window=window)
+        assert fcc.fcc_stream_status() == fcc.FCC_ERR_INVALID and fcc.fcc_stream_status() == fcc.FCC_OK
+        a, b = int(s.start_np[1]), int(s.start_np[2])
+        if window:
+            assert bool((O[0][a:b] == 0).all()) and bool((lse[0][a:b] == -torch.inf).all())
+            O[0][a:b], lse[0][a:b] = 7.0, 7.0
+            s.seqs[1] = (0, 0)
+        else:                                             # each of its rows is the newest of 160 positions
+            s.seqs = [s.seqs[0]] + [(1, 160)] * (b - a) + [s.seqs[2]]
+            s.start_np = np.concatenate([[0], np.arange(a, b + 1), [s.T]])
+            s.table_np = s.table_np[[0] + [1] * (b - a) + [2]]
+        check(s, 4, Q, O, lse, 128 ** -0.5, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 @pytest.mark.parametrize("case,G", [([(1, 300), (1, 50)], 4), ([(100, 300), (1, 50)], 4)])
 def test_strides_streams_lse_and_repeats(dtype, case, G):
     s = Step(case, dtype=dtype, R=2, behind=3)
