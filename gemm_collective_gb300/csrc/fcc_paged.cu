@@ -43,8 +43,9 @@ namespace {
 
 // Rows to a sequence and key/value head up to which items of 16 rows are faster than
 // tiles of 128, although an item reads the cache for every 16 rows: 40 sequences of 6000
-// positions, 8 heads take 155 us by items against 209 by tiles with 16 rows in bf16, 300
-// against 210 with 24; e4m3 202 against 298 with 24 and 32 rows, 293 against 298 with 40.
+// positions, 8 heads take 155 us by items with 16 rows in bf16 and 300 with 24, and 202 by
+// tiles with any number up to 128; e4m3 202 by items with 24 and 32 rows, 293 with 40, and
+// 261 by tiles.
 constexpr int kFewRowsBf16 = 16, kFewRowsE4m3 = 32;
 constexpr float kRaise = 8.f;                  // the reference is raised past this (log2 units)
 

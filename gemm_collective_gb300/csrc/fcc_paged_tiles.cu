@@ -9,7 +9,7 @@
 // equal runs as there are CTAs, one to an SM: causal, windowed and ragged steps load all
 // SMs alike, and a few rows over a long context are spread over all of them.  (Without
 // the three, the CTAs with a causal prompt's many short items came last: 1.60 against
-// 1.05 ms for 8192 rows of 64 heads.)  What a cut leaves of an item are partial sums, at
+// 1.05 ms for 8192 rows of 64 heads, which take 0.86 now.)  What a cut leaves of an item are partial sums, at
 // most two from a CTA, added in order by join_kernel.
 //
 // Within an item, for tile t and block j (all f32 in TMEM):
@@ -28,12 +28,15 @@
 // largest, 2^A of the keys and 2^B of the values, of each 32 positions; those enter at
 // the exponent (see fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
 //
-// What bounds it: 2048 rows of 32 heads over 32768 positions take 823 us in bf16
-// (1294 TFLOP/s, 0.66 of the measured burst peak), 1.9 us a block and pair.  A
-// 128 x 128 x 16 product alone takes 64 clocks, 2048 for a block; here each takes about
-// 100, because the operands of S fill shared memory's 128 bytes a clock by themselves
-// and the next blocks' TMA writes come on top.  e4m3 (1067 us) waits for its loaders'
-// conversions and the maximum that f16 needs before the exponentials.
+// What bounds it: 2048 rows of 32 heads over 32768 positions take 718 us in bf16
+// (1483 TFLOP/s, 0.75 of the measured burst peak), 1.7 us a block and pair.  A
+// 128 x 128 x 16 product alone takes 64 clocks, 2048 for a block and pair: the tensor
+// pipe is busy 61 % of the time, the schedulers issue in 45 % and the exponentials'
+// unit works in 31 %.  No unit is full: the rest is the way from the last score to the
+// first P V and back, of which two tiles cover one another's only in part, and shared
+// memory, which the operands of S fill by themselves while they run.  e4m3 (1035 us)
+// waits for its loaders' conversions and the maximum that f16 needs before the
+// exponentials.
 // Shared memory (128-byte swizzle): Q_t and four slots of [128 rows][D] 16-bit
 // values in atoms of 64 columns, K_0, V_0, K_1, V_1, ... in the slots; K is the
 // K-major and V the MN-major B operand of the same layout.
