@@ -34,9 +34,9 @@
 // pipe is busy 61 % of the time, the schedulers issue in 45 % and the exponentials'
 // unit works in 31 %.  No unit is full: the rest is the way from the last score to the
 // first P V and back, of which two tiles cover one another's only in part, and shared
-// memory, which the operands of S fill by themselves while they run.  e4m3 (1035 us)
-// waits for its loaders' conversions and the maximum that f16 needs before the
-// exponentials.
+// memory, which the operands of S fill by themselves while they run.  e4m3 (1005 us)
+// waits for its loaders, busy 0.85 of the time with conversions and addresses, and for
+// the maximum that f16 needs before the exponentials.
 // Shared memory (128-byte swizzle): Q_t and four slots of [128 rows][D] 16-bit
 // values in atoms of 64 columns, K_0, V_0, K_1, V_1, ... in the slots; K is the
 // K-major and V the MN-major B operand of the same layout.
@@ -707,30 +707,54 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
       ww.begin(a, *run, lane);
       int j = w.ja;                            // the block that is looked up next
       int page = -1, in_page = 0, r = 0, h = 0;  // this lane's position in the block looked up last
-      bool have = false;
-      auto look_up = [&]() {
-        have = w.more;
+      bool have = false, needed = false, left = w.more;
+      // The item: its rank, head, end, table and positions.  Those in (see_from, see_to]
+      // are seen by some row of it: others need no page.
+      int item_r = 0, item_h = 0, item_end = 0, see_from = 0, see_to = 0;
+      uint32_t positions = 0;
+      const int* table = nullptr;
+      auto new_item = [&]() {
+        j = w.ja;
+        item_r = w.rank(a);
+        item_h = w.head(a);
+        item_end = w.jb;
+        positions = w.q.ok ? w.q.L : 0;
+        table = a.step.table + w.b * a.step.max_pages;
+        const int row0 = w.pair * kPairRows, first = w.q.L - w.q.n;
+        see_from = max(-1, first + a.by_g(row0) - a.window);
+        see_to = first + a.by_g(min(w.q.n * a.G - row0, kPairRows) + row0 - 1);
+      };
+      // Asks for the page of the next block's position; answer() takes what has come.
+      auto ask = [&]() {
         page = -1;
+        needed = false;
+        have = left;
         if (!have) return;
-        const long long pos = static_cast<long long>(j) * kBlock + 32 * wl + lane;
-        r = w.rank(a);
-        h = w.head(a);
-        if (w.q.ok && pos < w.q.L) {
-          page = page_of(a.step, a.pool.pages, w.b, static_cast<int>(pos >> a.pool.log2P));
+        const uint32_t pos = static_cast<uint32_t>(j) * kBlock + 32 * wl + lane;
+        r = item_r;
+        h = item_h;
+        if (pos < positions) {
+          const uint32_t idx = pos >> a.pool.log2P;
+          if (idx < static_cast<uint32_t>(a.step.max_pages)) page = __ldg(table + idx);
           in_page = static_cast<int>(pos) & ((1 << a.pool.log2P) - 1);
-          if (page < 0) {
-            // (positions that no row sees need no page: before every row's window, or
-            // behind the last row)
-            const int first = w.q.L - w.q.n + a.by_g(w.pair * kPairRows);
-            const int last = w.q.L - w.q.n + a.by_g(min(w.q.n * a.G - w.pair * kPairRows, kPairRows) + w.pair * kPairRows - 1);
-            if (pos <= last && pos > static_cast<long long>(first) - a.window) record_invalid(a.status);
-          }
+          needed = static_cast<int>(pos) <= see_to && static_cast<int>(pos) > see_from;
         }
-        if (++j == w.jb) {
+        if (++j == item_end) {
           ww.next(a, lane);
-          j = w.ja;
+          left = w.more;
+          if (left) new_item();
         }
       };
+      auto answer = [&]() {
+        if (page >= 0 && page < a.pool.pages) return;
+        page = -1;
+        if (needed) record_invalid(a.status);
+      };
+      auto look_up = [&]() {
+        ask();
+        answer();
+      };
+      if (left) new_item();
       // Number of this lane's position's row in its rank's pools, -1 for none.
       auto row_of = [&]() -> int64_t {
         return page < 0 ? -1 : ((static_cast<int64_t>(page) * a.pool.H + h) << a.pool.log2P) + in_page;
@@ -767,7 +791,6 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         ++blk;
         return factor;
       };
-      look_up();
       if constexpr (E4M3) {
         // Eight lanes hold four 16-byte pieces of one 64-column atom of two rows next to
         // each other: their f16 stores fall into different banks.
@@ -779,24 +802,40 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         u = kind;
         auto fetch = [&](int64_t row, int r) {
           const char* pool = (kind == 0 ? a.pool.K[r] : a.pool.V[r]) + piece * 16;
+          if (a.pool.log2P >= 5 && __all_sync(0xffffffffu, row >= 0)) {   // one piece of a page
+            pool += (__shfl_sync(0xffffffffu, row, 0) + sub) * kRow;
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const int64_t src = __shfl_sync(0xffffffffu, row, i * kAtOnce + sub);
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (src >= 0) x[i] = *reinterpret_cast<const uint4*>(pool + src * kRow);
+            for (int i = 0; i < kN; ++i) x[i] = *reinterpret_cast<const uint4*>(pool + i * kAtOnce * kRow);
+          } else {
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const int64_t src = __shfl_sync(0xffffffffu, row, i * kAtOnce + sub);
+              x[i] = make_uint4(0, 0, 0, 0);
+              if (src >= 0) x[i] = *reinterpret_cast<const uint4*>(pool + src * kRow);
+            }
           }
           if (row >= 0) byte = (kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r])[row];
         };
-        // A block is looked up two blocks ahead and brought into the L2 one block ahead of
-        // its loads: they would wait for DRAM between one block's conversion and the next.
+        // (Pages taken as soon as they were asked for, an address for each load and the
+        // item's fields from shared memory each time: 1034 instead of 1005 us for the chunk.)
+        // A block's pages are asked for two blocks ahead; what has come a block later is
+        // brought into the L2, before that block's own loads: they would wait for DRAM
+        // between one block's conversion and the next.
+        look_up();
         int64_t row = row_of();
         bool full = have;
         if (full) fetch(row, r);
-        look_up();
+        ask();
         while (full) {
           const bool next = have;
-          const int next_r = r, next_h = h, next_page = page, next_in = in_page;
-          look_up();
+          answer();
+          const int64_t next_row = row_of();
+          const int next_r = r;
+          if (next_row >= 0) {
+            ptx::prefetch_l2((kind == 0 ? a.pool.K[r] : a.pool.V[r]) + next_row * kRow);
+            ptx::prefetch_l2((kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r]) + next_row);
+          }
+          ask();
           if (!(ok = wait_slot())) break;
           const uint32_t power = constants(row, byte);
           uint8_t* dst = sR + (u % kSlots) * kTile;
@@ -819,19 +858,15 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           if (lane == 0) ptx::mbar_arrive(&r_full[u % kSlots]);
           u += 2;
           full = next;
-          row = next_page < 0 ? -1 : ((static_cast<int64_t>(next_page) * a.pool.H + next_h) << a.pool.log2P) + next_in;
+          row = next_row;
           if (full) fetch(row, next_r);
-          if (page >= 0) {
-            const int64_t far = row_of();
-            ptx::prefetch_l2((kind == 0 ? a.pool.K[r] : a.pool.V[r]) + far * kRow);
-            ptx::prefetch_l2((kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r]) + far);
-          }
         }
       } else {
         // A warp's 32 positions come by TMA, a box of a page's rows and 64 columns at a
         // time, if they are all there (kBoxes: pages of 16 rows and more); otherwise,
         // at a sequence's end, through registers, with zeros for what is not.
         const int box = min(32, 1 << a.pool.log2P);
+        look_up();
         while (have) {
           const int64_t row = row_of();
           const int page_now = page, in_page_now = in_page, rr = r, hh = h;
