@@ -44,7 +44,7 @@ namespace {
 // Rows to a sequence and key/value head up to which items of 16 rows are faster than
 // tiles of 128, although an item reads the cache for every 16 rows: 40 sequences of 6000
 // positions, 8 heads take 155 us by items with 16 rows in bf16 and 300 with 24, and 202 by
-// tiles with any number up to 128; e4m3 202 by items with 24 and 32 rows, 293 with 40, and
+// tiles with any number up to 128; e4m3 192 by items with 24 and 32 rows, 293 with 40, and
 // 261 by tiles.
 constexpr int kFewRowsBf16 = 16, kFewRowsE4m3 = 32;
 constexpr float kRaise = 8.f;                  // the reference is raised past this (log2 units)
@@ -307,9 +307,25 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   int page[kPer], in_page[kPer] = {}, pool_r = 0, pool_h = 0;
   const int* table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;   // of lw's sequence
   uint32_t pos = static_cast<uint32_t>(lw.first) + static_cast<uint32_t>(lw.k) * kUnit + warp * kTok + lane;   // of the next slice's
+  // A page's number is checked where it was asked for, which waits for it, or with 16 rows
+  // to an item of e4m3 a slice later (40 x 2 tokens 104 instead of 110 us, 40 x 1-5 103
+  // instead of 105).  Where DRAM is the bound, later was slower: 1 x 1000003 e4m3 309
+  // instead of 304 us, 64 x 8192 bf16 201.2 instead of 199.7, 40 x 2 bf16 154.7 instead
+  // of 153.7.
+  constexpr bool kLater = E4M3 && NQ > 1;
+  bool asked[kPer];
+  auto check = [&](int i) {
+    if (static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.pool.pages)) {
+      page[i] = -1;
+      if (asked[i]) record_invalid(a.status);
+    }
+  };
   auto look_up = [&]() {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) page[i] = -1;
+    for (int i = 0; i < kPer; ++i) {
+      page[i] = -1;
+      asked[i] = false;
+    }
     if (!more) return;
     pool_r = lw.r;
     pool_h = lw.h;
@@ -320,10 +336,8 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
         const uint32_t idx = p >> a.pool.log2P;
         if (idx < static_cast<uint32_t>(a.step.max_pages)) page[i] = __ldg(table + idx);
         in_page[i] = p & ((1u << a.pool.log2P) - 1);
-        if (static_cast<uint32_t>(page[i]) >= static_cast<uint32_t>(a.pool.pages)) {
-          page[i] = -1;
-          record_invalid(a.status);
-        }
+        asked[i] = true;
+        if constexpr (!kLater) check(i);
       }
     }
     pos += kUnit;
@@ -338,6 +352,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
     uint32_t any = 0, run = 0xffffffffu;       // run: each 16 positions lie one after another in a page
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
+      if constexpr (kLater) check(i);
       s.there[i] = __ballot_sync(0xffffffffu, page[i] >= 0);
       any |= s.there[i];
       const int page0 = __shfl_sync(0xffffffffu, page[i], lane & 16), in_page0 = __shfl_sync(0xffffffffu, in_page[i], lane & 16);
