@@ -138,7 +138,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // A walk over a CTA's run of units: item after item, each from unit k to unit end.
-template <int kRows, int kUnit>
+// AGAIN: over whole items, every gridDim.x-th one, those that have rows to be computed again.
+template <int kRows, int kUnit, bool AGAIN>
 struct Walk {
   int b, item, k, end;
   Seq q;
@@ -176,7 +177,31 @@ struct Walk {
     whole_from = hi - a.window;
     whole_to = q.ok ? q.L - q.n + a.by_g(row0) : -1;
   }
+  // The item's rows that are to be computed again.
+  __device__ __forceinline__ uint32_t marked(const PagedArgs& a) const {
+    const int rh = item / tiles, row = (item - rh * tiles) * kRows;
+    const uint32_t m = a.again.bits(rh, q.s * a.G + row);
+    return m & ((1u << min(kRows, q.n * a.G - row)) - 1);
+  }
+  __device__ __forceinline__ bool find_marked(const PagedArgs& a) {
+    for (;; item += gridDim.x) {
+      while (item >= items) {
+        item -= items;
+        if (b + 1 >= a.step.B) return false;
+        measure(a, b + 1);
+      }
+      if (marked(a) != 0) break;
+    }
+    k = 0;
+    left = nk;
+    take(a);
+    return true;
+  }
   __device__ __forceinline__ bool next_item(const PagedArgs& a) {
+    if constexpr (AGAIN) {
+      item += gridDim.x;
+      return find_marked(a);
+    }
     if (left <= 0) return false;
     if (++item == items) {
       item = 0;
@@ -203,10 +228,10 @@ struct Sums {
   }
 };
 
-// Stores columns 16 j .. 16 j + 15 of rows row0 .. row0 + 7 of a sequence.
+// Stores columns 16 j .. 16 j + 15 of rows row0 .. row0 + 7 of a sequence, those whose bits are set.
 template <int D, bool E4M3>
 __device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int r, int h, int row0, int j, int lane,
-                                           const Sums& m) {
+                                           const Sums& m, uint32_t rows = 0xff) {
   const int g = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -221,7 +246,7 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int
       y = g & 1 ? y : other;
     }
     const int rho = row0 + 2 * c + i;
-    if (rho >= q.n * a.G) continue;
+    if (rho >= q.n * a.G || !(rows >> (2 * c + i) & 1)) continue;
     const int t = a.by_g(rho), head = h * a.G + (rho - t * a.G);
     const int64_t token = static_cast<int64_t>(q.s) + t;
     *reinterpret_cast<uint32_t*>(a.O[r] + (token * a.ldo + static_cast<int64_t>(head) * D + 16 * j + col) * 2) = ptx::pack_bf16x2(x, y);
@@ -230,7 +255,9 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int
   }
 }
 
-template <int D, bool E4M3, int NQ>
+// AGAIN: the rows that tiles of 128 left (Again), an item to a CTA from its first position
+// to its last: where they are summed does not depend on which others there are.
+template <int D, bool E4M3, int NQ, bool AGAIN>
 __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_kernel(const __grid_constant__ PagedArgs a) {
   using F = Few<D, E4M3, NQ>;
   constexpr int kTok = F::kTok, kUnit = F::kUnit, kPer = F::kPer, kWarps = F::kWarps, kHalf = F::kHalf, kStages = F::kStages;
@@ -248,51 +275,60 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   ptx::griddep_launch_dependents();
 
   // ---------------------------------------------- this CTA's run of units
-  Walk<F::kRows, kUnit> w;
-  const int per = (a.step.B + kWarps * 32 - 1) / (kWarps * 32);
-  const int b_first = min(a.step.B, static_cast<int>(threadIdx.x) * per), b_last = min(a.step.B, b_first + per);
-  long long mine = 0;
-  for (int b = b_first; b < b_last; ++b) {
-    mine += w.measure(a, b);
-    if (blockIdx.x == 0 && bad_sequence(a, w.q)) record_invalid(a.status);
-  }
-  long long upto = mine;
-#pragma unroll
-  for (int s = 1; s < 32; s *= 2) {
-    const long long v = __shfl_up_sync(0xffffffffu, upto, s);
-    if (lane >= s) upto += v;
-  }
-  if (lane == 31) s_scan[warp] = upto;
-  __syncthreads();
-  long long total = 0, from = upto - mine;
-#pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) from += s_scan[i];
-    total += s_scan[i];
-  }
-  const long long ctas = min(static_cast<long long>(gridDim.x), total);
+  Walk<F::kRows, kUnit, AGAIN> w;
+  long long total = 0, ctas = 0, u0 = 0;
   Header* const headers = reinterpret_cast<Header*>(a.ws);
-  if (threadIdx.x == 0) headers[blockIdx.x].parts = 0;
-  if (blockIdx.x >= ctas) return;
-  const long long u0 = blockIdx.x * total / ctas, u1 = (blockIdx.x + 1) * total / ctas;
-  if (u0 >= from && u0 < from + mine) {
-    long long off = u0 - from;
+  if constexpr (AGAIN) {
+    if (*a.again.any == 0) return;
+    w.measure(a, 0);
+    w.item = blockIdx.x;
+    if (!w.find_marked(a)) return;
+  } else {
+    const int per = (a.step.B + kWarps * 32 - 1) / (kWarps * 32);
+    const int b_first = min(a.step.B, static_cast<int>(threadIdx.x) * per), b_last = min(a.step.B, b_first + per);
+    long long mine = 0;
     for (int b = b_first; b < b_last; ++b) {
-      const long long n = w.measure(a, b);
-      if (off < n) {
-        s_b = b;
-        s_off = off;
-        break;
-      }
-      off -= n;
+      mine += w.measure(a, b);
+      if (blockIdx.x == 0 && bad_sequence(a, w.q)) record_invalid(a.status);
     }
+    long long upto = mine;
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, upto, s);
+      if (lane >= s) upto += v;
+    }
+    if (lane == 31) s_scan[warp] = upto;
+    __syncthreads();
+    long long from = upto - mine;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) from += s_scan[i];
+      total += s_scan[i];
+    }
+    ctas = min(static_cast<long long>(gridDim.x), total);
+    if (threadIdx.x == 0) headers[blockIdx.x].parts = 0;
+    if (blockIdx.x >= ctas) return;
+    u0 = blockIdx.x * total / ctas;
+    const long long u1 = (blockIdx.x + 1) * total / ctas;
+    if (u0 >= from && u0 < from + mine) {
+      long long off = u0 - from;
+      for (int b = b_first; b < b_last; ++b) {
+        const long long n = w.measure(a, b);
+        if (off < n) {
+          s_b = b;
+          s_off = off;
+          break;
+        }
+        off -= n;
+      }
+    }
+    __syncthreads();
+    w.measure(a, s_b);
+    w.item = static_cast<int>(s_off / w.nk);
+    w.k = static_cast<int>(s_off % w.nk);
+    w.left = u1 - u0;
+    w.take(a);
   }
-  __syncthreads();
-  w.measure(a, s_b);
-  w.item = static_cast<int>(s_off / w.nk);
-  w.k = static_cast<int>(s_off % w.nk);
-  w.left = u1 - u0;
-  w.take(a);
 
   // ------------------------------------------------------------- loading
   // The loads' own walk runs kStages - 1 slices ahead of the products, and the
@@ -302,7 +338,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   struct Slice {
     uint32_t there[kPer];                      // which positions the pages hold
   };
-  Walk<F::kRows, kUnit> lw = w;
+  Walk<F::kRows, kUnit, AGAIN> lw = w;
   bool more = true;
   int page[kPer], in_page[kPer] = {}, pool_r = 0, pool_h = 0;
   const int* table = a.step.table + static_cast<int64_t>(lw.b) * a.step.max_pages;   // of lw's sequence
@@ -590,8 +626,10 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
             for (int i = 0; i < 4; ++i) o[j][nq][i] *= f[i & 1];
         }
       }
-      bool plain = true;
-      if (!whole) {
+      // (e4m3 rows that are computed again saw powers far apart: their sums are f32 throughout)
+      constexpr bool kExact = AGAIN && E4M3;
+      bool plain = !kExact;
+      if (!kExact && !whole) {
         // A value that is not finite must not reach rows that do not see it through
         // a product with their p = 0.
         bool odd = false;
@@ -701,7 +739,8 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
           s_l[warp][8 * nq + 2 * c + i] = l[nq][i];
         }
       }
-    const bool complete = k0 == 0 && w.end == w.nk;
+    const bool complete = AGAIN || (k0 == 0 && w.end == w.nk);
+    const uint32_t wanted = AGAIN ? w.marked(a) : 0xffffffffu;
     // (the slice just used: its place is loaded again by the next item's first step)
     const int used = slot == 0 ? kStages - 1 : slot - 1;
     float4* const mine_o = reinterpret_cast<float4*>(ring + used * F::kStage);
@@ -738,7 +777,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
           m.add(reinterpret_cast<const float4*>(smem + (v * kStages + used) * F::kStage)[f4 * 32 + lane], f);
         }
         if (complete) {
-          store_rows<D, E4M3>(a, w.q, w.r, w.h, w.row0 + row - 2 * c, j, lane, m);
+          store_rows<D, E4M3>(a, w.q, w.r, w.h, w.row0 + row - 2 * c, j, lane, m, wanted >> (row - 2 * c));
         } else {
           if (j == 0 && g == 0) {
 #pragma unroll
@@ -819,10 +858,10 @@ template <int D, bool E4M3, int NQ>
 cudaError_t launch_few(const PagedArgs& a, int ctas, cudaStream_t st) {
   using F = Few<D, E4M3, NQ>;
   static bool attr_set[64] = {};
-  cudaError_t e = smem_attr_once(attr_set, few_rows_kernel<D, E4M3, NQ>, F::kSmem);
+  cudaError_t e = smem_attr_once(attr_set, few_rows_kernel<D, E4M3, NQ, false>, F::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned grid = static_cast<unsigned>(ctas);
-  if ((e = launch_pdl(few_rows_kernel<D, E4M3, NQ>, dim3(grid), dim3(F::kWarps * 32), F::kSmem, st, 1u, a)) != cudaSuccess)
+  if ((e = launch_pdl(few_rows_kernel<D, E4M3, NQ, false>, dim3(grid), dim3(F::kWarps * 32), F::kSmem, st, 1u, a)) != cudaSuccess)
     return e;
   return launch_pdl(combine_kernel<D, E4M3, NQ>, dim3(grid, NQ), dim3(D * 2), 0, st, 1u, a);
 }
@@ -831,6 +870,20 @@ template <int NQ>
 cudaError_t launch_few(const PagedArgs& a, bool e4m3, int ctas, cudaStream_t st) {
   return a.pool.d == 128 ? (e4m3 ? launch_few<128, true, NQ>(a, ctas, st) : launch_few<128, false, NQ>(a, ctas, st))
                          : (e4m3 ? launch_few<64, true, NQ>(a, ctas, st) : launch_few<64, false, NQ>(a, ctas, st));
+}
+
+// After launch_tiles: the rows that it left.
+template <int D, bool E4M3>
+cudaError_t launch_again(const PagedArgs& a, int ctas, cudaStream_t st) {
+  using F = Few<D, E4M3, 2>;
+  static bool attr_set[64] = {};
+  const cudaError_t e = smem_attr_once(attr_set, few_rows_kernel<D, E4M3, 2, true>, F::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(few_rows_kernel<D, E4M3, 2, true>, dim3(static_cast<unsigned>(ctas)), dim3(F::kWarps * 32), F::kSmem, st, 1u, a);
+}
+cudaError_t launch_again(const PagedArgs& a, bool e4m3, int ctas, cudaStream_t st) {
+  return a.pool.d == 128 ? (e4m3 ? launch_again<128, true>(a, ctas, st) : launch_again<128, false>(a, ctas, st))
+                         : (e4m3 ? launch_again<64, true>(a, ctas, st) : launch_again<64, false>(a, ctas, st));
 }
 
 // The form for a step: NQ tiles of 8 rows to an item, or 0 for tiles of 128 rows on
@@ -854,17 +907,17 @@ int ctas_of(int form, const fcc_opts* o) {
   return o != nullptr && o->max_ctas > 0 ? std::min(ctas, o->max_ctas) : ctas;
 }
 
-size_t form_ws_bytes(int form, int B, int64_t d, int ctas) {
+size_t form_ws_bytes(int form, int R, int64_t T, int B, int G, int H, int64_t d, int ctas) {
   return form != 0 ? header_bytes(ctas) + 2 * static_cast<size_t>(ctas) * part_floats(static_cast<int>(d), form) * sizeof(float)
-                   : tiles_ws_bytes(d, B, ctas);
+                   : tiles_ws_bytes(d, B, ctas, T * G, static_cast<int64_t>(R) * H);
 }
 
 // What a call asks for: enough for either type of cache.
-size_t paged_ws_bytes(int64_t T, int B, int G, int64_t d, const fcc_opts* o) {
+size_t paged_ws_bytes(int R, int64_t T, int B, int G, int H, int64_t d, const fcc_opts* o) {
   size_t most = 0;
   for (bool e4m3 : {false, true}) {
     const int form = form_of(T, B, G, e4m3);
-    most = std::max(most, form_ws_bytes(form, B, d, ctas_of(form, o)));
+    most = std::max(most, form_ws_bytes(form, R, T, B, G, H, d, ctas_of(form, o)));
   }
   return most;
 }
@@ -881,7 +934,7 @@ size_t fcc_paged_attention_workspace_size(int R, int64_t T, int B, int Hq, int H
   if (R < 1 || R > FCC_MAX_RANKS || T < 1 || B < 1 || H < 1 || Hq < H || Hq % H != 0 ||
       (d != 64 && d != 128))
     return 0;
-  return paged_ws_bytes(T, B, Hq / H, d, opts);
+  return paged_ws_bytes(R, T, B, Hq / H, H, d, opts);
 }
 
 fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const fcc_cache* cache,
@@ -932,8 +985,8 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   void* ws = nullptr;
   int sms = 0;
   unsigned long long timeout_ns = 0;
-  const fcc_status s = internal_prepare(opts, paged_ws_bytes(batch->T, batch->B, a.G, cache->d, opts), &ws,
-                                        &a.status, &sms, &timeout_ns);
+  const fcc_status s = internal_prepare(opts, paged_ws_bytes(R, batch->T, batch->B, a.G, cache->H, cache->d, opts),
+                                        &ws, &a.status, &sms, &timeout_ns);
   if (s != FCC_OK) return s;
   for (int r = 0; r < R; ++r) {
     a.Q[r] = static_cast<const char*>(Q[r]);
@@ -949,11 +1002,12 @@ fcc_status fcc_paged_attention(int R, const void* const* Q, int64_t ldq, const f
   a.held = static_cast<int>(std::min<int64_t>(batch->max_pages << a.pool.log2P, INT_MAX));
   a.window = window == 0 ? INT_MAX : static_cast<int>(std::min<int64_t>(window, INT_MAX));
   a.ws = static_cast<char*>(ws);
-  const cudaError_t e = form == 1   ? launch_few<1>(a, e4m3, ctas, st)
-                        : form == 2 ? launch_few<2>(a, e4m3, ctas, st)
-                                    : launch_tiles(a, e4m3, ctas, timeout_ns, st);
+  cudaError_t e = form == 1   ? launch_few<1>(a, e4m3, ctas, st)
+                  : form == 2 ? launch_few<2>(a, e4m3, ctas, st)
+                              : launch_tiles(a, e4m3, ctas, timeout_ns, st);
+  if (form == 0 && e == cudaSuccess) e = launch_again(a, e4m3, ctas_of(2, opts), st);
   if (e != cudaSuccess) return FCC_ERR_CUDA;
-  bump_launch_count(form != 0 ? 2 : 3);
+  bump_launch_count(form != 0 ? 2 : 4);
   return FCC_OK;
 }
 

@@ -6,6 +6,31 @@
 
 namespace fcc {
 
+// Rows that the tiles of 128 cannot give, one bit for each row of a rank's key/value
+// head: because in a product with P = 0 a value that is not finite reaches rows that do
+// not see it, and e4m3 rows that saw powers too far apart.  launch_again's kernel
+// computes them from all their positions.
+struct Again {
+  uint32_t* rows;              // [R * H][words]: bit i of a (rank, head) is row i % G of token i / G
+  int* any;                    // some bit is set
+  int64_t words;
+
+  __host__ __device__ static int64_t words_of(int64_t rows) { return (rows + 31) / 32 + 1; }   // (one for a mask's upper part)
+  __device__ __forceinline__ uint32_t* word(int rh, int row) const { return rows + rh * words + (row >> 5); }
+  // Rows row .. row + 31 whose bits in m are set (m has none behind the last row).
+  __device__ __forceinline__ void mark(int rh, int row, uint32_t m) const {
+    uint32_t* w = word(rh, row);
+    const int shift = row & 31;
+    atomicOr(w, m << shift);
+    if (shift != 0 && m >> (32 - shift) != 0) atomicOr(w + 1, m >> (32 - shift));
+  }
+  // The bits of rows row .. row + 31.
+  __device__ __forceinline__ uint32_t bits(int rh, int row) const {
+    const uint32_t* w = word(rh, row);
+    return __funnelshift_r(w[0], w[1], row & 31);
+  }
+};
+
 struct PagedArgs {
   PoolArgs pool;
   StepArgs step;
@@ -21,6 +46,7 @@ struct PagedArgs {
   char* ws;
   uint32_t g_mul, g_shift;     // rows / G for rows < 2^31: see by_g()
   int boxes;                   // pages come by TMA
+  Again again;                 // tiles only
 
   // x / G by multiplication: g_mul = ceil(2^(31 + g_shift) / G) with 2^(g_shift - 1) < G
   // <= 2^g_shift is exact for x < 2^31.
@@ -59,8 +85,9 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
 }
 
 // Tiles of 128 rows on the tensor cores' own memory (fcc_paged_tiles.cu).
-size_t tiles_ws_bytes(int64_t d, int B, int ctas);
-cudaError_t launch_tiles(const PagedArgs& a, bool e4m3, int ctas, unsigned long long timeout_ns,
+// rows: tokens times G; rank_heads: R * H.  launch_tiles fills a.again.
+size_t tiles_ws_bytes(int64_t d, int B, int ctas, int64_t rows, int64_t rank_heads);
+cudaError_t launch_tiles(PagedArgs& a, bool e4m3, int ctas, unsigned long long timeout_ns,
                          cudaStream_t st);
 
 }  // namespace fcc

@@ -10,7 +10,10 @@
 // SMs alike, and a few rows over a long context are spread over all of them.  (Without
 // the three, the CTAs with a causal prompt's many short items came last: 1.60 against
 // 1.05 ms for 8192 rows of 64 heads, which take 0.86 now.)  What a cut leaves of an item are partial sums, at
-// most two from a CTA, added in order by join_kernel.
+// most two from a CTA, added in order by join_kernel.  Rows that tiles cannot give (Again)
+// are computed behind them by launch_again's kernel, which waits for nothing: inside a
+// tile, where a warp alone needs 0.8 us a position, long rows would let the other warps'
+// waits run out.  The launch costs 2.3 us where no row is marked.
 //
 // Within an item, for tile t and block j (all f32 in TMEM):
 //   S_t = Q_t K_j^T;  P_t = 2^(S_t c - ref), in 16 bits over S_t's first columns;
@@ -138,9 +141,9 @@ struct Header {                                // of the item that a CTA begins 
 };
 
 // Workspace: the plan's totals, the headers, the cost of what is before each sequence,
-// then two partial results for each CTA.
+// two partial results for each CTA, then a bit for every row (see Again).
 struct Layout {
-  size_t headers, units, parts, part_bytes, total;
+  size_t headers, units, parts, part_bytes, again;
 };
 // References, sums, then [D / 4][256] float4.
 template <int D>
@@ -151,12 +154,13 @@ __host__ __device__ inline Layout layout_of(int64_t d, int B, int ctas) {
   l.units = l.headers + static_cast<size_t>(ctas) * sizeof(Header);
   l.parts = (l.units + static_cast<size_t>(B) * 8 + 255) & ~size_t{255};
   l.part_bytes = kPairRows * static_cast<size_t>(d + 2) * 4;
-  l.total = l.parts + 2 * static_cast<size_t>(ctas) * l.part_bytes;
+  l.again = l.parts + 2 * static_cast<size_t>(ctas) * l.part_bytes;
   return l;
 }
 struct Totals {                                // at the workspace's start
   long long cost;                              // of all items
   int ctas;                                    // with work
+  int again;                                   // some row's bit is set (tests read it here, 12 bytes in)
 };
 
 __device__ __forceinline__ int pairs_of(const PagedArgs& a, const Seq& q) {
@@ -248,13 +252,15 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     total += s_scan[i];
   }
   const long long ctas = min(static_cast<long long>(grid), total);
+  const int64_t words = rh * a.again.words;
+  for (int64_t i = threadIdx.x; i < words; i += kPlanThreads) a.again.rows[i] = 0;
   // (from here on units[b] is the cost of what is before sequence b)
   for (int b = b_first; b < b_last; ++b) {
     const long long n = units[b];
     units[b] = from;
     from += n;
   }
-  if (threadIdx.x == 0) *reinterpret_cast<Totals*>(a.ws) = Totals{total, static_cast<int>(ctas)};
+  if (threadIdx.x == 0) *reinterpret_cast<Totals*>(a.ws) = Totals{total, static_cast<int>(ctas), 0};
 }
 
 // Where the run that begins `u` blocks into the list begins; cost0: what is before its
@@ -403,7 +409,7 @@ struct alignas(16) Columns {
 
 // 2^(byte - top) in f16 (both halves).  An e4m3 code (a multiple of 2^-9) times it is
 // exact in f16 down to 2^-15.  A group with powers further apart is `wide`: the rows
-// that met it are computed again one by one.  (Byte 63 holds what is nearly zero on its
+// that met it are computed again (Again).  (Byte 63 holds what is nearly zero on its
 // own, a row of zeros above all: that may vanish.)
 __device__ __forceinline__ uint32_t f16_power(int byte, int top) {
   const int k = byte - top;
@@ -479,55 +485,6 @@ __device__ __forceinline__ float sum2(const uint64_t (&v)[2]) {
 // The place of column group c4 (4 values) of a row in a partial result.
 __device__ __forceinline__ float4* part_at(char* part, int c4, int row) {
   return reinterpret_cast<float4*>(part + kPairRows * 8) + c4 * kPairRows + row;
-}
-
-// One row over positions [from, to], computed again by a warp from the definition:
-// lanes hold D / 32 columns each.  Rows whose sums are not finite come here, because
-// in a product with P = 0 a value that is not finite reaches rows that do not see it,
-// and rows that saw powers too far apart.
-template <int D, bool E4M3>
-__device__ __noinline__ void row_again(const PagedArgs& a, int b, int r, int h, int head, int64_t t, int from, int to, int lane,
-                                       float (&o)[D / 32], float& ref, float& l) {
-  constexpr int N = D / 32;
-  float x[N];
-  const __nv_bfloat16* src = reinterpret_cast<const __nv_bfloat16*>(a.Q[r]) + t * a.ldq + static_cast<int64_t>(head) * D + lane * N;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = __bfloat162float(src[i]);
-    o[i] = 0.f;
-  }
-  ref = -INFINITY;
-  l = 0.f;
-  for (int64_t j = from; j <= to; ++j) {
-    const int page = page_of(a.step, a.pool.pages, b, static_cast<int>(j >> a.pool.log2P));
-    if (page < 0) continue;
-    const int64_t row = ((static_cast<int64_t>(page) * a.pool.H + h) << a.pool.log2P) + (j & ((1 << a.pool.log2P) - 1));
-    float k[N], v[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int64_t at = row * D + lane * N + i;
-      if constexpr (E4M3) {
-        const float fk = __int_as_float(a.pool.Ke[r][row] << 23), fv = __int_as_float(a.pool.Ve[r][row] << 23);
-        k[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(a.pool.K[r][at]), __NV_E4M3))) * fk;
-        v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<uint8_t>(a.pool.V[r][at]), __NV_E4M3))) * fv;
-      } else {
-        k[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.K[r])[at]);
-        v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.pool.V[r])[at]);
-      }
-    }
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s = fmaf(x[i], k[i], s);
-#pragma unroll
-    for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-    s *= a.scale_log2;
-    const float top = fmaxf(ref, s);
-    const float f = ex2_from(ref, top), e = ex2_from(s, top);
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * f + (s == -INFINITY ? 0.f : e * v[i]);
-    ref = top;
-  }
 }
 
 struct PoolMaps {                              // bf16 pools with pages of 16 rows and more
@@ -1098,7 +1055,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
       // The next item's queries: this tile's S are all complete.
       const Walk& cur = ww.old;
       const int64_t o_token = token;
-      const int o_head = head, o_qpos = qpos;
+      const int o_head = head;
       const bool o_live = live;
       ww.next(a, lane);
       more = w.more;
@@ -1166,28 +1123,12 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
                                                             __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
         }
       }
-      for (unsigned m = __ballot_sync(0xffffffffu, odd && o_live); m != 0; m &= m - 1) {
-        const int src = __ffs(m) - 1;
-        const int64_t tok = __shfl_sync(0xffffffffu, o_token, src);
-        const int hd = __shfl_sync(0xffffffffu, o_head, src), p = __shfl_sync(0xffffffffu, o_qpos, src);
-        const int from = static_cast<int>(max(static_cast<long long>(cur.ja) * kBlock, static_cast<long long>(p) - a.window + 1));
-        const int to = static_cast<int>(min(static_cast<long long>(cur.jb) * kBlock - 1, static_cast<long long>(p)));
-        float o[D / 32], ref1, l1;
-        row_again<D, E4M3>(a, cur.b, r, cur.head(a), hd, tok, from, to, lane, o, ref1, l1);
-        const int prow1 = t * kTileRows + quarter * 32 + src;
-        const float inv1 = l1 == 0.f ? 0.f : 1.f / l1;
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-          const int col = lane * (D / 32) + i;
-          if (complete)
-            reinterpret_cast<__nv_bfloat16*>(a.O[r])[tok * a.ldo + static_cast<int64_t>(hd) * D + col] = __float2bfloat16(o[i] * inv1);
-          else
-            reinterpret_cast<float*>(part_at(part, col >> 2, prow1))[col & 3] = o[i];
-        }
-        if (lane == src) {
-          ref = ref1;
-          l = l1;
-        }
+      // Rows that this form cannot give are left to launch_again's kernel: nothing that
+      // could take long stands between two barriers here.
+      const unsigned m = __ballot_sync(0xffffffffu, odd && o_live);
+      if (m != 0 && lane == 0) {
+        a.again.mark(cur.rh, cur.q.s * a.G + cur.pair * kPairRows + t * kTileRows + quarter * 32, m);
+        *a.again.any = 1;
       }
       if (complete) {
         if (o_live && a.lse[r] != nullptr)
@@ -1335,10 +1276,15 @@ cudaError_t launch(PagedArgs a, int ctas, unsigned long long timeout_ns, cudaStr
 
 }  // namespace
 
-size_t tiles_ws_bytes(int64_t d, int B, int ctas) { return layout_of(d, B, std::min(ctas, kMaxCtas)).total; }
+size_t tiles_ws_bytes(int64_t d, int B, int ctas, int64_t rows, int64_t rank_heads) {
+  return layout_of(d, B, std::min(ctas, kMaxCtas)).again + static_cast<size_t>(rank_heads) * Again::words_of(rows) * 4;
+}
 
-cudaError_t launch_tiles(const PagedArgs& a, bool e4m3, int ctas, unsigned long long timeout_ns, cudaStream_t st) {
+cudaError_t launch_tiles(PagedArgs& a, bool e4m3, int ctas, unsigned long long timeout_ns, cudaStream_t st) {
   ctas = std::min(ctas, kMaxCtas);
+  a.again.rows = reinterpret_cast<uint32_t*>(a.ws + layout_of(a.pool.d, a.step.B, ctas).again);
+  a.again.any = &reinterpret_cast<Totals*>(a.ws)->again;
+  a.again.words = Again::words_of(static_cast<int64_t>(a.step.T) * a.G);
   return a.pool.d == 128 ? (e4m3 ? launch<128, true>(a, ctas, timeout_ns, st) : launch<128, false>(a, ctas, timeout_ns, st))
                          : (e4m3 ? launch<64, true>(a, ctas, timeout_ns, st) : launch<64, false>(a, ctas, timeout_ns, st));
 }

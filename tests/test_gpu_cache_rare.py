@@ -1,0 +1,129 @@
+"""The paged attention's tiles on contents that they cannot give by themselves: values that are not finite, and e4m3
+rows whose powers of two are far apart.  Such rows are marked and computed again behind the tiles.
+
+Tolerances: those of the attention (see test_gpu_cache.py), which hold for either way.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache as oc
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover - CPU container
+    pytest.skip("needs a GPU", allow_module_level=True)
+
+import gemm_collective_gb300 as fcc  # noqa: E402
+from tests.gpu_util import to_f64  # noqa: E402
+from tests.test_gpu_cache import Step, attend, check, queries  # noqa: E402
+
+
+def attend_again(s, G, Q, **opts):
+    """attend() in tiles with a workspace of its own; also whether rows were computed again (the plan's fourth word)."""
+    n = fcc.fcc_paged_attention_workspace_size(s.R, s.T, len(s.seqs), s.H * G, s.H, s.d)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    O, z = attend(s, G, Q, opts=fcc.make_opts(workspace=ws, workspace_bytes=n, **opts))
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    return O, z, int(ws[12:16].view(torch.int32))
+
+
+def set_powers(s, which, e):
+    s.exps[which] = np.clip(e, 63, 247).astype(np.uint8)
+    s.vals[which] = oc.values(s.codes[which], s.exps[which])
+
+
+def test_powers_far_apart_in_long_sequences_stay_within_the_wait_limit():
+    """Each block of 20000 positions holds powers too far apart, and every CTA has several items: no warp of the tiles
+    may wait for a row that takes long (2 ms here, in the simplest form a row of 20000 positions takes 16)."""
+    s = Step([(40, 20000), (70, 300), (36, 6000)], H=2, d=64, dtype="e4m3", seed=11)
+    for which in (0, 1):
+        e = s.exps[which].astype(int)
+        e[:, :, :, 3::16] -= 40
+        set_powers(s, which, e)
+    s.upload()
+    Q = queries(s, 4)
+    for ctas in (3, 0):
+        O, lse, again = attend_again(s, 4, Q, max_ctas=ctas, timeout_ns=2_000_000)
+        assert again == 1
+        check(s, 4, Q, O, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_a_value_that_is_not_finite_costs_other_rows_nothing(dtype):
+    """NaN in one value that every row of a long sequence sees: their outputs are NaN, all others' what they are."""
+    s = Step([(50, 20000), (40, 600), (33, 33)], H=2, d=64, dtype=dtype, seed=12)
+    page, row = s.table_np[0, 100 // s.P], 100 % s.P
+    if s.e4m3:
+        s.codes[1][0, page, 1, row, 7] = 0x7F
+    else:
+        s.pools[1][0, page, 1, row, 7] = float("nan")
+    s.upload()
+    G = 4
+    Q = queries(s, G)
+    O, lse, again = attend_again(s, G, Q, max_ctas=2, timeout_ns=2_000_000)
+    assert again == 1
+    hit = O[0][:50, G:].clone()
+    assert bool(hit[..., 7].isnan().all()) and bool(hit[..., :7].isfinite().all()) and bool(hit[..., 8:].isfinite().all())
+    O[0][:50, G:, 7] = 0   # (column 7 of the second head is NaN and checked: the oracle's value is set to match)
+    if s.e4m3:
+        s.vals[1][0, page, 1, row, 7] = 0.0
+    s.vals[1][0, :, 1, :, 7] = 0.0
+    O[0][50:, G:, 7] = 0   # (nor is that column compared in the other sequences, whose values were set to 0 with it)
+    check(s, G, Q, O, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("G", [1, 3, 7])
+@pytest.mark.parametrize("R", [1, 2])
+def test_marked_rows_anywhere_in_a_step(G, R):
+    """Sequences whose rows begin anywhere in a word of marks, some with powers far apart, on every rank."""
+    s = Step([(50, 90), (7, 300), (0, 5), (0, 0), (133, 133), (90, 120), (1, 40), (129, 700)], H=2, d=128, P=16, dtype="e4m3", R=R,
+             seed=G, lead=1, behind=2)
+    for which in (0, 1):
+        e = s.exps[which].astype(int)
+        for b in (1, 4, 7):
+            for page in s.table_np[b]:
+                if page >= 0:
+                    e[:, page, b % 2, 5] -= 40
+        set_powers(s, which, e)
+    s.upload()
+    Q = queries(s, G)
+    O, lse, again = attend_again(s, G, Q)
+    assert again == 1
+    check(s, G, Q, O, lse, 1 / np.sqrt(128))
+    O2, lse2, _ = attend_again(s, G, Q)
+    assert all(torch.equal(a, b) for a, b in zip(O + lse, O2 + lse2))   # a fixed order of summation
+    O3, lse3, _ = attend_again(s, G, Q, max_ctas=5)
+    check(s, G, Q, O3, lse3, 1 / np.sqrt(128))
+
+
+def test_marks_of_the_call_before_are_gone():
+    """The same workspace for a step with marked rows and one without, as a captured step is replayed."""
+    s = Step([(60, 200), (20, 333)], H=1, dtype="bf16", seed=3)
+    Q = queries(s, 4)
+    clean, z0, again = attend_again(s, 4, Q)
+    assert again == 0
+    n = fcc.fcc_paged_attention_workspace_size(1, s.T, 2, 4, 1, 128)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    o = fcc.make_opts(workspace=ws, workspace_bytes=n)
+    page, row = s.table_np[0, 0], 3
+    keep = s.V[0][page, 0, row].clone()
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    O, z = torch.zeros_like(Q[0]), torch.zeros(s.T, 4, device="cuda")
+    cache, batch = s.cache(), s.batch()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=st):
+        fcc.fcc_paged_attention(1, Q, cache, batch, 4, [O], [z], opts=o, stream=torch.cuda.current_stream())
+    for bad in (False, True, False, True):
+        s.V[0][page, 0, row] = float("inf") if bad else keep
+        O.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert fcc.fcc_stream_status() == fcc.FCC_OK
+        assert int(ws[12:16].view(torch.int32)) == int(bad)
+        if bad:
+            # (inf times positive weights; the second sequence does not see it)
+            assert bool((to_f64(O[:60]) == np.inf).all()) and torch.equal(O[60:], clean[0][60:])
+        else:
+            assert torch.equal(O, clean[0]) and torch.equal(z, z0[0])
