@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           byte = min(byte, 254);
           const int top = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 1));
           const bool wide = __any_sync(0xffffffffu, row >= 0 && too_wide(byte, top));
-          factor = f16_power(byte, top);
+          factor = row >= 0 ? f16_power(byte, top) : 0u;   // (where there is no position, byte is an earlier block's)
           if (lane == 0) {
             cc.wide[kind][wl] = wide;
             if (kind == 0) {

@@ -16,14 +16,14 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU container
 
 import gemm_collective_gb300 as fcc  # noqa: E402
 from tests.gpu_util import to_f64  # noqa: E402
-from tests.test_gpu_cache import Step, attend, check, queries  # noqa: E402
+from tests.test_gpu_cache import Step, attend, check, dev, queries  # noqa: E402
 
 
-def attend_again(s, G, Q, **opts):
+def attend_again(s, G, Q, scale=0.0, window=0, **opts):
     """attend() in tiles with a workspace of its own; also whether rows were computed again (the plan's fourth word)."""
     n = fcc.fcc_paged_attention_workspace_size(s.R, s.T, len(s.seqs), s.H * G, s.H, s.d)
     ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
-    O, z = attend(s, G, Q, opts=fcc.make_opts(workspace=ws, workspace_bytes=n, **opts))
+    O, z = attend(s, G, Q, scale, window, opts=fcc.make_opts(workspace=ws, workspace_bytes=n, **opts))
     assert fcc.fcc_stream_status() == fcc.FCC_OK
     return O, z, int(ws[12:16].view(torch.int32))
 
@@ -127,3 +127,23 @@ def test_marks_of_the_call_before_are_gone():
             assert bool((to_f64(O[:60]) == np.inf).all()) and torch.equal(O[60:], clean[0][60:])
         else:
             assert torch.equal(O, clean[0]) and torch.equal(z, z0[0])
+
+
+@pytest.mark.parametrize("L", [257, 289, 352, 400, 384])
+@pytest.mark.parametrize("powers", [(113, 113), (129, 113), (113, 90), (240, 190)])
+def test_positions_that_are_not_there_have_no_power(powers, L):
+    """A last block that ends inside or before a group of 32 positions, behind blocks with larger powers: what is not
+    there must not take a power from the block before (an infinity times zero), which would mark every row."""
+    s = Step([(64, L), (33, L - 31)], H=1, d=64, dtype="e4m3", seed=L)
+    for which in (0, 1):
+        e = np.full_like(s.exps[which], powers[0] if which else 120).astype(int)
+        for b, (_, n) in enumerate(s.seqs):
+            for j in range(n // 128 * 128, n):
+                e[:, s.table_np[b, j // s.P], :, j % s.P] = powers[1] if which else 120
+        set_powers(s, which, e)
+    s.upload()
+    Q = queries(s, 4)
+    for ctas in (1, 0):
+        O, lse, again = attend_again(s, 4, Q, max_ctas=ctas)
+        check(s, 4, Q, O, lse, 1 / 8)
+        assert again == 0, ctas
