@@ -727,7 +727,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         uint32_t factor = 0;
         if constexpr (E4M3) {
           byte = min(byte, 254);
-          const int top = max(1, __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 1));
+          // (a group without positions: a power that leaves its factor of the masked scores above zero)
+          const int most = __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 0), top = most > 0 ? most : 127;
           const bool wide = __any_sync(0xffffffffu, row >= 0 && too_wide(byte, top));
           factor = row >= 0 ? f16_power(byte, top) : 0u;   // (where there is no position, byte is an earlier block's)
           if (lane == 0) {
@@ -918,7 +919,9 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           }
 #pragma unroll
           for (int k = 1; k < kQ; k *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
-          const int e = max(static_cast<int>(top >> 7) - 127, -100) - 14;
+          // (a row of zeros keeps 2^0: the least power, times a group's 2^A, may round to 0, and a masked
+          // score of -inf times that is NaN)
+          const int e = top == 0 ? 0 : max(static_cast<int>(top >> 7) - 127, -100) - 14;
           const float f = power_of_two(-e);
           auto f16 = [&](uint32_t y) { return pack_f16x2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f); };
           v = make_uint4(f16(v.x), f16(v.y), f16(v.z), f16(v.w));

@@ -147,3 +147,23 @@ def test_positions_that_are_not_there_have_no_power(powers, L):
         O, lse, again = attend_again(s, 4, Q, max_ctas=ctas)
         check(s, 4, Q, O, lse, 1 / 8)
         assert again == 0, ctas
+
+
+@pytest.mark.parametrize("L", [40, 168, 300, 384])
+@pytest.mark.parametrize("scale", [0.0, 1e-20, 3.0])
+def test_rows_of_small_queries(L, scale):
+    """Queries of zero and of 2^-8 to 2^-30, and a scale that makes everything small: a masked score is -inf times a
+    factor that must not round to zero, above all where a block ends before its last group of 32 positions."""
+    s = Step([(40, L)], H=1, d=128, dtype="e4m3", seed=L)
+    Q = queries(s, 4)
+    Q[0][0] = 0
+    Q[0][17, 2] = 0
+    Q[0][5:9] *= 2.0 ** -8
+    Q[0][9] *= 2.0 ** -30
+    O, lse, again = attend_again(s, 4, Q, scale=scale)
+    check(s, 4, Q, O, lse, scale or 128 ** -0.5)
+    assert again == 0
+    Q[0][11] *= 2.0 ** -110       # (these may be computed again)
+    Q[0][13, 1] *= 2.0 ** -130
+    O, lse, _ = attend_again(s, 4, Q, scale=scale)
+    check(s, 4, Q, O, lse, scale or 128 ** -0.5)
