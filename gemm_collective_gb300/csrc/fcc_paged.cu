@@ -47,7 +47,10 @@ namespace {
 // tiles with any number up to 128; e4m3 192 by items with 24 and 32 rows, 293 with 40, and
 // 261 by tiles.
 constexpr int kFewRowsBf16 = 16, kFewRowsE4m3 = 32;
-constexpr float kRaise = 8.f;                  // the reference is raised past this (log2 units)
+// The reference is raised past this (log2 units).  f16 is used to its end: a row's largest
+// p lies between 2^8 and 2^16, and what vanishes, p below 2^-25, is below 2^-33 of it.
+template <bool E4M3>
+constexpr float kRaise = E4M3 ? 7.9f : 8.f;
 
 struct Header {                                // of the item whose first part CTA c holds last
   int parts;                                   // CTAs from c on (0: none)
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
   constexpr int kTok = F::kTok, kUnit = F::kUnit, kPer = F::kPer, kWarps = F::kWarps, kHalf = F::kHalf, kStages = F::kStages;
   constexpr int kM = kTok / 16;                // products' rows of 16 positions
   constexpr int kD = D / 16;
-  constexpr float kOff = E4M3 ? 6.f : 0.f;     // p up to 2^(kOff + kRaise): f16 holds 2^14, and 2^-38 of it
+  constexpr float kOff = E4M3 ? 8.f : 0.f;    // p up to 2^(kOff + kRaise)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[kWarps], s_off;
   __shared__ int s_b;
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
             float& t = s[mt][nq][i];
             t = E4M3 ? fmaf(t * scale[nq][i & 1], kx[i >> 1], vx[i >> 1]) : t * scale[nq][i & 1];
             if (!whole && !sees(mt, nq, i)) t = -INFINITY;
-            raise |= t > ref[nq][i & 1] + (kOff + kRaise);
+            raise |= t > ref[nq][i & 1] + (kOff + kRaise<E4M3>);
           }
       }
       if (__any_sync(0xffffffffu, raise)) {
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_ker
 #pragma unroll
             for (int x = 4; x < 32; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
             f[i] = 1.f;
-            if (top > ref[nq][i] + (kOff + kRaise)) {
+            if (top > ref[nq][i] + (kOff + kRaise<E4M3>)) {
               f[i] = ex2_from(ref[nq][i], top - kOff);
               ref[nq][i] = top - kOff;
               l[nq][i] *= f[i];

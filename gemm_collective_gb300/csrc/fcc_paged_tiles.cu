@@ -111,9 +111,10 @@ constexpr uint32_t kAtom = 128 * 128;
 // units).  bf16 has f32's exponents: P may grow far, and the raise (which rescales O_t
 // in tensor memory) can wait for the next block.  A row whose sums overflow all the
 // same (2^127 within one block) is not finite at the end and is computed again.  f16
-// ends at 2^16: there the maximum is taken before the exponentials.
+// ends at 2^16: there the maximum is taken before the exponentials, and a row's largest P
+// is kept between 2^8 and 2^16, as in fcc_paged.cu.
 template <bool E4M3>
-constexpr float kRaise = E4M3 ? 8.f : 32.f;
+constexpr float kRaise = E4M3 ? 7.9f : 32.f;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;                // S_t at 128 t, O_t at 256 + 128 t
 constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
   constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
   constexpr uint32_t kIdescS = (ptx::idesc_bf16_f32(kTileRows, kBlock, false, false) & ~kBf16) | kFormat;
   constexpr uint32_t kIdescO = (ptx::idesc_bf16_f32(kTileRows, D, false, true) & ~kBf16) | kFormat;
-  constexpr float kOff = E4M3 ? 6.f : 0.f;     // p up to 2^14 in f16, see fcc_paged.cu
+  constexpr float kOff = E4M3 ? 8.f : 0.f;    // p up to 2^(kOff + kRaise) in f16
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));

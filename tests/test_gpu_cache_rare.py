@@ -167,3 +167,29 @@ def test_rows_of_small_queries(L, scale):
     Q[0][13, 1] *= 2.0 ** -130
     O, lse, _ = attend_again(s, 4, Q, scale=scale)
     check(s, 4, Q, O, lse, scale or 128 ** -0.5)
+
+
+@pytest.mark.parametrize("case,G", [([(1, 70)], 8), ([(2, 70)], 8), ([(80, 149)], 4)])
+@pytest.mark.parametrize("bits", [10.3, 26.4764])
+def test_small_probabilities_keep_their_digits(case, G, bits):
+    """e4m3, by items of 8 and 16 rows and by tiles: one position, whose values are zero, has 2^bits times the weight
+    of each other.  The output is the others'.  The largest probability is 2^8 at least, so that theirs
+    are 2^-18.5 at least, and f16 rounds them by 2^-25 at most: 2^-6.5 of themselves in the worst case.  These are
+    46.00 steps of 2^-24, off by less than 2^-10 (with a largest of 2^6 they were 11.50 steps, off by 2^-4.5)."""
+    s = Step(case, H=1, d=128, dtype="e4m3", seed=int(bits))
+    for which in (0, 1):
+        set_powers(s, which, np.full_like(s.exps[which], 119).astype(int))
+    page, row = s.table_np[0, 0], 3
+    s.codes[0][:] = 0
+    s.codes[0][0, page, 0, row, 0] = 0x38                     # 1.0: the only key that is not zero
+    s.codes[1][(s.codes[1] & 0x7F) == 0] |= 1
+    s.codes[1][0, page, 0, row] = 0
+    for which in (0, 1):
+        s.vals[which] = oc.values(s.codes[which], s.exps[which])
+    s.upload()
+    Q = [torch.zeros(s.T, G, 128, device="cuda", dtype=torch.bfloat16)]
+    Q[0][..., 0] = 1.0
+    scale = float(np.float32(bits * np.log(2) * 2.0 ** 8))    # (the key is 2^-8)
+    O, lse = attend(s, G, Q, scale=scale)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(s, G, Q, O, lse, scale)
