@@ -27,8 +27,8 @@
 // 128 columns), then those that load keys and values and the one that issues the
 // products.  The loaders look up every position's page for itself (any page size).
 // bf16 rows go by TMA into the swizzled tile, 32 positions to a warp.  e4m3 rows pass
-// through registers and become f16 there, times their powers of two relative to the
-// largest, 2^A of the keys and 2^B of the values, of each 32 positions; those enter at
+// through registers and become f16 there, times their powers of two relative to
+// 2^A of the keys and 2^B of the values, 2^-7 of each 32 positions' largest; those enter at
 // the exponent (see fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
 //
 // What bounds it: 2048 rows of 32 heads over 32768 positions take 718 us in bf16
@@ -403,21 +403,26 @@ constexpr int kWalks = 17;
 // What the softmax warps need to know of a block's columns, for each 32 of them: e4m3
 // the largest powers of two of their keys and values; which positions the pages hold.
 struct alignas(16) Columns {
-  float ka[4], vb[4], vi[4];                   // 2^A, B and 2^-B
+  float ka[4], vb[4], vi[4];                   // 2^A, B and 2^-B, 2^kLift below the largest
   uint32_t there[4];
   uint32_t wide[2][4];                         // keys', values' powers too far apart for f16, see f16_power()
 };
 
-// 2^(byte - top) in f16 (both halves).  An e4m3 code (a multiple of 2^-9) times it is
-// exact in f16 down to 2^-15.  A group with powers further apart is `wide`: the rows
-// that met it are computed again (Again).  (Byte 63 holds what is nearly zero on its
-// own, a row of zeros above all: that may vanish.)
+// 2^(byte - top + kLift) in f16 (both halves): codes end at 448 * 2^7 = 57344, below f16's
+// largest, and a code (a multiple of 2^-9) times a power is exact down to 2^-15, with f16's
+// subnormal numbers: over 22 powers.  A group with powers further apart is `wide`: the rows
+// that met it are computed again (Again).  (P's 33 bits: of an output of values 2^22 below
+// their neighbours', which they outweigh by more than that, a neighbour's lost part is 2^-11.
+// To mark such rows by the size of their sums took 1 to 4 % of every chunk, and marked one
+// in a hundred of rows with a quiet position near their query that lost nothing.)
+constexpr int kLift = 7;
 __device__ __forceinline__ uint32_t f16_power(int byte, int top) {
-  const int k = byte - top;
+  const int k = byte - top + kLift;
   const uint32_t h = k >= -14 ? static_cast<uint32_t>(15 + k) << 10 : k == -15 ? 1u << 9 : 0u;
   return h | (h << 16);
 }
-__device__ __forceinline__ bool too_wide(int byte, int top) { return byte < top - 15 && byte > 63; }
+constexpr int kWide = 15 + kLift;
+constexpr int kZeroByte = 63;                  // append's least, and what a row of zeros has
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -723,22 +728,24 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
       // What the softmax warps are told of the block (called once the block's slot is
       // free: the products of the block that had these constants four blocks ago were
       // issued before the slot was handed back).  e4m3: returns this position's factor.
-      auto constants = [&](int64_t row, int byte) -> uint32_t {
+      // least: the least byte of the warp's rows that are not zero (any power leaves those what they are).
+      auto constants = [&](int64_t row, int byte, int least) -> uint32_t {
         Columns& cc = cols[blk % kCols];
         uint32_t factor = 0;
         if constexpr (E4M3) {
           byte = min(byte, 254);
           // (a group without positions: a power that leaves its factor of the masked scores above zero)
-          const int most = __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 0), top = most > 0 ? most : 127;
-          const bool wide = __any_sync(0xffffffffu, row >= 0 && too_wide(byte, top));
+          const int most = __reduce_max_sync(0xffffffffu, row >= 0 ? byte : 0), top = most > 0 ? max(most, kLift + 1) : 127;
+          const bool wide = least < top - kWide;
           factor = row >= 0 ? f16_power(byte, top) : 0u;   // (where there is no position, byte is an earlier block's)
           if (lane == 0) {
+            const int scale = top - kLift;
             cc.wide[kind][wl] = wide;
             if (kind == 0) {
-              cc.ka[wl] = __int_as_float(top << 23);
+              cc.ka[wl] = __int_as_float(scale << 23);
             } else {
-              cc.vb[wl] = static_cast<float>(top - 127);
-              cc.vi[wl] = __int_as_float((254 - top) << 23);
+              cc.vb[wl] = static_cast<float>(scale - 127);
+              cc.vi[wl] = __int_as_float((254 - scale) << 23);
             }
           }
         }
@@ -775,6 +782,18 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           }
           if (row >= 0) byte = (kind == 0 ? a.pool.Ke[r] : a.pool.Ve[r])[row];
         };
+        // Which of the 32 rows are not zero, by rows i * kAtOnce + sub of the lanes that hold them.
+        auto not_zero = [&]() -> uint32_t {
+          uint32_t rows = 0;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const uint32_t m = __ballot_sync(0xffffffffu, ((x[i].x | x[i].y | x[i].z | x[i].w) & 0x7f7f7f7fu) != 0);
+#pragma unroll
+            for (int n = 0; n < kAtOnce; ++n)
+              rows |= (m >> (kAtoms * 8 * (n >> 1) + 4 * (n & 1)) & (kAtoms == 2 ? 0xf0fu : 0xfu)) != 0 ? 1u << (i * kAtOnce + n) : 0u;
+          }
+          return rows;
+        };
         // (Pages taken as soon as they were asked for, an address for each load and the
         // item's fields from shared memory each time: 1034 instead of 1005 us for the chunk.)
         // A block's pages are asked for two blocks ahead; what has come a block later is
@@ -796,7 +815,12 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
           }
           ask();
           if (!(ok = wait_slot())) break;
-          const uint32_t power = constants(row, byte);
+          int least = __reduce_min_sync(0xffffffffu, row >= 0 ? byte : 255);
+          if (least == kZeroByte) {
+            const uint32_t rows = not_zero();
+            least = __reduce_min_sync(0xffffffffu, row >= 0 && (rows >> lane & 1) != 0 ? byte : 255);
+          }
+          const uint32_t power = constants(row, byte, least);
           uint8_t* dst = sR + (u % kSlots) * kTile;
 #pragma unroll
           for (int i = 0; i < kN; ++i) {
@@ -834,7 +858,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv, ++u) {
             if (!(ok = wait_slot())) break;
-            if (kv == 0) constants(row, 0);
+            if (kv == 0) constants(row, 0, 0);
             uint8_t* dst = sR + (u % kSlots) * kTile;
             uint64_t* bar = &r_full[u % kSlots];
             if (boxes) {

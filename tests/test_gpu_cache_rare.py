@@ -193,3 +193,47 @@ def test_small_probabilities_keep_their_digits(case, G, bits):
     O, lse = attend(s, G, Q, scale=scale)
     assert fcc.fcc_stream_status() == fcc.FCC_OK
     check(s, G, Q, O, lse, scale)
+
+
+@pytest.mark.parametrize("apart", [16, 20, 22])
+def test_powers_up_to_22_apart_are_a_tiles_own(apart):
+    """Values (and keys) that append makes quiet beside their neighbours, one position in eight and each its own way."""
+    s = Step([(60, 700), (33, 95)], H=2, d=128, dtype="e4m3", seed=apart)
+    for which in (0, 1):
+        e = np.full_like(s.exps[which], 140).astype(int)
+        quiet = s.g.random(e.shape) < 1 / 8
+        e[quiet] -= s.g.integers(0, apart + 1, e.shape)[quiet]
+        if which == 0:
+            e -= 22
+        # (a column in which the loudest position holds zero shows the others' P, which f16 may have cut short)
+        s.codes[which][(s.codes[which] & 0x7F) == 0] |= 1
+        set_powers(s, which, e)
+    s.upload()
+    Q = queries(s, 4)
+    for window in (0, 3):
+        O, lse, again = attend_again(s, 4, Q, window=window)
+        check(s, 4, Q, O, lse, 128 ** -0.5, window)
+        assert again == 0
+
+
+def test_a_cache_with_quiet_rows_as_append_writes_it():
+    """Value rows 2^-20 of the others in one place of a hundred (and rows of zeros) are ordinary contents."""
+    H, d, P, L, n, G = 2, 128, 16, 1500, 100, 4
+    s = Step([(n, L)], H=H, d=d, P=P, dtype="e4m3", seed=2)
+    g = torch.Generator(device="cuda").manual_seed(0)
+    k, v = (torch.randn(L, H, d, device="cuda", generator=g) for _ in range(2))
+    v *= torch.where(torch.rand(L, H, 1, device="cuda", generator=g) < 0.01, 2.0 ** -20, 1.0)
+    v[5] = 0
+    k[300] = 0
+    k, v = k.bfloat16(), v.bfloat16()
+    fcc.fcc_cache_append(1, [k], [v], s.cache(), fcc.make_batch(dev([0, L]), dev([L]), s.table, L, 1, s.max_pages))
+    for which, x in ((0, k), (1, v)):
+        codes, power = oc.quantise(to_f64(x))
+        for j in range(L):
+            page, row = s.table_np[0, j // P], j % P
+            s.codes[which][0, page, :, row], s.exps[which][0, page, :, row] = codes[j], power[j]
+        s.vals[which] = oc.values(s.codes[which], s.exps[which])
+    Q = queries(s, G)
+    O, lse, again = attend_again(s, G, Q)
+    check(s, G, Q, O, lse, 1 / np.sqrt(d))
+    assert again == 0
