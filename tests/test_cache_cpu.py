@@ -166,3 +166,20 @@ def test_scales_whose_exponents_overflow_are_refused(fcc):
     # scale * log2(e) is what a score is multiplied by; FLT_MAX / log2(e) is 2.3587e38
     for scale in (2.36e38, 3.4e38):
         assert _calls(fcc, scale=scale, which=("attention",)) == [fcc.FCC_ERR_INVALID]
+
+
+def test_batches_of_other_types_and_sizes_are_refused(fcc):
+    start, length, table = (torch.zeros(n, dtype=torch.int32) for n in (4, 3, 15))
+    good = dict(start=start, len=length, table=table.view(3, 5))
+    assert _batch(fcc, **good).table == table.data_ptr()
+    _batch(fcc, start=torch.zeros(9, dtype=torch.int32), len=table[3:], table=torch.zeros(7, 5, dtype=torch.int32))  # larger ones
+    _batch(fcc, **dict(good, table=table))
+    for k in [dict(start=start.long()), dict(len=length.float()), dict(table=table.view(3, 5).long()),
+              dict(start=start[:3]), dict(len=length[:2]), dict(table=table[:14]), dict(table=table[:10].view(2, 5)),
+              dict(table=table.view(5, 3)), dict(table=torch.zeros(3, 8, dtype=torch.int32)[:, :5]),
+              dict(table=table.view(5, 3).t()), dict(start=torch.zeros(8, dtype=torch.int32)[::2])]:
+        with pytest.raises(fcc.FccError) as e:
+            _batch(fcc, **dict(good, **k))
+        assert e.value.status == fcc.FCC_ERR_INVALID, k
+    one = torch.zeros(4, 8, dtype=torch.int32)
+    fcc.make_batch(start, length, one[1:2, :5], 4, 1, 5)    # a single row of a wider table
