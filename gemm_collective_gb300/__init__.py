@@ -97,7 +97,8 @@ def make_cache(K, V, pages, page_size, H, d, dtype=FCC_BF16, K_exp=None, V_exp=N
     c = fcc_cache(*(None if a is None else ctypes.addressof(a) for a in arrays), pages, page_size,
                   H, d, dtype)
     c.arrays = arrays  # (the structure holds their addresses)
-    c.ranks = min((len(a) for a in arrays if a is not None), default=0)
+    used = arrays if dtype == FCC_E4M3 else arrays[:2]  # (the powers' arrays are ignored otherwise)
+    c.ranks = min((len(a) for a in used if a is not None), default=0)
     return c
 
 

@@ -183,3 +183,10 @@ def test_batches_of_other_types_and_sizes_are_refused(fcc):
         assert e.value.status == fcc.FCC_ERR_INVALID, k
     one = torch.zeros(4, 8, dtype=torch.int32)
     fcc.make_batch(start, length, one[1:2, :5], 4, 1, 5)    # a single row of a wider table
+
+
+def test_a_cache_counts_the_ranks_of_the_arrays_that_it_uses(fcc):
+    two = [16, 32]
+    assert fcc.make_cache(two, two, 9, 16, 2, 128, fcc.FCC_BF16, [16], []).ranks == 2
+    assert fcc.make_cache(two, [16], 9, 16, 2, 128).ranks == 1
+    assert fcc.make_cache(two, two, 9, 16, 2, 128, fcc.FCC_E4M3, two, [16]).ranks == 1
