@@ -44,11 +44,12 @@ __device__ __forceinline__ int64_t places_of(const MoveArgs& a, int t0) {
   // the 16 rows' sequences: the one of t0, plus the starts up to t behind it
   int b = warp_find_seq(a.step, t0);
   for (int from = b + 1; from < a.step.B; from += 32) {
-    const int s = from + lane < a.step.B ? __ldg(a.step.start + from + lane) : 0x7fffffff;
+    const bool there = from + lane < a.step.B;
+    const int s = there ? __ldg(a.step.start + from + lane) : 0;
     unsigned more = 0;
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {
-      const unsigned m = __ballot_sync(0xffffffffu, s <= t0 + i);
+      const unsigned m = __ballot_sync(0xffffffffu, there && s <= t0 + i);   // (t0 + i may be the largest int)
       if ((lane & (kGroup - 1)) == i) b += __popc(m);
       more = m;
     }

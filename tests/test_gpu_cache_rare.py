@@ -237,3 +237,17 @@ def test_a_cache_with_quiet_rows_as_append_writes_it():
     O, lse, again = attend_again(s, G, Q)
     check(s, G, Q, O, lse, 1 / np.sqrt(d))
     assert again == 0
+
+
+def test_the_longest_token_arrays():
+    """T = 2^31 - 1, where the last group of rows ends at the largest int.  Only a sequence's own rows are touched,
+    which begin the arrays here."""
+    s = Step([(5, 9), (2, 40)], H=1, d=64, dtype="bf16", seed=1)
+    T = s.T
+    out = [torch.full((T, 1, 64), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    fcc.fcc_cache_gather(1, s.cache(), s.batch(2 ** 31 - 1), [out[0]], [out[1]])
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    for which in range(2):
+        for b, (n, L) in enumerate(s.seqs):
+            a = int(s.start_np[b])
+            assert np.array_equal(to_f64(out[which][a:a + n]), s.held(which, 0, b, L - n, L))
