@@ -45,7 +45,8 @@ namespace {
 // tiles of 128, although an item reads the cache for every 16 rows: 40 sequences of 6000
 // positions, 8 heads take 155 us by items with 16 rows in bf16 and 300 with 24, and 202 by
 // tiles with any number up to 128; e4m3 192 by items with 24 and 32 rows, 293 with 40, and
-// 261 by tiles.
+// 261 by tiles.  For sequences alike: the average says nothing of a chunk among single rows,
+// which one call takes in 1.02 to 3.5 times the two parts' time (fcc.h says how to split it).
 constexpr int kFewRowsBf16 = 16, kFewRowsE4m3 = 32;
 // The reference is raised past this (log2 units).  f16 is used to its end: a row's largest
 // p lies between 2^8 and 2^16, and what vanishes, p below 2^-25, is below 2^-33 of it.
@@ -259,14 +260,15 @@ __device__ __forceinline__ void store_rows(const PagedArgs& a, const Seq& q, int
 }
 
 // AGAIN: the rows that tiles of 128 left (Again), an item to a CTA from its first position
-// to its last: where they are summed does not depend on which others there are.
+// to its last: where they are summed does not depend on which others there are.  All 65536
+// rows over 32768 positions take 6.4 ms in bf16 and 37 in e4m3, beside 0.7 and 1.0 in tiles.
 template <int D, bool E4M3, int NQ, bool AGAIN>
 __global__ void __launch_bounds__(Few<D, E4M3, NQ>::kWarps * 32, 2) few_rows_kernel(const __grid_constant__ PagedArgs a) {
   using F = Few<D, E4M3, NQ>;
   constexpr int kTok = F::kTok, kUnit = F::kUnit, kPer = F::kPer, kWarps = F::kWarps, kHalf = F::kHalf, kStages = F::kStages;
   constexpr int kM = kTok / 16;                // products' rows of 16 positions
   constexpr int kD = D / 16;
-  constexpr float kOff = E4M3 ? 8.f : 0.f;    // p up to 2^(kOff + kRaise)
+  constexpr float kOff = E4M3 ? 8.f : 0.f;     // p up to 2^(kOff + kRaise)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_scan[kWarps], s_off;
   __shared__ int s_b;

@@ -9,7 +9,7 @@
 // equal runs as there are CTAs, one to an SM: causal, windowed and ragged steps load all
 // SMs alike, and a few rows over a long context are spread over all of them.  (Without
 // the three, the CTAs with a causal prompt's many short items came last: 1.60 against
-// 1.05 ms for 8192 rows of 64 heads, which take 0.86 now.)  What a cut leaves of an item are partial sums, at
+// 1.05 ms for 8192 rows of 64 heads, which take 0.86 to 0.88 now.)  What a cut leaves of an item are partial sums, at
 // most two from a CTA, added in order by join_kernel.  Rows that tiles cannot give (Again)
 // are computed behind them by launch_again's kernel, which waits for nothing: inside a
 // tile, where a warp alone needs 0.8 us a position, long rows would let the other warps'
@@ -32,10 +32,11 @@
 // the exponent (see fcc_paged.cu): t = 2^A (S c) + B, P = 2^(t - ref), l += 2^-B sum P.
 //
 // What bounds it: 2048 rows of 32 heads over 32768 positions take 718 us in bf16
-// (1483 TFLOP/s, 0.75 of the measured burst peak), 1.7 us a block and pair.  A
+// (1483 TFLOP/s, 0.75 of the measured burst peak; 760 to 780 in a loop of calls, 0.70, where
+// power holds the clock down), 1.7 us a block and pair.  A
 // 128 x 128 x 16 product alone takes 64 clocks, 2048 for a block and pair: the tensor
-// pipe is busy 61 % of the time, the schedulers issue in 45 % and the exponentials'
-// unit works in 31 %.  No unit is full: the rest is the way from the last score to the
+// pipe is busy 63 % of the time, the schedulers issue in 45 % and the exponentials'
+// unit works in 32 %.  No unit is full: the rest is the way from the last score to the
 // first P V and back, of which two tiles cover one another's only in part, and shared
 // memory, which the operands of S fill by themselves while they run.  e4m3 (1005 us)
 // waits for its loaders, busy 0.85 of the time with conversions and addresses, and for
@@ -119,9 +120,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;                // S_t at 128 t, O_t at 256 + 128 t
 constexpr uint64_t kDrainNs = 50ull * 1000 * 1000;
 // Warps: 8 softmax, 4 loading (e4m3: 4 for the keys and 4 for the values), 1 issuing and
-// its 3 idle neighbours.  Registers: the launch's are dealt out anew.  Next to nothing
-// may spill: what shared memory leaves of the L1 is too small to hold it (200 bytes a
-// thread made a 2048-row prompt three times as slow).
+// its 3 idle neighbours.  Registers: the launch's are dealt out anew.  Little may spill
+// (62 bytes of 128-column e4m3 do, 4 of the others): what shared memory leaves of the L1 is
+// too small to hold it (200 bytes a thread made a 2048-row prompt three times as slow).
 template <bool E4M3>
 struct Roles {
   static constexpr int kLoadWarps = E4M3 ? 8 : 4;
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
   constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
   constexpr uint32_t kIdescS = (ptx::idesc_bf16_f32(kTileRows, kBlock, false, false) & ~kBf16) | kFormat;
   constexpr uint32_t kIdescO = (ptx::idesc_bf16_f32(kTileRows, D, false, true) & ~kBf16) | kFormat;
-  constexpr float kOff = E4M3 ? 8.f : 0.f;    // p up to 2^(kOff + kRaise) in f16
+  constexpr float kOff = E4M3 ? 8.f : 0.f;     // p up to 2^(kOff + kRaise) in f16
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1038,6 +1039,11 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         late = -INFINITY;
         // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
         const float sub = ref == -INFINITY ? 0.f : ref;
+        // l takes P as it is in f32, the product with V takes it in 16 bits: half a step of bf16 is
+        // 2^-9, of f16 2^-12.  In bf16, where a row's largest P is any number up to 2^32, its
+        // rounding shows: an output is off by 0.0023 of itself where its own rounding is
+        // 0.0017.  With the rounded P in l that was 0.0017 too, but the chunk took 743 instead of
+        // 719 us, and lse was off by 0.004 instead of 5e-6.
         auto exponentials = [&](uint32_t (&x)[32], int k) {
           const float ck = E4M3 ? c * cc.ka[k] : c, rk = E4M3 ? cc.vb[k] - sub : -sub;
           const uint64_t c2 = ptx::f32x2_pack(ck, ck), r2 = ptx::f32x2_pack(rk, rk);
