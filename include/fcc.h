@@ -518,8 +518,9 @@ fcc_status fcc_cache_gather(int R, const fcc_cache *cache, const fcc_batch *batc
  * product with V in 16 bits (bf16; f16 where the cache is e4m3), relative to a running
  * maximum (f16: weights below 2^-33 of a row's largest may vanish, each 2^-33 of the
  * largest value that the row sees at most).  Repeatable (a fixed order of summation).
- * Powers of an e4m3 cache are read as append writes them (bytes 63 to 247).  O[r] must
- * not overlap Q[r].
+ * Powers of an e4m3 cache are read as append writes them (bytes 63 to 247); those of the
+ * values that a row sees are at most 2^120 apart (beyond, the weights of the smaller ones
+ * may be missing from the sum).  O[r] must not overlap Q[r].
  * A sequence with len[b] < n has no visible positions; a row with none has
  * O = 0, lse = -inf.  Where a needed page is not valid, or lies past
  * max_pages, its positions are left out.  Both record FCC_ERR_INVALID.

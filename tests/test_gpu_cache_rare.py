@@ -298,3 +298,22 @@ def test_a_step_in_two_calls(dtype):
         fcc.fcc_paged_attention(1, Q, s.cache(), batch, s.H * G, O, lse)
     assert fcc.fcc_stream_status() == fcc.FCC_OK
     check(s, G, Q, O, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("case,G", [([(1, 200)], 8), ([(2, 200)], 8), ([(80, 279)], 4)])
+def test_zeros_beside_values_2_to_the_120_above(case, G):
+    """The widest range of powers that a row may see: 70 positions of zeros (byte 63) before values of byte 183.  The
+    zeros' weights count in the sum: p 2^-b is 2^8 2^-120 2^64 for them and 2^8 2^-56 for the others."""
+    s = Step(case, H=1, d=64, dtype="e4m3", seed=20)
+    e = np.full_like(s.exps[1], 183).astype(int)
+    for j in range(70):
+        page, row = s.table_np[0, j // s.P], j % s.P
+        e[:, page, :, row] = 63
+        s.codes[1][:, page, :, row] = 0
+    set_powers(s, 0, np.full_like(s.exps[0], 119).astype(int))
+    set_powers(s, 1, e)
+    s.upload()
+    Q = queries(s, G)
+    O, lse = attend(s, G, Q)
+    assert fcc.fcc_stream_status() == fcc.FCC_OK
+    check(s, G, Q, O, lse, 1 / 8)
