@@ -102,28 +102,24 @@ def make_cache(K, V, pages, page_size, H, d, dtype=FCC_BF16, K_exp=None, V_exp=N
     return c
 
 
-def _int32s(x, n, what):
+def _int32s(x, rows, width, what):
     # a tensor of another type, or with fewer or other places than the kernels read, would be misread without a word
     if hasattr(x, "data_ptr"):
-        if str(x.dtype).rpartition(".")[2] != "int32":
+        if str(x.dtype) != "torch.int32":
             raise FccError(FCC_ERR_INVALID, f"{what} holds {x.dtype}, not int32")
-        rows, width = n
-        if x.ndim == 2:  # (one row may lie anywhere)
-            fits = x.shape[0] >= rows and x.shape[1] == width and (x.stride(0) == width or rows == 1)
-        else:
-            fits = x.ndim == 1 and x.shape[0] >= rows * width
-        if not fits or (x.shape[-1] > 1 and x.stride(-1) != 1):
+        dims = x.dim()
+        if not (dims == 1 or dims == 2 and x.size(1) == width) or x.numel() < rows * width or not (
+                x.is_contiguous() or dims == 2 and rows == 1 and x.stride(1) == 1):
             raise FccError(FCC_ERR_INVALID, f"{what} is not {rows} x {width} int32 values one after another")
-    return x
 
 
 def make_batch(start, len, table, T, B, max_pages) -> fcc_batch:
     """The description of a step's sequences (int32 arrays on the device): see fcc_batch in fcc.h.
 
     Tensors are checked for their type and size; addresses are taken as they are."""
-    _int32s(start, (1, B + 1), "start")
-    _int32s(len, (1, B), "len")
-    _int32s(table, (B, max_pages), "table")
+    _int32s(start, 1, B + 1, "start")
+    _int32s(len, 1, B, "len")
+    _int32s(table, B, max_pages, "table")
     return fcc_batch(_addr(start), _addr(len), _addr(table), max_pages, T, B)
 
 
