@@ -1039,8 +1039,8 @@ __global__ void __launch_bounds__(Roles<E4M3>::kThreads, 1) tiles_kernel(const _
         late = -INFINITY;
         // (a row that has seen nothing yet: 2^(-inf - 0) = 0)
         const float sub = ref == -INFINITY ? 0.f : ref;
-        // l takes P as it is in f32, the product with V takes it in 16 bits: half a step of bf16 is
-        // 2^-9, of f16 2^-12.  In bf16, where a row's largest P is any number up to 2^32, its
+        // l takes P as it is in f32, the product with V takes it in 16 bits: off by 2^-8 of it
+        // at most in bf16, by 2^-11 in f16.  In bf16, where a row's largest P is any number up to 2^32, its
         // rounding shows: an output is off by 0.0023 of itself where its own rounding is
         // 0.0017.  With the rounded P in l that was 0.0017 too, but the chunk took 743 instead of
         // 719 us, and lse was off by 0.004 instead of 5e-6.
